@@ -77,6 +77,14 @@ extern "C" {
 #define MOE_ACT_SRELU 2        /* relu(h)^2, non-gated: FC1 has n columns, w1 [E, d, n],
                                   h and dh [M_cap, n], dw1 [E, d, n] [P1, problem and
                                   published-evidence sections: the sReLU family] */
+/* further activations of the dense linear layer (non-gated) */
+#define MOE_ACT_NONE 3         /* identity */
+#define MOE_ACT_SILU 4         /* silu(z) */
+#define MOE_ACT_GELU 5         /* gelu(z), exact */
+
+/* passes of moe_linear_workspace_bytes (bits) */
+#define MOE_LINEAR_FWD 0x1
+#define MOE_LINEAR_BWD 0x2
 
 /* stage bits of moe_grouped_mlp_fwd / moe_grouped_mlp_bwd */
 #define MOE_STAGE_FC1 0x01     /* H = X_perm W1_e, A = GLU(H)               */
@@ -411,6 +419,135 @@ int moe_quant_mxfp8(const uint16_t* src, int batch, int64_t R, int C, int mode,
 int moe_permute_quant_mxfp8(const uint16_t* x, const int32_t* src_of, int T, int k, int E, int d,
                             int64_t M_cap, int mode, uint8_t* q_row, uint8_t* s_row,
                             uint8_t* q_col, uint8_t* s_col, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The dense half of a mixture-of-experts layer: the router projection and the
+ * shared expert that every token passes, their 8-bit activation checkpoints,
+ * and the router's losses.
+ *
+ * A linear layer is z = x W + b, y = f(z) + r with x [T, K], W [K, N], z [T, N]
+ * and y, r [T, NO]: NO = N, or N / 2 for the gated activations, whose columns
+ * are interleaved as in w1 above (32 gate columns, then their 32 up columns).
+ * K and N are multiples of 8 (N of 64 when gated) up to MOE_MAX_WIDTH; T >= 1
+ * is any row count. Pointers to tensors of 16-bit values or codes, and the
+ * workspace, are 16-byte aligned. Outputs must not overlap inputs, except that
+ * a residual may be the output itself.
+ *
+ * An 8-bit checkpoint of a [T, N] activation is its row-wise MXFP8 copy: codes
+ * [T, N] and scales [T, N / 32], as moe_quant_mxfp8 writes it (N % 32 == 0): 33
+ * bytes for 32 values. A rounding of one step moves a value by at most 2^-4 of
+ * itself (2^-10 * 2^e below the block's normal range). It is meant for finite
+ * values.
+ * ------------------------------------------------------------------------- */
+
+/* Device workspace (bytes) of a linear layer's calls: MOE_LINEAR_FWD for
+ * moe_linear_fwd, MOE_LINEAR_BWD for moe_act_bwd, moe_linear_dgrad and
+ * moe_linear_wgrad (which may share it, one after the other on a stream). 0 for
+ * invalid shapes, and where none is needed. A workspace holds nothing between
+ * calls; calls that may overlap in time (two streams, two graphs replayed side
+ * by side) need one each. Host-only. */
+size_t moe_linear_workspace_bytes(int T, int K, int N, int pass);
+
+/*
+ * moe_linear_fwd -- y = f(x W + b) + r in one matrix product with its epilogue.
+ *   The sum over K and the epilogue are fp32; y is rounded once, to bf16, or is
+ *   fp32 when y_f32 != 0 (router logits).
+ *   x [T, K], w [K, N], bias [N] or NULL, residual [T, NO] or NULL (bf16, in);
+ *   y [T, NO] (out). For the backward, optionally z: as bf16 (z [T, N]) and / or
+ *   as an 8-bit checkpoint of its bf16 value (z_q [T, N], z_s [T, N / 32], both
+ *   or neither). act: any MOE_ACT_*; with MOE_ACT_NONE there is no z to keep.
+ *   Few rows (single tokens, decode batches) cut K over the chip and join the
+ *   parts in a second launch, in a fixed order.
+ *   workspace: moe_linear_workspace_bytes(T, K, N, MOE_LINEAR_FWD) bytes.
+ */
+int moe_linear_fwd(const uint16_t* x, const uint16_t* w, const uint16_t* bias, const uint16_t* residual, int T,
+                   int K, int N, int act, int y_f32, void* y, uint16_t* z, uint8_t* z_q, uint8_t* z_s,
+                   void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * moe_act_bwd -- through the activation: dz = dy f'(z) (gated: dg = dy u f'(g),
+ *   du = dy f(g), interleaved like z), dbias = sum over t of dz, a = f(z).
+ *   dy [T, NO] bf16 (NULL when only a is asked for); z [T, N] bf16, or z_q and
+ *   z_s, its 8-bit checkpoint (neither with MOE_ACT_NONE, where dz = dy).
+ *   dz [T, N] bf16, a [T, NO] bf16, dbias [N] fp32 (out; each NULL when not
+ *   wanted): dbias sums the fp32 values of dz before their rounding to bf16; a
+ *   is recomputed for the next layer's weight gradient.
+ *   workspace: moe_linear_workspace_bytes(T, K, N, MOE_LINEAR_BWD) bytes when
+ *   dbias is asked for.
+ */
+int moe_act_bwd(const uint16_t* dy, const uint16_t* z, const uint8_t* z_q, const uint8_t* z_s, int T, int N,
+                int act, uint16_t* dz, uint16_t* a, float* dbias, void* workspace, size_t workspace_bytes,
+                moe_stream_t stream);
+
+/*
+ * moe_linear_dgrad -- dx = dz W^T + r: dz [T, N], w [K, N], residual [T, K] or
+ *   NULL (a gradient that reaches x by another way; may be dx itself), dx [T, K]
+ *   (bf16, fp32 sums, one rounding).
+ */
+int moe_linear_dgrad(const uint16_t* dz, const uint16_t* w, const uint16_t* residual, int T, int K, int N,
+                     uint16_t* dx, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * moe_linear_wgrad -- dw = x^T dz, or dw += x^T dz when accumulate != 0 (fp32
+ *   only): x [T, K] bf16, or x_q and x_s, its 8-bit checkpoint; dz [T, N] bf16;
+ *   dw [K, N] fp32 when dw_f32 != 0, else bf16.
+ */
+int moe_linear_wgrad(const uint16_t* x, const uint8_t* x_q, const uint8_t* x_s, const uint16_t* dz, int T, int K,
+                     int N, int dw_f32, int accumulate, void* dw, void* workspace, size_t workspace_bytes,
+                     moe_stream_t stream);
+
+/*
+ * moe_dequant_mxfp8 -- restores an 8-bit checkpoint: out [R, C] bf16 from codes q
+ *   [R, C] and scales s [R, C / 32] (row-wise, as moe_quant_mxfp8 writes them).
+ *   Exact wherever code * scale is a bf16 number (all but values below bf16's
+ *   smallest normal, which round to nearest). Scale 255 and codes 0x7f, 0xff are
+ *   NaN. Requires C % 32 == 0.
+ */
+int moe_dequant_mxfp8(const uint8_t* q, const uint8_t* s, int64_t R, int C, uint16_t* out, moe_stream_t stream);
+
+/* Device workspace (bytes) of moe_balance_loss. Host-only. */
+size_t moe_balance_workspace_bytes(int T, int E, int S);
+
+/*
+ * moe_balance_loss -- the router's load-balance and z losses with the per-expert
+ *   counts, per sequence. With p = softmax(logits[t]) and n_s the live tokens of
+ *   sequence s:
+ *     f_se = E counts[s, e] / (k n_s),  P_se = mean of p_e over the live tokens,
+ *     B = mean over the sequences with a live token of sum_e f_se P_se,
+ *     Z = mean over all live tokens of (log sum_e exp logits[t, e])^2,
+ *     loss[0] = balance_coef B + z_coef Z, loss[1] = B, loss[2] = Z.
+ *   A token is live unless valid[t] == 0, it lies outside [seq_offsets[0],
+ *   seq_offsets[S]), or it has no finite logit. Non-finite logits have
+ *   probability 0, as in the router. Without a live token every loss is 0.
+ *   logits [T, E] fp32, topk_idx [T, k] int32 (from moe_route_counts; entries
+ *   outside [0, E) are not counted), valid [T] bytes or NULL (all valid),
+ *   seq_offsets [S + 1] int32 ascending, device, or NULL with S = 1 (in);
+ *   loss [3] fp32, counts [S, E] int32, prob [S, E] fp32 (P; 0 for a sequence
+ *   without live tokens), tokens [S + 2] int32 (n_s, then the number of sequences
+ *   with a live token, then all live tokens) (out).
+ *   Sums are joined in a fixed order: the same inputs give the same bits.
+ *   workspace: moe_balance_workspace_bytes(T, E, S) bytes.
+ * Requires 1 <= k <= E <= MOE_MAX_EXPERTS, 1 <= S <= T.
+ */
+int moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* valid,
+                     const int32_t* seq_offsets, int T, int E, int k, int S, float balance_coef, float z_coef,
+                     float* loss, int32_t* counts, float* prob, int32_t* tokens, void* workspace,
+                     size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * moe_balance_loss_bwd -- gradient of loss[0] w.r.t. the logits (the counts have
+ *   none), times the upstream gradient grad [1] fp32 (device; NULL: 1):
+ *     g (balance_coef / (S' n_s) p_e (f_se - sum_j f_sj p_j) + z_coef 2 lse_t p_e / n)
+ *   for live tokens, 0 for the others. counts and tokens are moe_balance_loss's
+ *   outputs; logits, valid, seq_offsets and the sizes those of its call.
+ *   dlogits [T, E] fp32 (out), or added to it when accumulate != 0 (the gradient
+ *   that moe_route_bwd wrote); dlogits_bf16 [T, E] or NULL: the result rounded,
+ *   for the projection's gradient products.
+ */
+int moe_balance_loss_bwd(const float* logits, const int32_t* counts, const int32_t* tokens, const uint8_t* valid,
+                         const int32_t* seq_offsets, int T, int E, int k, int S, float balance_coef,
+                         float z_coef, const float* grad, int accumulate, float* dlogits, uint16_t* dlogits_bf16,
+                         moe_stream_t stream);
 
 #ifdef __cplusplus
 }

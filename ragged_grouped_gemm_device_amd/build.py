@@ -13,7 +13,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
-SOURCES = ["api.cpp", "route.hip", "permute.hip", "gemm.hip", "mx.hip"]
+SOURCES = ["api.cpp", "api_dense.cpp", "route.hip", "permute.hip", "gemm.hip", "mx.hip", "dense.hip", "act.hip",
+           "balance.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,219 @@
+// Elementwise passes of the dense linear layer's backward, and the restoring of
+// 8-bit checkpoints.
+//
+//   moe_act_bwd        dz = dy * f'(z), a = f(z), dbias = column sums of dz, with z
+//                      read as bf16 or straight from its MXFP8 checkpoint
+//   moe_dequant_mxfp8  bf16 values of row-wise MXFP8 codes
+//
+// All are bound by HBM traffic: 16-byte accesses, one pass.
+#include <algorithm>
+
+#include "gemm_common.hpp"
+#include "mx_common.hpp"
+
+namespace moe {
+
+// 2^(s - 127); code 0 is the subnormal 2^-127, code 255 NaN
+__device__ __forceinline__ float e8m0_value(uint32_t s) {
+    return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7fc00000u : s << 23);
+}
+
+// 4 E4M3 codes (low byte first) times a scale
+__device__ __forceinline__ void e4m3x4_value(uint32_t w, float sc, float* v) {
+    const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+    const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    v[0] = a.x * sc, v[1] = a.y * sc, v[2] = b.x * sc, v[3] = b.y * sc;
+}
+
+struct ActArgs {
+    const uint16_t* dy;  // [T, NO], or nullptr: only a
+    const uint16_t* z;   // [T, N], or nullptr: z_q, z_s
+    const uint8_t* z_q;
+    const uint8_t* z_s;
+    int T, N;
+    uint16_t* dz;  // [T, N] or nullptr
+    uint16_t* a;   // [T, NO] or nullptr
+    float* part;   // [row chunks, N] column sums, or nullptr
+    int rows;      // rows per chunk
+};
+
+__device__ __forceinline__ void unpack8(uint4 w, float* v) {
+    unpack_bf16x4(make_uint2(w.x, w.y), v);
+    unpack_bf16x4(make_uint2(w.z, w.w), v + 4);
+}
+__device__ __forceinline__ uint4 pack8(const float* v) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+}
+
+// A workgroup takes 32 groups of 8 output columns (gated: with their 8 gate and
+// 8 up columns) and `rows` rows, 8 rows at a time; a thread keeps its columns'
+// sums of dz (fp32, before the rounding) in registers over the rows, joined over
+// the 8 row lanes in LDS in a fixed order.
+template <int ACT, bool Z8>
+__global__ void __launch_bounds__(256) act_bwd_kernel(ActArgs p) {
+    constexpr bool G = ACT < 2;
+    constexpr int H = G ? 2 : 1;
+    __shared__ float s_sum[8][32][8 * H + 1];
+    const int gl = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const int NO = G ? p.N / 2 : p.N;
+    const int g = blockIdx.x * 32 + gl;
+    const bool live = g < NO / 8;
+    const int c0 = G ? (g >> 2) * 64 + (g & 3) * 8 : g * 8;
+    const int64_t r0 = (int64_t)blockIdx.y * p.rows;
+    const int64_t r1 = min(r0 + p.rows, (int64_t)p.T);
+    float sum[H][8];
+#pragma unroll
+    for (int u = 0; u < H; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[u][i] = 0.f;
+    for (int64_t m = r0 + rl; live && m < r1; m += 8) {
+        float d[8], z[H][8], o[H][8], a[8];
+        if (p.dy) unpack8(*(const uint4*)(p.dy + m * NO + 8 * g), d);
+        else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] = 0.f;
+        }
+        if constexpr (ACT != 3) {
+#pragma unroll
+            for (int u = 0; u < H; ++u) {
+                const int col = c0 + 32 * u;
+                if constexpr (Z8) {
+                    const uint2 q = *(const uint2*)(p.z_q + m * p.N + col);
+                    const float sc = e8m0_value(p.z_s[m * (p.N / 32) + col / 32]);
+                    e4m3x4_value(q.x, sc, z[u]);
+                    e4m3x4_value(q.y, sc, z[u] + 4);
+                } else {
+                    unpack8(*(const uint4*)(p.z + m * p.N + col), z[u]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (G) {
+                float f, df;
+                glu_gate_grad<ACT>(z[0][i], f, df);
+                a[i] = f * z[1][i];
+                o[0][i] = d[i] * z[1][i] * df;
+                o[1][i] = d[i] * f;
+            } else if constexpr (ACT == 3) {
+                a[i] = 0.f;
+                o[0][i] = d[i];
+            } else {
+                float df;
+                dense_act_grad<ACT>(z[0][i], a[i], df);
+                o[0][i] = d[i] * df;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < H; ++u) {
+            if (p.dz) *(uint4*)(p.dz + m * p.N + c0 + 32 * u) = pack8(o[u]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[u][i] += o[u][i];
+        }
+        if (ACT != 3 && p.a) *(uint4*)(p.a + m * NO + 8 * g) = pack8(a);
+    }
+    if (!p.part) return;
+#pragma unroll
+    for (int u = 0; u < H; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s_sum[rl][gl][8 * u + i] = sum[u][i];
+    __syncthreads();
+    for (int q = threadIdx.x; q < 32 * 8 * H; q += 256) {
+        const int gq = q / (8 * H), iq = q % (8 * H);
+        const int gg = blockIdx.x * 32 + gq;
+        if (gg >= NO / 8) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int l = 0; l < 8; ++l) v += s_sum[l][gq][iq];
+        const int col = (G ? (gg >> 2) * 64 + (gg & 3) * 8 : gg * 8) + (iq >> 3) * 32 + (iq & 7);
+        p.part[(int64_t)blockIdx.y * p.N + col] = v;
+    }
+}
+
+// dbias[c] = sum of the chunks' column sums, in a fixed order: 64 columns and 4
+// chunk lanes per workgroup.
+__global__ void __launch_bounds__(256) colsum_kernel(const float* __restrict__ part, int chunks, int N,
+                                                     float* __restrict__ out) {
+    __shared__ float s_v[4][64];
+    const int cl = threadIdx.x & 63, l = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + cl;
+    float v = 0.f;
+    if (c < N)
+        for (int k = l; k < chunks; k += 4) v += part[(int64_t)k * N + c];
+    s_v[l][cl] = v;
+    __syncthreads();
+    if (l == 0 && c < N) out[c] = (s_v[0][cl] + s_v[1][cl]) + (s_v[2][cl] + s_v[3][cl]);
+}
+
+// 16 codes a thread: 16 bytes in, 32 bytes out.
+__global__ void __launch_bounds__(256) dequant_mxfp8_kernel(const uint8_t* __restrict__ q,
+                                                            const uint8_t* __restrict__ s, int64_t n16,
+                                                            uint16_t* __restrict__ out) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n16; i += (int64_t)gridDim.x * 256) {
+        const uint4 w = ((const uint4*)q)[i];
+        const float sc = e8m0_value(s[i >> 1]);
+        float v[16];
+        e4m3x4_value(w.x, sc, v);
+        e4m3x4_value(w.y, sc, v + 4);
+        e4m3x4_value(w.z, sc, v + 8);
+        e4m3x4_value(w.w, sc, v + 12);
+        uint4* o = (uint4*)out + 2 * i;
+        o[0] = pack8(v);
+        o[1] = pack8(v + 8);
+    }
+}
+
+// Row chunks of moe_act_bwd: about 2048 workgroups, at least 8 rows each.
+static void act_chunks(int T, int N, bool gated, int& rows, int& chunks) {
+    const int64_t tiles = ((gated ? N / 2 : N) / 8 + 31) / 32;
+    const int64_t r = ((int64_t)T * tiles + 2047) / 2048;
+    rows = (int)std::max<int64_t>(8, (r + 7) / 8 * 8);
+    chunks = (T + rows - 1) / rows;
+}
+
+size_t act_part_bytes(int T, int N) {
+    size_t most = 0;
+    for (int gated = 0; gated < 2; ++gated) {
+        int rows, chunks;
+        act_chunks(T, N, gated, rows, chunks);
+        most = std::max(most, chunks > 1 ? (size_t)chunks * N * sizeof(float) : 0);
+    }
+    return most;
+}
+
+int launch_act_bwd(const uint16_t* dy, const uint16_t* z, const uint8_t* z_q, const uint8_t* z_s, int T, int N,
+                   int act, uint16_t* dz, uint16_t* a, float* dbias, void* ws, hipStream_t s) {
+    const bool gated = act < 2;
+    int rows, chunks;
+    act_chunks(T, N, gated, rows, chunks);
+    ActArgs p{};
+    p.dy = dy, p.z = z, p.z_q = z_q, p.z_s = z_s, p.T = T, p.N = N, p.dz = dz, p.a = a, p.rows = rows;
+    p.part = !dbias ? nullptr : chunks > 1 ? (float*)ws : dbias;
+    const dim3 grid((unsigned)(((gated ? N / 2 : N) / 8 + 31) / 32), (unsigned)chunks);
+    auto go = [&](auto A) {
+        constexpr int ACT = decltype(A)::value;
+        if (ACT != 3 && !z) act_bwd_kernel<ACT, ACT != 3><<<grid, 256, 0, s>>>(p);
+        else act_bwd_kernel<ACT, false><<<grid, 256, 0, s>>>(p);
+    };
+    switch (act) {
+        case 0: go(std::integral_constant<int, 0>{}); break;
+        case 1: go(std::integral_constant<int, 1>{}); break;
+        case 2: go(std::integral_constant<int, 2>{}); break;
+        case 3: go(std::integral_constant<int, 3>{}); break;
+        case 4: go(std::integral_constant<int, 4>{}); break;
+        default: go(std::integral_constant<int, 5>{}); break;
+    }
+    if (dbias && chunks > 1)
+        colsum_kernel<<<(unsigned)((N + 63) / 64), 256, 0, s>>>((const float*)ws, chunks, N, dbias);
+    return hipGetLastError() == hipSuccess ? 0 : -4;
+}
+
+int launch_dequant_mxfp8(const uint8_t* q, const uint8_t* sc, int64_t R, int C, uint16_t* out, hipStream_t s) {
+    const int64_t n16 = R * (C / 16);
+    const int64_t blocks = std::min<int64_t>((n16 + 255) / 256, (int64_t)1 << 20);
+    dequant_mxfp8_kernel<<<(unsigned)blocks, 256, 0, s>>>(q, sc, n16, out);
+    return hipGetLastError() == hipSuccess ? 0 : -4;
+}
+
+}  // namespace moe

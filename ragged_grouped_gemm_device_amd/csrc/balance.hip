@@ -1,0 +1,401 @@
+// Router losses: the load-balance loss and the z loss of softmax routing, per
+// sequence, with their gradient.
+//
+//   p = softmax(logits[t]); over the n_s live tokens of sequence s:
+//   f_se = E c_se / (k n_s), c_se pairs routed to expert e; P_se = mean of p_e
+//   B = mean over sequences with a live token of sum_e f_se P_se
+//   Z = mean over all live tokens of (log sum_e exp(logits[t, e]))^2
+//   loss = cb B + cz Z, f held constant in the gradient (counts have none):
+//   dloss/dlogits[t, e] = cb / (S' n_s) p_e (f_se - sum_j f_sj p_j) + cz 2 lse / n p_e
+//
+// The forward cuts the tokens into chunks; a chunk walks the sequences it holds
+// and leaves one row of partial sums (probabilities, counts, live tokens, lse^2)
+// per (chunk, sequence) pair. Chunk c and sequence s use row c + s: walking the
+// tokens, either c or s grows at each step, so rows are distinct and fewer than
+// chunks + S. Sums are joined in a fixed order (no floating-point atomics): the
+// same inputs give the same bits.
+#include <algorithm>
+
+#include "gemm_common.hpp"
+
+namespace moe {
+
+struct BalanceArgs {
+    const float* logits;
+    const int32_t* topk_idx;
+    const uint8_t* valid;
+    const int32_t* seq;  // [S + 1] or nullptr: one sequence of all T tokens
+    int T, E, k, S;
+    int CT;  // tokens per chunk
+    float* rows;  // [nchunks + S][2 E + 2]: probabilities, counts, live tokens, lse^2
+    float* bal;   // [S][etiles] partial sums of f P
+    float* zs;    // [S] lse^2
+    float cb, cz;
+    float* loss;
+    int32_t* counts;
+    float* prob;
+    int32_t* tokens;
+    int etiles;
+    // backward
+    const float* grad;
+    int accumulate;
+    float* dlogits;
+    uint16_t* dlogits16;
+};
+
+// first and past-the-end token of sequence s, kept inside [0, T]
+__device__ __forceinline__ int seq_at(const BalanceArgs& p, int s) {
+    if (!p.seq) return s == 0 ? 0 : p.T;
+    const int v = p.seq[s];
+    return v < 0 ? 0 : v > p.T ? p.T : v;
+}
+
+// Calls f(s, a, b) for every run [a, b) of tokens of one sequence inside
+// [t0, t1); s = -1 for tokens before the first or behind the last sequence.
+template <class F>
+__device__ __forceinline__ void for_sequences(const BalanceArgs& p, int t0, int t1, F&& f) {
+    int lo = -1, hi = p.S;  // largest s with seq_at(s) <= t0
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (seq_at(p, mid) <= t0) lo = mid;
+        else hi = mid;
+    }
+    int t = t0;
+    for (int s = lo; t < t1; ++s) {
+        const int e = s >= p.S ? t1 : min(t1, seq_at(p, s + 1));
+        if (e > t) {
+            f(s >= p.S ? -1 : s, t, e);
+            t = e;
+        }
+    }
+}
+
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+    return v;
+}
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+
+// One token's logits in a group of G lanes (lane gl: experts gl + G i). Non-finite
+// logits count as -inf (probability 0), as in the router. Returns whether the
+// token has a finite logit; x becomes exp(x - max).
+template <int G, int PER>
+__device__ __forceinline__ bool token_softmax(const BalanceArgs& p, int t, int gl, bool on, float (&x)[PER],
+                                              float& mx, float& inv, float& lse) {
+    const float* row = p.logits + (int64_t)t * p.E;
+    mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = gl + G * i;
+        float v = on && e < p.E ? row[e] : -INFINITY;
+        if (!isfinite(v)) v = -INFINITY;
+        x[i] = v;
+        mx = fmaxf(mx, v);
+    }
+    mx = group_max<G>(mx);
+    const bool some = mx > -INFINITY;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        x[i] = x[i] > -INFINITY ? expf(x[i] - mx) : 0.f;
+        s += x[i];
+    }
+    s = group_sum<G>(s);
+    inv = some ? 1.f / s : 0.f;
+    lse = some ? mx + logf(s) : 0.f;
+    return some;
+}
+
+template <int G, int PER>
+__global__ void __launch_bounds__(256) balance_chunk_kernel(BalanceArgs p) {
+    __shared__ float s_p[4][G * PER];
+    __shared__ int s_cnt[G * PER];
+    __shared__ float s_z[4];
+    __shared__ int s_n[4];
+    constexpr int NG = 256 / G;  // tokens at a time
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int gl = lane % G, grp = tid / G;
+    for (int e = tid; e < G * PER; e += 256) s_cnt[e] = 0;
+    __syncthreads();
+    const int c = blockIdx.x;
+    const int t0 = c * p.CT, t1 = min(p.T, t0 + p.CT);
+    for_sequences(p, t0, t1, [&](int s, int a, int b) {
+        if (s < 0) return;
+        float acc[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+        float z = 0.f;
+        int n = 0;
+        for (int tb = a; tb < b; tb += NG) {
+            const int t = tb + grp;
+            const bool on = t < b && (!p.valid || p.valid[t] != 0);
+            float x[PER], mx, inv, lse;
+            const bool some = token_softmax<G, PER>(p, on ? t : a, gl, on, x, mx, inv, lse);
+            if (some) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) acc[i] += x[i] * inv;
+                if (gl == 0) {
+                    z += lse * lse;
+                    ++n;
+                }
+                for (int j = gl; j < p.k; j += G) {
+                    const int e = p.topk_idx[(int64_t)t * p.k + j];
+                    if (e >= 0 && e < p.E) atomicAdd(&s_cnt[e], 1);
+                }
+            }
+        }
+        // over the wavefront's groups, then its 4 wavefronts
+#pragma unroll
+        for (int o = 32; o >= G; o >>= 1) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) acc[i] += __shfl_xor(acc[i], o, 64);
+            z += __shfl_xor(z, o, 64);
+            n += __shfl_xor(n, o, 64);
+        }
+        if (lane < G) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) s_p[wave][gl + G * i] = acc[i];
+        }
+        if (lane == 0) {
+            s_z[wave] = z;
+            s_n[wave] = n;
+        }
+        __syncthreads();
+        float* row = p.rows + (int64_t)(c + s) * (2 * p.E + 2);
+        for (int e = tid; e < p.E; e += 256) {
+            row[e] = (s_p[0][e] + s_p[1][e]) + (s_p[2][e] + s_p[3][e]);
+            ((int32_t*)row)[p.E + e] = s_cnt[e];
+            s_cnt[e] = 0;
+        }
+        if (tid == 0) {
+            ((int32_t*)row)[2 * p.E] = s_n[0] + s_n[1] + s_n[2] + s_n[3];
+            row[2 * p.E + 1] = (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]);
+        }
+        __syncthreads();
+    });
+}
+
+// Workgroup s etiles + x: sequence s, experts [32 x, 32 x + 32): joins the chunks' rows.
+__global__ void __launch_bounds__(256) balance_join_kernel(BalanceArgs p) {
+    __shared__ float s_p[8][33], s_z[256];
+    __shared__ int s_c[8][33], s_n[256];
+    const int tid = threadIdx.x, el = tid & 31, l = tid >> 5;
+    const int s = blockIdx.x / p.etiles, et = blockIdx.x - s * p.etiles, e = et * 32 + el;
+    const int a = seq_at(p, s), b = seq_at(p, s + 1);
+    const int c0 = a / p.CT, c1 = b > a ? (b - 1) / p.CT + 1 : c0;
+    const int64_t w = 2 * p.E + 2;
+    float pe = 0.f, z = 0.f;
+    int ce = 0, n = 0;
+    for (int c = c0 + l; c < c1 && e < p.E; c += 8) {
+        const float* row = p.rows + (c + s) * w;
+        pe += row[e];
+        ce += ((const int32_t*)row)[p.E + e];
+    }
+    for (int c = c0 + tid; c < c1; c += 256) {
+        const float* row = p.rows + (c + s) * w;
+        n += ((const int32_t*)row)[2 * p.E];
+        z += row[2 * p.E + 1];
+    }
+    s_p[l][el] = pe;
+    s_c[l][el] = ce;
+    s_n[tid] = n;
+    s_z[tid] = z;
+    __syncthreads();
+    for (int o = 128; o > 0; o >>= 1) {
+        if (tid < o) {
+            s_n[tid] += s_n[tid + o];
+            s_z[tid] += s_z[tid + o];
+        }
+        __syncthreads();
+    }
+    n = s_n[0];
+    if (tid < 64) {
+        float v = 0.f;
+        if (tid < 32 && e < p.E) {
+            float sum = 0.f;
+            int cnt = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                sum += s_p[q][el];
+                cnt += s_c[q][el];
+            }
+            const float mean = n > 0 ? sum / (float)n : 0.f;
+            p.counts[(int64_t)s * p.E + e] = cnt;
+            p.prob[(int64_t)s * p.E + e] = mean;
+            v = n > 0 ? (float)cnt * ((float)p.E / ((float)p.k * (float)n)) * mean : 0.f;
+        }
+        v = wave_sum(v);
+        if (tid == 0) {
+            p.bal[(int64_t)s * p.etiles + et] = v;
+            if (et == 0) {
+                p.tokens[s] = n;
+                p.zs[s] = s_z[0];
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256) balance_loss_kernel(BalanceArgs p) {
+    __shared__ double s_b[256], s_z[256];
+    __shared__ int s_n[256], s_live[256];
+    const int tid = threadIdx.x;
+    double b = 0.0, z = 0.0;
+    int n = 0, live = 0;
+    for (int64_t i = tid; i < (int64_t)p.S * p.etiles; i += 256) b += p.bal[i];
+    for (int s = tid; s < p.S; s += 256) {
+        z += p.zs[s];
+        const int m = p.tokens[s];
+        n += m;
+        live += m > 0;
+    }
+    s_b[tid] = b, s_z[tid] = z, s_n[tid] = n, s_live[tid] = live;
+    __syncthreads();
+    for (int o = 128; o > 0; o >>= 1) {
+        if (tid < o) {
+            s_b[tid] += s_b[tid + o];
+            s_z[tid] += s_z[tid + o];
+            s_n[tid] += s_n[tid + o];
+            s_live[tid] += s_live[tid + o];
+        }
+        __syncthreads();
+    }
+    if (tid == 0) {
+        const double bal = s_live[0] ? s_b[0] / s_live[0] : 0.0, zl = s_n[0] ? s_z[0] / s_n[0] : 0.0;
+        p.loss[0] = (float)(p.cb * bal + p.cz * zl);
+        p.loss[1] = (float)bal;
+        p.loss[2] = (float)zl;
+        p.tokens[p.S] = s_live[0];
+        p.tokens[p.S + 1] = s_n[0];
+    }
+}
+
+// The gradient, one group of G lanes per token. f enters less its value at the
+// largest logit: the gradient does not change (sum_e p_e = 1), and where one
+// expert holds nearly all the probability, f_e - sum_j f_j p_j no longer cancels.
+template <int G, int PER>
+__global__ void __launch_bounds__(256) balance_bwd_kernel(BalanceArgs p) {
+    constexpr int NG = 256 / G;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int gl = lane % G, grp = tid / G;
+    const int t0 = blockIdx.x * p.CT, t1 = min(p.T, t0 + p.CT);
+    const float up = p.grad ? p.grad[0] : 1.f;
+    const int live = p.tokens[p.S], ntot = p.tokens[p.S + 1];
+    const float zc = ntot > 0 ? up * p.cz * 2.f / (float)ntot : 0.f;
+    for_sequences(p, t0, t1, [&](int s, int a, int b) {
+        const int n = s >= 0 ? p.tokens[s] : 0;
+        const float fs = n > 0 ? (float)p.E / ((float)p.k * (float)n) : 0.f;
+        const float bc = n > 0 ? up * p.cb / ((float)live * (float)n) : 0.f;
+        float f[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = gl + G * i;
+            f[i] = s >= 0 && e < p.E ? (float)p.counts[(int64_t)s * p.E + e] * fs : 0.f;
+        }
+        for (int tb = a; tb < b; tb += NG) {
+            const int t = tb + grp;
+            const bool on = s >= 0 && t < b && (!p.valid || p.valid[t] != 0);
+            float x[PER], mx, inv, lse;
+            token_softmax<G, PER>(p, on ? t : a, gl, on, x, mx, inv, lse);
+            float ref = -INFINITY;  // x = exp(logit - max) is 1 at the largest logit
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (x[i] == 1.f) ref = fmaxf(ref, f[i]);
+            ref = group_max<G>(ref);
+            float dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                x[i] *= inv;
+                if (x[i] > 0.f) dot += x[i] * (f[i] - ref);
+            }
+            dot = group_sum<G>(dot);
+            if (t < b) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int e = gl + G * i;
+                    if (e < p.E) {
+                        const int64_t at = (int64_t)t * p.E + e;
+                        float d = x[i] > 0.f ? x[i] * (bc * ((f[i] - ref) - dot) + zc * lse) : 0.f;
+                        if (p.accumulate) d += p.dlogits[at];
+                        p.dlogits[at] = d;
+                        if (p.dlogits16) p.dlogits16[at] = (uint16_t)f32_to_bf16(d);
+                    }
+                }
+            }
+        }
+    });
+}
+
+static int balance_group(int E) { return E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64; }
+
+// Tokens per chunk: about 1024 workgroups, at least one token per lane group.
+static int balance_chunk(int T, int E) {
+    const int ng = 256 / balance_group(E);
+    const int ct = (T + 1023) / 1024;
+    return (ct + ng - 1) / ng * ng;
+}
+
+static int balance_etiles(int E) { return (E + 31) / 32; }
+
+size_t balance_workspace_bytes(int T, int E, int S) {
+    const int ct = balance_chunk(T, E);
+    const int64_t rows = ((int64_t)T + ct - 1) / ct + S;
+    return (size_t)(rows * (2 * E + 2) + (int64_t)S * balance_etiles(E) + S) * sizeof(float);
+}
+
+template <class F>
+static void by_experts(int E, F&& f) {
+    using std::integral_constant;
+    if (E <= 8) f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+    else if (E <= 16) f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+    else if (E <= 32) f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+    else if (E <= 64) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else if (E <= 128) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    else if (E <= 256) f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+    else if (E <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+    else f(integral_constant<int, 64>{}, integral_constant<int, MOE_MAX_E / 64>{});
+}
+
+int launch_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* valid, const int32_t* seq,
+                        int T, int E, int k, int S, float cb, float cz, float* loss, int32_t* counts,
+                        float* prob, int32_t* tokens, void* ws, hipStream_t s) {
+    BalanceArgs p{};
+    p.logits = logits, p.topk_idx = topk_idx, p.valid = valid, p.seq = seq, p.T = T, p.E = E, p.k = k, p.S = S;
+    p.CT = balance_chunk(T, E);
+    const int nchunks = (T + p.CT - 1) / p.CT;
+    p.etiles = balance_etiles(E);
+    p.rows = (float*)ws;
+    p.bal = p.rows + (int64_t)(nchunks + S) * (2 * E + 2);
+    p.zs = p.bal + (int64_t)S * p.etiles;
+    p.cb = cb, p.cz = cz, p.loss = loss, p.counts = counts, p.prob = prob, p.tokens = tokens;
+    by_experts(E, [&](auto G, auto PER) {
+        balance_chunk_kernel<decltype(G)::value, decltype(PER)::value><<<nchunks, 256, 0, s>>>(p);
+    });
+    balance_join_kernel<<<(unsigned)((int64_t)p.etiles * S), 256, 0, s>>>(p);
+    balance_loss_kernel<<<1, 256, 0, s>>>(p);
+    return hipGetLastError() == hipSuccess ? 0 : -4;
+}
+
+int launch_balance_loss_bwd(const float* logits, const int32_t* counts, const int32_t* tokens,
+                            const uint8_t* valid, const int32_t* seq, int T, int E, int k, int S, float cb,
+                            float cz, const float* grad, int accumulate, float* dlogits, uint16_t* dlogits16,
+                            hipStream_t s) {
+    BalanceArgs p{};
+    p.logits = logits, p.valid = valid, p.seq = seq, p.T = T, p.E = E, p.k = k, p.S = S;
+    p.CT = balance_chunk(T, E);
+    p.counts = const_cast<int32_t*>(counts), p.tokens = const_cast<int32_t*>(tokens);
+    p.cb = cb, p.cz = cz, p.grad = grad, p.accumulate = accumulate, p.dlogits = dlogits, p.dlogits16 = dlogits16;
+    const int nchunks = (T + p.CT - 1) / p.CT;
+    by_experts(E, [&](auto G, auto PER) {
+        balance_bwd_kernel<decltype(G)::value, decltype(PER)::value><<<nchunks, 256, 0, s>>>(p);
+    });
+    return hipGetLastError() == hipSuccess ? 0 : -4;
+}
+
+}  // namespace moe

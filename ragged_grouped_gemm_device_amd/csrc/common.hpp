@@ -76,6 +76,31 @@ __device__ __forceinline__ void plain_act_grad(float x, float& f, float& df) {
     df = 2.f * r;
 }
 
+// Non-gated activations of the dense linear layer: ACT 2 squared ReLU, 3 identity,
+// 4 SiLU, 5 exact GELU; and with the derivative.
+template <int ACT>
+__device__ __forceinline__ float plain_act(float x) {
+    if constexpr (ACT == 2) {
+        const float r = fmaxf(x, 0.f);
+        return r * r;
+    } else if constexpr (ACT == 3) {
+        return x;
+    } else {
+        return glu_gate<ACT - 4>(x);
+    }
+}
+template <int ACT>
+__device__ __forceinline__ void dense_act_grad(float x, float& f, float& df) {
+    if constexpr (ACT == 2) {
+        plain_act_grad<2>(x, f, df);
+    } else if constexpr (ACT == 3) {
+        f = x;
+        df = 1.f;
+    } else {
+        glu_gate_grad<ACT - 4>(x, f, df);
+    }
+}
+
 // Unpack 4 bf16 held in a uint2 into floats.
 __device__ __forceinline__ void unpack_bf16x4(uint2 v, float* f) {
     f[0] = __uint_as_float(v.x << 16);

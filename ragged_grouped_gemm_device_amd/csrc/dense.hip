@@ -1,0 +1,545 @@
+// Dense linear layer on gfx950 bf16 MFMA (v_mfma_f32_32x32x16_bf16): the router
+// projection and the shared expert that run beside the routed experts.
+//
+//   forward  y  = f(x W + b) + r     A = x [T, K] K-major,  B = W [K, N] N-major
+//   dgrad    dx = dz W^T + r         A = dz [T, N] K-major, B = W read along its rows, K-major
+//   wgrad    dw = x^T dz (+ dw)      A = x, B = dz, both with the reduction (tokens) outermost
+//
+// One kernel template: a workgroup owns a BM x BN tile, its wavefronts 32 TM x
+// 64 pieces of it (fp32 accumulators in the MFMA layout); K moves in slabs of 64
+// through ST LDS stages filled by direct global -> LDS copies. Buffer bounds turn
+// everything past the matrices' rows into zeros and a lane whose columns lie past
+// the end uses an offset past every buffer, so any T >= 1 and any K, N that are
+// multiples of 8 take the same path.
+//
+// The epilogue adds the bias to the fp32 accumulators (z), optionally stores z as
+// bf16 or as MXFP8 codes of its bf16 value, applies the activation to the fp32 z,
+// adds the residual and rounds once.
+#include <algorithm>
+
+#include "gemm_common.hpp"
+#include "mx_common.hpp"
+
+namespace moe {
+
+constexpr int DBK = 64;  // K elements per slab (128 bytes)
+
+struct DenseArgs {
+    const uint16_t* A;
+    int64_t lda;
+    const uint16_t* B;
+    int64_t ldb;
+    int M, N, K;  // rows and columns of the product, reduction length
+    int ntm, ntn;
+    int splits, split_slabs;  // K slabs per split
+    const uint16_t* bias;     // [N] or nullptr
+    const uint16_t* res;      // [M, NO] or nullptr (NO: columns of the output)
+    void* out;                // [M, NO] bf16, or fp32 when out_f32
+    int out_f32, accumulate;
+    uint16_t* z;   // [M, N] or nullptr
+    uint8_t* z_q;  // [M, N] codes, [M, N / 32] scales, or nullptr
+    uint8_t* z_s;
+    float* part;  // [splits, M, N] raw sums instead of an epilogue, or nullptr
+};
+
+template <int ACT>
+constexpr bool kGated = ACT == 0 || ACT == 1;
+
+// 16-byte chunk swizzle of row k in an MN-major slab of W columns: a transpose
+// read touches 4 neighbouring k rows, 64 bytes each; the XOR spreads them over
+// the four 64-byte quarters of LDS's 256-byte bank window.
+template <int W>
+__device__ __forceinline__ int mn_swz(int k) {
+    if constexpr (W == 256) return (k & 7) << 2;
+    else return (k & 3) << 2;
+}
+
+// Row-wise MXFP8 block of a 32 x 32 block held the MFMA way, as mx_rowq32, for
+// rows that may lie past the matrix: every lane takes part in the exchanges and
+// only the lanes of a real row store.
+__device__ __forceinline__ void mx_rowq32_if(const uint32_t pk[8], int lane, bool ok, uint8_t* q, uint8_t* sc) {
+    uint32_t am = 0;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) am = max_u16x2(am, pk[r] & 0x7fff7fffu);
+    uint32_t amax = max(am & 0xffffu, am >> 16);
+    amax = max(amax, (uint32_t)__shfl_xor((int)amax, 32, 64));
+    const int e = mx_block_exp(amax);
+    const float inv = mx_inv_scale(e);
+    uint32_t w[4];
+#pragma unroll
+    for (int Q = 0; Q < 4; ++Q)
+        w[Q] = e4m3x4(bf16_lo(pk[2 * Q]) * inv, bf16_hi(pk[2 * Q]) * inv, bf16_lo(pk[2 * Q + 1]) * inv,
+                      bf16_hi(pk[2 * Q + 1]) * inv);
+    const int h = (lane >> 5) & 1;
+    const uint32_t g0 = h ? w[0] : w[2], g1 = h ? w[1] : w[3];
+    const auto s0 = __builtin_amdgcn_permlane32_swap(g0, g0, false, false);
+    const auto s1 = __builtin_amdgcn_permlane32_swap(g1, g1, false, false);
+    const uint32_t r0 = h ? s0[0] : s0[1], r1 = h ? s1[0] : s1[1];
+    if (ok) {
+        *(uint4*)(q + 16 * h) = h ? make_uint4(r0, w[2], r1, w[3]) : make_uint4(w[0], r0, w[1], r1);
+        if (h == 0) *sc = (uint8_t)(e + 127);
+    }
+}
+
+// 8 output values v of row m, columns [col, col + 8): residual, accumulation, one rounding.
+__device__ __forceinline__ void dense_store8(const DenseArgs& p, int64_t at, float* v) {
+    if (p.res) {
+        const uint4 r = *(const uint4*)(p.res + at);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] += bf16_lo(w[i]);
+            v[2 * i + 1] += bf16_hi(w[i]);
+        }
+    }
+    if (p.out_f32) {
+        float4* o = (float4*)((float*)p.out + at);
+        if (p.accumulate) {
+            const float4 a = o[0], b = o[1];
+            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+            v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+        }
+        o[0] = make_float4(v[0], v[1], v[2], v[3]);
+        o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *(uint4*)((uint16_t*)p.out + at) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    }
+}
+
+// Wait until at most N vector-memory operations are in flight and every LDS
+// operation has completed, then the workgroup barrier.
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+template <int DBM, int DBN, int WMW, int WNW, int ST, bool A_KMAJ, bool B_KMAJ, int ACT>
+__global__ void __launch_bounds__(WMW * WNW * 64, 2) dense_gemm_kernel(DenseArgs p) {
+    constexpr int NT = WMW * WNW * 64;
+    constexpr int TM = DBM / (32 * WMW), TN = DBN / (32 * WNW);
+    static_assert(TN == 2, "a wavefront owns 64 columns: 32 gate and 32 up columns of a gated layer");
+    constexpr int ABYTES = DBM * 128, STAGE = (DBM + DBN) * 128;
+    constexpr int LA = ABYTES / (NT * 16), LB = (STAGE - ABYTES) / (NT * 16);
+    static_assert(ST * STAGE >= WMW * WNW * 8192, "the epilogue stages 8 KiB per wavefront");
+    __shared__ __attribute__((aligned(1024))) uint8_t s_ab[ST * STAGE];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WNW, wn = wave % WNW;
+
+    // tile: splits outermost, then bands of 4 M tiles with the M tiles inner, each
+    // XCD taking a contiguous run so that its L2 holds a window's operand panels
+    const int per = p.ntm * p.ntn;
+    const int tt = xcd_remap(blockIdx.x, per * p.splits);
+    const int split = __builtin_amdgcn_readfirstlane(tt / per);
+    const int t = tt - split * per;
+    const int band = t / (4 * p.ntn), within = t - band * 4 * p.ntn;
+    const int bm = min(4, p.ntm - band * 4);
+    const int m0 = __builtin_amdgcn_readfirstlane((band * 4 + within % bm) * DBM);
+    const int n0 = __builtin_amdgcn_readfirstlane((within / bm) * DBN);
+    const int slabs = (p.K + DBK - 1) / DBK;
+    const int ks0 = split * p.split_slabs;
+    const int nk = min(p.split_slabs, slabs - ks0);
+
+    // Operand sources: a 64-bit base per slab, 32-bit lane offsets inside it. Copy i
+    // of the workgroup fills LDS chunks [i NT, (i + 1) NT) of 16 bytes in thread
+    // order; each lane fetches whichever global chunk the swizzled layout has there.
+    const char* a_base;
+    const char* b_base;
+    int64_t a_bytes, b_bytes, a_step, b_step;
+    uint32_t a_off, b_off, a_istep, b_istep;
+    int a_c = 0, b_c = 0;  // K-major: this lane's first k inside a slab
+    if constexpr (A_KMAJ) {
+        const int r = tid >> 3, c = (tid & 7) ^ kmaj_swz(r);
+        a_base = (const char*)(p.A + (int64_t)m0 * p.lda);
+        a_bytes = (int64_t)min(p.M - m0, DBM) * p.lda * 2;
+        a_step = DBK * 2;
+        a_off = (uint32_t)((r * p.lda + c * 8) * 2);
+        a_istep = (uint32_t)(NT / 8 * p.lda * 2);
+        a_c = c * 8;
+    } else {
+        constexpr int CPR = DBM / 8;
+        const int kr = tid / CPR, c = (tid % CPR) ^ mn_swz<DBM>(kr);
+        const int col = m0 + c * 8;
+        a_base = (const char*)p.A;
+        a_bytes = (int64_t)p.K * p.lda * 2;
+        a_step = (int64_t)DBK * p.lda * 2;
+        a_off = col < p.M ? (uint32_t)((kr * p.lda + col) * 2) : kMasked;
+        a_istep = (uint32_t)(NT / CPR * p.lda * 2);
+    }
+    if constexpr (B_KMAJ) {
+        const int r = tid >> 3, c = (tid & 7) ^ kmaj_swz(r);
+        b_base = (const char*)(p.B + (int64_t)n0 * p.ldb);
+        b_bytes = (int64_t)min(p.N - n0, DBN) * p.ldb * 2;
+        b_step = DBK * 2;
+        b_off = (uint32_t)((r * p.ldb + c * 8) * 2);
+        b_istep = (uint32_t)(NT / 8 * p.ldb * 2);
+        b_c = c * 8;
+    } else {
+        constexpr int CPR = DBN / 8;
+        const int kr = tid / CPR, c = (tid % CPR) ^ mn_swz<DBN>(kr);
+        const int col = n0 + c * 8;
+        b_base = (const char*)p.B;
+        b_bytes = (int64_t)p.K * p.ldb * 2;
+        b_step = (int64_t)DBK * p.ldb * 2;
+        b_off = col < p.N ? (uint32_t)((kr * p.ldb + col) * 2) : kMasked;
+        b_istep = (uint32_t)(NT / CPR * p.ldb * 2);
+    }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS char*)&s_ab[0] + wave * 1024;
+    // K slab `ks` (of the whole reduction) into LDS stage `st`. In a last slab that
+    // ends inside, a K-major lane past K fetches nothing (zeros); an operand with K
+    // outermost ends at its last row by the buffer bound.
+    auto issue = [&](int ks, int st) {
+        const i32x4_t ra = rsrc_from(a_base, a_bytes, (int64_t)ks * a_step);
+        const i32x4_t rb = rsrc_from(b_base, b_bytes, (int64_t)ks * b_step);
+        const uint32_t l0 = lds0 + st * STAGE;
+        const int left = p.K - ks * DBK;
+        const bool am = A_KMAJ && a_c >= left, bmk = B_KMAJ && b_c >= left;
+#pragma unroll
+        for (int i = 0; i < LA; ++i) lds_copy16(ra, l0 + i * NT * 16, am ? kMasked : a_off + i * a_istep);
+#pragma unroll
+        for (int i = 0; i < LB; ++i) lds_copy16(rb, l0 + ABYTES + i * NT * 16, bmk ? kMasked : b_off + i * b_istep);
+    };
+
+    // MFMA operand of a 32-row (or 32-column) piece at K step ks: lane l holds index
+    // l & 31 and k = 16 ks + 8 (l >> 5) + [0, 8)
+    auto frag = [&](const uint8_t* s, auto KM, auto W, int base, int ks) -> bf16x8_t {
+        if constexpr (decltype(KM)::value) {
+            const int r = base + (lane & 31);
+            return __builtin_bit_cast(bf16x8_t, *(const uint4*)(s + kmaj_byte(r, 2 * ks + (lane >> 5))));
+        } else {
+            constexpr int w = decltype(W)::value;
+            const int lg = lane & 15;
+            const int c = base + 16 * ((lane >> 4) & 1) + 4 * (lg & 3);
+            const int k0 = 16 * ks + 8 * (lane >> 5) + (lg >> 2);
+            const int o0 = k0 * (2 * w) + (((c >> 3) ^ mn_swz<w>(k0)) << 4) + (c & 7) * 2;
+            const int k1 = k0 + 4;
+            const int o1 = k1 * (2 * w) + (((c >> 3) ^ mn_swz<w>(k1)) << 4) + (c & 7) * 2;
+            const bf16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4_t*)(s + o0));
+            const bf16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4_t*)(s + o1));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    };
+    auto fragA = [&](const uint8_t* s, int i, int ks) {
+        return frag(s, std::bool_constant<A_KMAJ>{}, std::integral_constant<int, DBM>{}, wm * 32 * TM + 32 * i, ks);
+    };
+    auto fragB = [&](const uint8_t* s, int j, int ks) {
+        return frag(s + ABYTES, std::bool_constant<B_KMAJ>{}, std::integral_constant<int, DBN>{}, wn * 64 + 32 * j, ks);
+    };
+
+    f32x16_t acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = (f32x16_t){};
+
+    for (int s = 0; s < ST - 1 && s < nk; ++s) issue(ks0 + s, s);
+    int st = 0;
+    for (int kt = 0; kt < nk; ++kt) {
+        // slab kt has landed, and every wavefront is done with slab kt - 1, whose
+        // stage the copies of slab kt + ST - 1 fill
+        if (nk - 1 - kt >= ST - 2) wait_barrier<(ST - 2) * (LA + LB)>();
+        else wait_barrier<0>();
+        const uint8_t* s = s_ab + st * STAGE;
+        bf16x8_t fa[2][TM], fb[2][TN];
+        fb[0][0] = fragB(s, 0, 0);
+        fa[0][0] = fragA(s, 0, 0);
+        fb[0][1] = fragB(s, 1, 0);
+#pragma unroll
+        for (int i = 1; i < TM; ++i) fa[0][i] = fragA(s, i, 0);
+        if (kt + ST - 1 < nk) issue(ks0 + kt + ST - 1, (st + ST - 1) % ST);
+        static_for<DBK / 16>([&](auto KS) {
+            constexpr int ks = KS, c = ks & 1;
+            if constexpr (ks + 1 < DBK / 16) {
+                fb[c ^ 1][0] = fragB(s, 0, ks + 1);
+                fa[c ^ 1][0] = fragA(s, 0, ks + 1);
+                fb[c ^ 1][1] = fragB(s, 1, ks + 1);
+#pragma unroll
+                for (int i = 1; i < TM; ++i) fa[c ^ 1][i] = fragA(s, i, ks + 1);
+            }
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[c][j], fa[c][i], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_s_setprio(0);
+        });
+        st = st + 1 == ST ? 0 : st + 1;
+    }
+
+    // ------------------------------------------------------------ epilogue
+    // Lane l holds row l & 31 of each 32 x 32 piece and, in register 4 Q + s, column
+    // 8 Q + 4 h + s, h = l >> 5. Values leave through this wavefront's 8 KiB of LDS so
+    // that a store instruction covers whole row runs; 16-byte chunks are XOR-swizzled
+    // by the row.
+    wait_barrier<0>();
+    uint8_t* stg = s_ab + wave * 8192;
+    const int h = lane >> 5, r = lane & 31;
+    const int col0 = n0 + wn * 64;
+    if (col0 >= p.N) return;  // no barrier follows: the staging is this wavefront's own
+    const int NO = kGated<ACT> ? p.N / 2 : p.N;
+    static_for<TM>([&](auto I) {
+        const int mb = m0 + wm * 32 * TM + 32 * I;
+        if (mb >= p.M) return;
+        if (ACT == 3 && p.part) {  // raw sums of this split
+            static_for<TN>([&](auto J) {
+                static_for<4>([&](auto Q) {
+                    const int ch = 8 * J + 2 * Q + h;
+                    *(float4*)(stg + r * 256 + ((ch ^ (r & 15)) << 4)) = make_float4(
+                        acc[I][J][4 * Q], acc[I][J][4 * Q + 1], acc[I][J][4 * Q + 2], acc[I][J][4 * Q + 3]);
+                });
+            });
+            wave_lds_sync();
+            float* out = p.part + (int64_t)split * p.M * p.N;
+            static_for<8>([&](auto It) {
+                const int R = 4 * It + (lane >> 4), c = lane & 15;
+                const float4 v = *(const float4*)(stg + R * 256 + ((c ^ (R & 15)) << 4));
+                const int m = mb + R, col = col0 + 4 * c;
+                if (m < p.M && col < p.N) *(float4*)(out + (int64_t)m * p.N + col) = v;
+            });
+            wave_lds_sync();
+            return;
+        }
+        if (p.bias) {
+            static_for<TN>([&](auto J) {
+                static_for<4>([&](auto Q) {
+                    const int col = col0 + 32 * J + 8 * Q + 4 * h;
+                    if (col < p.N) {
+                        float b[4];
+                        unpack_bf16x4(*(const uint2*)(p.bias + col), b);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) acc[I][J][4 * Q + s] += b[s];
+                    }
+                });
+            });
+        }
+        if (ACT != 3 && (p.z || p.z_q)) {
+            uint32_t pk[TN][8];
+            static_for<TN>([&](auto J) {
+                static_for<8>([&](auto R8) { pk[J][R8] = pack_bf16x2(acc[I][J][2 * R8], acc[I][J][2 * R8 + 1]); });
+            });
+            if (p.z_q) {
+                static_for<TN>([&](auto J) {
+                    const int cb = col0 + 32 * J;
+                    if (cb < p.N)
+                        mx_rowq32_if(pk[J], lane, mb + r < p.M, p.z_q + (int64_t)(mb + r) * p.N + cb,
+                                     p.z_s + (int64_t)(mb + r) * (p.N / 32) + cb / 32);
+                });
+            }
+            if (p.z) {
+                static_for<TN>([&](auto J) {
+                    static_for<4>([&](auto Q) {
+                        const int ch = 4 * J + Q;
+                        *(uint2*)(stg + r * 128 + ((ch ^ ((r >> 1) & 7)) << 4) + 8 * h) =
+                            make_uint2(pk[J][2 * Q], pk[J][2 * Q + 1]);
+                    });
+                });
+                wave_lds_sync();
+                static_for<4>([&](auto It) {
+                    const int R = 8 * It + (lane >> 3), c = lane & 7;
+                    const uint4 v = *(const uint4*)(stg + R * 128 + ((c ^ ((R >> 1) & 7)) << 4));
+                    const int m = mb + R, col = col0 + 8 * c;
+                    if (m < p.M && col < p.N) *(uint4*)(p.z + (int64_t)m * p.N + col) = v;
+                });
+                wave_lds_sync();
+            }
+        }
+        if constexpr (kGated<ACT>) {
+            static_for<4>([&](auto Q) {
+                float v[4];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) v[s] = glu_gate<ACT>(acc[I][0][4 * Q + s]) * acc[I][1][4 * Q + s];
+                const int ch = 2 * Q + h;
+                *(float4*)(stg + r * 128 + ((ch ^ (r & 7)) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
+            });
+            wave_lds_sync();
+            static_for<2>([&](auto It) {
+                const int R = 16 * It + (lane >> 2), c = lane & 3;
+                float v[8];
+                *(float4*)v = *(const float4*)(stg + R * 128 + (((2 * c) ^ (R & 7)) << 4));
+                *(float4*)(v + 4) = *(const float4*)(stg + R * 128 + (((2 * c + 1) ^ (R & 7)) << 4));
+                const int m = mb + R;
+                if (m < p.M) dense_store8(p, (int64_t)m * NO + col0 / 2 + 8 * c, v);
+            });
+        } else {
+            static_for<TN>([&](auto J) {
+                static_for<4>([&](auto Q) {
+                    float v[4];
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) v[s] = plain_act<ACT>(acc[I][J][4 * Q + s]);
+                    const int ch = 8 * J + 2 * Q + h;
+                    *(float4*)(stg + r * 256 + ((ch ^ (r & 15)) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
+                });
+            });
+            wave_lds_sync();
+            static_for<4>([&](auto It) {
+                const int R = 8 * It + (lane >> 3), c = lane & 7;
+                float v[8];
+                *(float4*)v = *(const float4*)(stg + R * 256 + (((2 * c) ^ (R & 15)) << 4));
+                *(float4*)(v + 4) = *(const float4*)(stg + R * 256 + (((2 * c + 1) ^ (R & 15)) << 4));
+                const int m = mb + R, col = col0 + 8 * c;
+                if (m < p.M && col < p.N) dense_store8(p, (int64_t)m * NO + col, v);
+            });
+        }
+        wave_lds_sync();
+    });
+}
+
+// Joins the K splits: the partial sums of 8 output columns (gated: 8 gate and 8
+// up columns) are added in split order, then the same epilogue as the kernel's.
+template <int ACT>
+__global__ void __launch_bounds__(256) dense_join_kernel(DenseArgs p) {
+    const int NO = kGated<ACT> ? p.N / 2 : p.N;
+    const int ng = NO / 8;
+    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (idx >= (int64_t)p.M * ng) return;  // z_q: whole groups of 4 threads, ng % 4 == 0
+    const int64_t m = idx / ng;
+    const int g = (int)(idx - m * ng);
+    constexpr int H = kGated<ACT> ? 2 : 1;
+    const int c0 = kGated<ACT> ? (g >> 2) * 64 + (g & 3) * 8 : g * 8;
+    float v[H][8];
+#pragma unroll
+    for (int u = 0; u < H; ++u) {
+        const int col = c0 + 32 * u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+        for (int s = 0; s < p.splits; ++s) {
+            const float4* q = (const float4*)(p.part + ((int64_t)s * p.M + m) * p.N + col);
+            const float4 a = q[0], b = q[1];
+            v[u][0] += a.x, v[u][1] += a.y, v[u][2] += a.z, v[u][3] += a.w;
+            v[u][4] += b.x, v[u][5] += b.y, v[u][6] += b.z, v[u][7] += b.w;
+        }
+        if (p.bias) {
+            float b[8];
+            const uint4 w = *(const uint4*)(p.bias + col);
+            unpack_bf16x4(make_uint2(w.x, w.y), b);
+            unpack_bf16x4(make_uint2(w.z, w.w), b + 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[u][i] += b[i];
+        }
+        if (ACT != 3 && (p.z || p.z_q)) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pk[i] = pack_bf16x2(v[u][2 * i], v[u][2 * i + 1]);
+            if (p.z) *(uint4*)(p.z + m * p.N + col) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            if (p.z_q) {
+                uint32_t am = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) am = max_u16x2(am, pk[i] & 0x7fff7fffu);
+                uint32_t amax = max(am & 0xffffu, am >> 16);
+                amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1, 64));
+                amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2, 64));
+                const int e = mx_block_exp(amax);
+                const float inv = mx_inv_scale(e);
+                uint2 q;
+                q.x = e4m3x4(bf16_lo(pk[0]) * inv, bf16_hi(pk[0]) * inv, bf16_lo(pk[1]) * inv, bf16_hi(pk[1]) * inv);
+                q.y = e4m3x4(bf16_lo(pk[2]) * inv, bf16_hi(pk[2]) * inv, bf16_lo(pk[3]) * inv, bf16_hi(pk[3]) * inv);
+                *(uint2*)(p.z_q + m * p.N + col) = q;
+                if ((g & 3) == 0) p.z_s[m * (p.N / 32) + col / 32] = (uint8_t)(e + 127);
+            }
+        }
+    }
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (kGated<ACT>) y[i] = glu_gate<ACT>(v[0][i]) * v[1][i];
+        else y[i] = plain_act<ACT>(v[0][i]);
+    }
+    dense_store8(p, m * NO + 8 * g, y);
+}
+
+// ------------------------------------------------------------------ host side
+// Tile and split of a product. Large tiles read each operand fewer times and run
+// the MFMAs with fewer LDS reads, but only pay when they fill the chip; otherwise
+// 128 x 128 tiles (two workgroups a compute unit), with K cut into pieces while
+// fewer than two workgroups a compute unit would run and a piece keeps 4 slabs.
+struct DensePlan {
+    bool big;
+    int ntm, ntn, splits, split_slabs;
+};
+constexpr int kDenseCus = 256;
+
+static DensePlan dense_plan(int64_t M, int64_t N, int64_t K) {
+    DensePlan d{};
+    const int64_t tb = ((M + 255) / 256) * ((N + 255) / 256);
+    const int64_t slabs = (K + DBK - 1) / DBK;
+    d.big = tb >= kDenseCus * 3 / 4;
+    const int64_t e = d.big ? 256 : 128;
+    d.ntm = (int)((M + e - 1) / e);
+    d.ntn = (int)((N + e - 1) / e);
+    int64_t s = 1;
+    const int64_t tiles = (int64_t)d.ntm * d.ntn;
+    if (!d.big) s = std::max<int64_t>(1, std::min<int64_t>(2 * kDenseCus / tiles, slabs / 4));
+    d.split_slabs = (int)((slabs + s - 1) / s);
+    d.splits = (int)((slabs + d.split_slabs - 1) / d.split_slabs);
+    return d;
+}
+
+size_t dense_part_bytes(int64_t M, int64_t N, int64_t K) {
+    const DensePlan d = dense_plan(M, N, K);
+    return d.splits > 1 ? (size_t)d.splits * M * N * sizeof(float) : 0;
+}
+
+template <bool A_KMAJ, bool B_KMAJ, int ACT>
+static void dense_launch(const DensePlan& d, const DenseArgs& a, hipStream_t s) {
+    const unsigned grid = (unsigned)(d.ntm * d.ntn * d.splits);
+    if (d.big)
+        dense_gemm_kernel<256, 256, 2, 4, 2, A_KMAJ, B_KMAJ, ACT><<<grid, 512, 0, s>>>(a);
+    else
+        dense_gemm_kernel<128, 128, 2, 2, 2, A_KMAJ, B_KMAJ, ACT><<<grid, 256, 0, s>>>(a);
+}
+
+template <bool A_KMAJ, bool B_KMAJ, int ACT>
+static int dense_run(DenseArgs a, void* ws, hipStream_t s) {
+    const DensePlan d = dense_plan(a.M, a.N, a.K);
+    a.ntm = d.ntm;
+    a.ntn = d.ntn;
+    a.splits = d.splits;
+    a.split_slabs = d.split_slabs;
+    if (d.splits == 1) {
+        a.part = nullptr;
+        dense_launch<A_KMAJ, B_KMAJ, ACT>(d, a, s);
+    } else {
+        a.part = (float*)ws;
+        dense_launch<A_KMAJ, B_KMAJ, 3>(d, a, s);
+        const int64_t items = (int64_t)a.M * ((kGated<ACT> ? a.N / 2 : a.N) / 8);
+        dense_join_kernel<ACT><<<(unsigned)((items + 255) / 256), 256, 0, s>>>(a);
+    }
+    return hipGetLastError() == hipSuccess ? 0 : -4;
+}
+
+int launch_linear_fwd(const uint16_t* x, const uint16_t* w, const uint16_t* bias, const uint16_t* res, int T,
+                      int K, int N, int act, int y_f32, void* y, uint16_t* z, uint8_t* z_q, uint8_t* z_s,
+                      void* ws, hipStream_t s) {
+    DenseArgs a{};
+    a.A = x, a.lda = K, a.B = w, a.ldb = N, a.M = T, a.N = N, a.K = K;
+    a.bias = bias, a.res = res, a.out = y, a.out_f32 = y_f32, a.z = z, a.z_q = z_q, a.z_s = z_s;
+    switch (act) {
+        case 0: return dense_run<true, false, 0>(a, ws, s);
+        case 1: return dense_run<true, false, 1>(a, ws, s);
+        case 2: return dense_run<true, false, 2>(a, ws, s);
+        case 3: return dense_run<true, false, 3>(a, ws, s);
+        case 4: return dense_run<true, false, 4>(a, ws, s);
+        default: return dense_run<true, false, 5>(a, ws, s);
+    }
+}
+
+int launch_linear_dgrad(const uint16_t* dz, const uint16_t* w, const uint16_t* res, int T, int K, int N,
+                        uint16_t* dx, void* ws, hipStream_t s) {
+    DenseArgs a{};
+    a.A = dz, a.lda = N, a.B = w, a.ldb = N, a.M = T, a.N = K, a.K = N;
+    a.res = res, a.out = dx;
+    return dense_run<true, true, 3>(a, ws, s);
+}
+
+int launch_linear_wgrad(const uint16_t* x, const uint16_t* dz, int T, int K, int N, int dw_f32, int accumulate,
+                        void* dw, void* ws, hipStream_t s) {
+    DenseArgs a{};
+    a.A = x, a.lda = K, a.B = dz, a.ldb = N, a.M = K, a.N = N, a.K = T;
+    a.out = dw, a.out_f32 = dw_f32, a.accumulate = accumulate;
+    return dense_run<false, false, 3>(a, ws, s);
+}
+
+}  // namespace moe

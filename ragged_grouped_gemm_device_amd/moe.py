@@ -27,6 +27,11 @@ MOE_MAX_EXPERTS = 1024
 MOE_ACT_SWIGLU = 0
 MOE_ACT_GEGLU = 1
 MOE_ACT_SRELU = 2   # non-gated relu(h)^2: FC1 width n
+MOE_ACT_NONE = 3    # the dense linear layer's further activations
+MOE_ACT_SILU = 4
+MOE_ACT_GELU = 5
+MOE_LINEAR_FWD = 0x1
+MOE_LINEAR_BWD = 0x2
 MOE_STAGE_FC1 = 0x01
 MOE_STAGE_FC2 = 0x02
 MOE_STAGE_DGRAD2 = 0x04
@@ -62,6 +67,15 @@ SIGNATURES = {
                                  C.c_uint, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P]),
     "moe_quant_mxfp8": (_I, [_P, _I, _I64, _I, _I, _P, _P, _P, _P, _P]),
     "moe_permute_quant_mxfp8": (_I, [_P, _P, _I, _I, _I, _I, _I64, _I, _P, _P, _P, _P, _P]),
+    "moe_linear_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "moe_linear_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_act_bwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
+    "moe_linear_dgrad": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _SZ, _P]),
+    "moe_linear_wgrad": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "moe_dequant_mxfp8": (_I, [_P, _P, _I64, _I, _P, _P]),
+    "moe_balance_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_balance_loss": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, C.c_float, C.c_float, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_balance_loss_bwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, C.c_float, C.c_float, _P, _I, _P, _P, _P]),
 }
 
 
@@ -268,6 +282,173 @@ def moe_permute_quant_mxfp8(x, src_of, k, E, mode, q_row=None, s_row=None, q_col
     rc = _lib().moe_permute_quant_mxfp8(_ptr(x), _ptr(src_of), T, k, E, d, src_of.shape[0], mode,
                                         _ptr(q_row), _ptr(s_row), _ptr(q_col), _ptr(s_col), _stream())
     _check("moe_permute_quant_mxfp8", rc)
+
+
+# ------------------------------------------------------------------ dense half of the layer
+_GATED = (MOE_ACT_SWIGLU, MOE_ACT_GEGLU)
+_BF, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _operand(t, shape, dtype, name, device):
+    """A tensor handed over by address must be exactly this dense matrix, on the device whose
+    stream the call goes to."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape)}")
+    if not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name}: needs a dense tensor on {device}")
+
+
+def _device(t):
+    """The device of the call: that of its first operand, which has to be the current one (the
+    kernels go to the current device's stream)."""
+    if t.device.type == "cuda" and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"operands are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _space(ws, device):
+    """(address, bytes) of a workspace tensor."""
+    if ws is None:
+        return None, 0
+    if not ws.is_contiguous() or ws.device != device:
+        raise ValueError(f"workspace: needs a dense tensor on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def moe_linear_workspace_bytes(T: int, K: int, N: int, passes: int = MOE_LINEAR_FWD | MOE_LINEAR_BWD) -> int:
+    return int(_lib().moe_linear_workspace_bytes(T, K, N, passes))
+
+
+def moe_linear_fwd(x, w, y, act=MOE_ACT_NONE, bias=None, residual=None, z=None, z_q=None, z_s=None,
+                   workspace=None):
+    """y = f(x w + bias) + residual; y is bf16 or fp32. z, or z_q and z_s, keep the pre-activation
+    for the backward pass (as bf16, as an 8-bit checkpoint)."""
+    dev = _device(x)
+    (T, K), N = x.shape, w.shape[1]
+    out = (T, N // 2 if act in _GATED else N)
+    _operand(x, (T, K), _BF, "x", dev)
+    _operand(w, (K, N), _BF, "w", dev)
+    _operand(y, out, (_BF, _F32), "y", dev)
+    _operand(bias, (N,), _BF, "bias", dev)
+    _operand(residual, out, _BF, "residual", dev)
+    _operand(z, (T, N), _BF, "z", dev)
+    _operand(z_q, (T, N), _U8, "z_q", dev)
+    _operand(z_s, (T, N // MOE_MX_BLOCK), _U8, "z_s", dev)
+    ws, nws = _space(workspace, dev)
+    rc = _lib().moe_linear_fwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), T, K, N, act, int(y.dtype == _F32),
+                               _ptr(y), _ptr(z), _ptr(z_q), _ptr(z_s), ws, nws, _stream())
+    _check("moe_linear_fwd", rc)
+
+
+def moe_act_bwd(dy, dz, act=MOE_ACT_NONE, z=None, z_q=None, z_s=None, a=None, dbias=None, workspace=None):
+    """dz = dy f'(z) with z as bf16 or from its 8-bit checkpoint; optionally a = f(z) and dbias =
+    column sums of dz. dz (and dy, when only a is wanted) may be None."""
+    ref = next(t for t in (z, z_q, dy) if t is not None)
+    dev = _device(ref)
+    T, N = ref.shape
+    out = (T, N // 2 if act in _GATED else N)
+    _operand(dy, out, _BF, "dy", dev)
+    _operand(z, (T, N), _BF, "z", dev)
+    _operand(z_q, (T, N), _U8, "z_q", dev)
+    _operand(z_s, (T, N // MOE_MX_BLOCK), _U8, "z_s", dev)
+    _operand(dz, (T, N), _BF, "dz", dev)
+    _operand(a, out, _BF, "a", dev)
+    _operand(dbias, (N,), _F32, "dbias", dev)
+    ws, nws = _space(workspace, dev)
+    rc = _lib().moe_act_bwd(_ptr(dy), _ptr(z), _ptr(z_q), _ptr(z_s), T, N, act, _ptr(dz), _ptr(a), _ptr(dbias),
+                            ws, nws, _stream())
+    _check("moe_act_bwd", rc)
+
+
+def moe_linear_dgrad(dz, w, dx, residual=None, workspace=None):
+    """dx = dz w^T + residual (residual may be dx itself)."""
+    dev = _device(dz)
+    T, (K, N) = dz.shape[0], w.shape
+    _operand(dz, (T, N), _BF, "dz", dev)
+    _operand(w, (K, N), _BF, "w", dev)
+    _operand(dx, (T, K), _BF, "dx", dev)
+    _operand(residual, (T, K), _BF, "residual", dev)
+    ws, nws = _space(workspace, dev)
+    _check("moe_linear_dgrad", _lib().moe_linear_dgrad(_ptr(dz), _ptr(w), _ptr(residual), T, K, N, _ptr(dx), ws,
+                                                       nws, _stream()))
+
+
+def moe_linear_wgrad(x, dz, dw, x_q=None, x_s=None, accumulate=False, workspace=None):
+    """dw = x^T dz (added to an fp32 dw with accumulate); x as bf16, or None with its 8-bit
+    checkpoint x_q, x_s."""
+    dev = _device(dz)
+    (T, N), K = dz.shape, dw.shape[0]
+    _operand(x, (T, K), _BF, "x", dev)
+    _operand(x_q, (T, K), _U8, "x_q", dev)
+    _operand(x_s, (T, K // MOE_MX_BLOCK), _U8, "x_s", dev)
+    _operand(dz, (T, N), _BF, "dz", dev)
+    _operand(dw, (K, N), (_BF, _F32), "dw", dev)
+    ws, nws = _space(workspace, dev)
+    _check("moe_linear_wgrad", _lib().moe_linear_wgrad(_ptr(x), _ptr(x_q), _ptr(x_s), _ptr(dz), T, K, N,
+                                                       int(dw.dtype == _F32), int(bool(accumulate)), _ptr(dw), ws,
+                                                       nws, _stream()))
+
+
+def moe_dequant_mxfp8(q, s, out):
+    """bf16 values of row-wise MXFP8 codes (restores an 8-bit checkpoint)."""
+    dev = _device(q)
+    R, Cc = q.shape
+    _operand(q, (R, Cc), _U8, "q", dev)
+    _operand(s, (R, Cc // MOE_MX_BLOCK), _U8, "s", dev)
+    _operand(out, (R, Cc), _BF, "out", dev)
+    _check("moe_dequant_mxfp8", _lib().moe_dequant_mxfp8(_ptr(q), _ptr(s), R, Cc, _ptr(out), _stream()))
+
+
+def moe_balance_workspace_bytes(T: int, E: int, S: int = 1) -> int:
+    return int(_lib().moe_balance_workspace_bytes(T, E, S))
+
+
+def _sequences(seq_offsets, S, dev):
+    _operand(seq_offsets, (S + 1,), _I32, "seq_offsets", dev)
+
+
+def moe_balance_loss(logits, topk_idx, loss, counts, prob, tokens, workspace, balance_coef, z_coef, valid=None,
+                     seq_offsets=None):
+    """Router losses [total, balance, z] with the per-sequence expert counts [S, E], mean
+    probabilities [S, E] and live tokens [S + 2] that the backward reads."""
+    dev = _device(logits)
+    (T, E), k, S = logits.shape, topk_idx.shape[1], counts.shape[0]
+    _operand(logits, (T, E), _F32, "logits", dev)
+    _operand(topk_idx, (T, k), _I32, "topk_idx", dev)
+    _operand(valid, (T,), (_U8, torch.bool), "valid", dev)
+    _sequences(seq_offsets, S, dev)
+    _operand(loss, (3,), _F32, "loss", dev)
+    _operand(counts, (S, E), _I32, "counts", dev)
+    _operand(prob, (S, E), _F32, "prob", dev)
+    _operand(tokens, (S + 2,), _I32, "tokens", dev)
+    ws, nws = _space(workspace, dev)
+    rc = _lib().moe_balance_loss(_ptr(logits), _ptr(topk_idx), _ptr(valid), _ptr(seq_offsets), T, E, k, S,
+                                 balance_coef, z_coef, _ptr(loss), _ptr(counts), _ptr(prob), _ptr(tokens), ws, nws,
+                                 _stream())
+    _check("moe_balance_loss", rc)
+
+
+def moe_balance_loss_bwd(logits, counts, tokens, dlogits, k, balance_coef, z_coef, valid=None, seq_offsets=None,
+                         grad=None, accumulate=False, dlogits_bf16=None):
+    """Gradient of the total router loss w.r.t. the logits, written to (or, with accumulate, added
+    to) dlogits; grad: the loss's upstream gradient (one fp32 value on the device)."""
+    dev = _device(logits)
+    (T, E), S = logits.shape, counts.shape[0]
+    _operand(logits, (T, E), _F32, "logits", dev)
+    _operand(counts, (S, E), _I32, "counts", dev)
+    _operand(tokens, (S + 2,), _I32, "tokens", dev)
+    _operand(valid, (T,), (_U8, torch.bool), "valid", dev)
+    _sequences(seq_offsets, S, dev)
+    _operand(dlogits, (T, E), _F32, "dlogits", dev)
+    _operand(dlogits_bf16, (T, E), _BF, "dlogits_bf16", dev)
+    if grad is not None:
+        _operand(grad.reshape(1), (1,), _F32, "grad", dev)
+    rc = _lib().moe_balance_loss_bwd(_ptr(logits), _ptr(counts), _ptr(tokens), _ptr(valid), _ptr(seq_offsets), T, E,
+                                     k, S, balance_coef, z_coef, _ptr(grad), int(bool(accumulate)), _ptr(dlogits),
+                                     _ptr(dlogits_bf16), _stream())
+    _check("moe_balance_loss_bwd", rc)
 
 
 # ------------------------------------------------------------------ buffers
