@@ -36,6 +36,7 @@ struct BalanceArgs {
     float* prob;
     int32_t* tokens;
     int etiles;
+    int alone;  // one workgroup does it all
     // backward
     const float* grad;
     int accumulate;
@@ -70,41 +71,77 @@ __device__ __forceinline__ void for_sequences(const BalanceArgs& p, int t0, int 
     }
 }
 
+// Reductions over a token's group of G lanes (every lane gets the result): DPP
+// quad permutes and row mirrors inside 16 lanes, lane exchanges beyond.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
+template <int G, class Op>
+__device__ __forceinline__ float group_reduce(float v, Op op) {
+    if constexpr (G >= 2) v = op(v, dpp<0xB1>(v));    // lane ^ 1
+    if constexpr (G >= 4) v = op(v, dpp<0x4E>(v));    // lane ^ 2
+    if constexpr (G >= 8) v = op(v, dpp<0x141>(v));   // the other quad of 8 lanes
+    if constexpr (G >= 16) v = op(v, dpp<0x140>(v));  // the other half of 16 lanes
+    if constexpr (G >= 32) v = op(v, __shfl_xor(v, 16, 64));
+    if constexpr (G >= 64) v = op(v, __shfl_xor(v, 32, 64));
+    return v;
+}
 template <int G>
 __device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-    return v;
+    return group_reduce<G>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-    return v;
+    return group_reduce<G>(v, [](float a, float b) { return a + b; });
 }
 
-// One token's logits in a group of G lanes (lane gl: experts gl + G i). Non-finite
-// logits count as -inf (probability 0), as in the router. Returns whether the
-// token has a finite logit; x becomes exp(x - max).
-template <int G, int PER>
-__device__ __forceinline__ bool token_softmax(const BalanceArgs& p, int t, int gl, bool on, float (&x)[PER],
-                                              float& mx, float& inv, float& lse) {
+// Expert of element i of lane gl: four neighbours a lane when rows are whole
+// 16-byte pieces (V4), else one.
+template <int G, bool V4>
+__device__ __forceinline__ int expert_of(int gl, int i) {
+    return V4 ? (i >> 2) * 4 * G + 4 * gl + (i & 3) : gl + G * i;
+}
+
+// One token's logits, PER a lane. Non-finite logits, experts past E and tokens
+// that are not live (on == false) count as -inf (probability 0), as in the router.
+template <int G, int PER, bool V4>
+__device__ __forceinline__ void token_load(const BalanceArgs& p, int t, int gl, bool on, float (&x)[PER]) {
     const float* row = p.logits + (int64_t)t * p.E;
-    mx = -INFINITY;
+    if constexpr (V4) {
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+            const int e = expert_of<G, true>(gl, i);
+            float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (on && e < p.E) v = *(const float4*)(row + e);
+            x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = expert_of<G, false>(gl, i);
+            x[i] = on && e < p.E ? row[e] : -INFINITY;
+        }
+    }
+}
+
+// x becomes exp(x - max); returns whether the token has a finite logit. The
+// hardware exponential's argument x log2(e) is rounded once: 2^-24 |x| relative.
+template <int G, int PER>
+__device__ __forceinline__ bool token_softmax(float (&x)[PER], float& inv, float& lse) {
+    float mx = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int e = gl + G * i;
-        float v = on && e < p.E ? row[e] : -INFINITY;
-        if (!isfinite(v)) v = -INFINITY;
-        x[i] = v;
-        mx = fmaxf(mx, v);
+        if (!isfinite(x[i])) x[i] = -INFINITY;
+        mx = fmaxf(mx, x[i]);
     }
     mx = group_max<G>(mx);
     const bool some = mx > -INFINITY;
+    const float ref = some ? mx : 0.f;  // exp(-inf - 0) = 0
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        x[i] = x[i] > -INFINITY ? expf(x[i] - mx) : 0.f;
+        x[i] = __expf(x[i] - ref);
         s += x[i];
     }
     s = group_sum<G>(s);
@@ -113,81 +150,13 @@ __device__ __forceinline__ bool token_softmax(const BalanceArgs& p, int t, int g
     return some;
 }
 
-template <int G, int PER>
-__global__ void __launch_bounds__(256) balance_chunk_kernel(BalanceArgs p) {
-    __shared__ float s_p[4][G * PER];
-    __shared__ int s_cnt[G * PER];
-    __shared__ float s_z[4];
-    __shared__ int s_n[4];
-    constexpr int NG = 256 / G;  // tokens at a time
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int gl = lane % G, grp = tid / G;
-    for (int e = tid; e < G * PER; e += 256) s_cnt[e] = 0;
-    __syncthreads();
-    const int c = blockIdx.x;
-    const int t0 = c * p.CT, t1 = min(p.T, t0 + p.CT);
-    for_sequences(p, t0, t1, [&](int s, int a, int b) {
-        if (s < 0) return;
-        float acc[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-        float z = 0.f;
-        int n = 0;
-        for (int tb = a; tb < b; tb += NG) {
-            const int t = tb + grp;
-            const bool on = t < b && (!p.valid || p.valid[t] != 0);
-            float x[PER], mx, inv, lse;
-            const bool some = token_softmax<G, PER>(p, on ? t : a, gl, on, x, mx, inv, lse);
-            if (some) {
-#pragma unroll
-                for (int i = 0; i < PER; ++i) acc[i] += x[i] * inv;
-                if (gl == 0) {
-                    z += lse * lse;
-                    ++n;
-                }
-                for (int j = gl; j < p.k; j += G) {
-                    const int e = p.topk_idx[(int64_t)t * p.k + j];
-                    if (e >= 0 && e < p.E) atomicAdd(&s_cnt[e], 1);
-                }
-            }
-        }
-        // over the wavefront's groups, then its 4 wavefronts
-#pragma unroll
-        for (int o = 32; o >= G; o >>= 1) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) acc[i] += __shfl_xor(acc[i], o, 64);
-            z += __shfl_xor(z, o, 64);
-            n += __shfl_xor(n, o, 64);
-        }
-        if (lane < G) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) s_p[wave][gl + G * i] = acc[i];
-        }
-        if (lane == 0) {
-            s_z[wave] = z;
-            s_n[wave] = n;
-        }
-        __syncthreads();
-        float* row = p.rows + (int64_t)(c + s) * (2 * p.E + 2);
-        for (int e = tid; e < p.E; e += 256) {
-            row[e] = (s_p[0][e] + s_p[1][e]) + (s_p[2][e] + s_p[3][e]);
-            ((int32_t*)row)[p.E + e] = s_cnt[e];
-            s_cnt[e] = 0;
-        }
-        if (tid == 0) {
-            ((int32_t*)row)[2 * p.E] = s_n[0] + s_n[1] + s_n[2] + s_n[3];
-            row[2 * p.E + 1] = (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]);
-        }
-        __syncthreads();
-    });
-}
-
-// Workgroup s etiles + x: sequence s, experts [32 x, 32 x + 32): joins the chunks' rows.
-__global__ void __launch_bounds__(256) balance_join_kernel(BalanceArgs p) {
+// Joins the chunks' rows of sequence s for experts [32 et, 32 et + 32); all 256
+// threads of a workgroup, also one after another for several (s, et).
+__device__ __forceinline__ void balance_join(const BalanceArgs& p, int s, int et) {
     __shared__ float s_p[8][33], s_z[256];
     __shared__ int s_c[8][33], s_n[256];
     const int tid = threadIdx.x, el = tid & 31, l = tid >> 5;
-    const int s = blockIdx.x / p.etiles, et = blockIdx.x - s * p.etiles, e = et * 32 + el;
+    const int e = et * 32 + el;
     const int a = seq_at(p, s), b = seq_at(p, s + 1);
     const int c0 = a / p.CT, c1 = b > a ? (b - 1) / p.CT + 1 : c0;
     const int64_t w = 2 * p.E + 2;
@@ -240,9 +209,11 @@ __global__ void __launch_bounds__(256) balance_join_kernel(BalanceArgs p) {
             }
         }
     }
+    __syncthreads();
 }
 
-__global__ void __launch_bounds__(256) balance_loss_kernel(BalanceArgs p) {
+// The losses from the joined sums (one workgroup of 256 threads).
+__device__ __forceinline__ void balance_total(const BalanceArgs& p) {
     __shared__ double s_b[256], s_z[256];
     __shared__ int s_n[256], s_live[256];
     const int tid = threadIdx.x;
@@ -276,10 +247,99 @@ __global__ void __launch_bounds__(256) balance_loss_kernel(BalanceArgs p) {
     }
 }
 
+__global__ void __launch_bounds__(256) balance_join_kernel(BalanceArgs p) {
+    const int s = blockIdx.x / p.etiles;
+    balance_join(p, s, blockIdx.x - s * p.etiles);
+}
+__global__ void __launch_bounds__(256) balance_total_kernel(BalanceArgs p) { balance_total(p); }
+
+// A group of G lanes per token, PER logits a lane, two tokens' loads in flight. One
+// workgroup alone (small inputs) goes on to join and finish.
+template <int G, int PER, bool V4>
+__global__ void __launch_bounds__(256) balance_chunk_kernel(BalanceArgs p) {
+    __shared__ float s_p[4][G * PER];
+    __shared__ int s_cnt[G * PER];
+    __shared__ float s_z[4];
+    __shared__ int s_n[4];
+    constexpr int NG = 256 / G;  // tokens at a time
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int gl = lane % G, grp = tid / G;
+    for (int e = tid; e < G * PER; e += 256) s_cnt[e] = 0;
+    __syncthreads();
+    const int c = blockIdx.x;
+    const int t0 = c * p.CT, t1 = min(p.T, t0 + p.CT);
+    for_sequences(p, t0, t1, [&](int s, int a, int b) {
+        if (s < 0) return;
+        float acc[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+        float z = 0.f;
+        int n = 0;
+        auto take = [&](int t, float (&x)[PER]) {
+            float inv, lse;
+            const bool some = token_softmax<G, PER>(x, inv, lse);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) acc[i] += x[i] * inv;
+            if (some) {
+                if (gl == 0) {
+                    z += lse * lse;
+                    ++n;
+                }
+                for (int j = gl; j < p.k; j += G) {
+                    const int e = p.topk_idx[(int64_t)t * p.k + j];
+                    if (e >= 0 && e < p.E) atomicAdd(&s_cnt[e], 1);
+                }
+            }
+        };
+        for (int tb = a; tb < b; tb += 2 * NG) {
+            float x0[PER], x1[PER];
+            const int ta = tb + grp, tc = ta + NG;
+            const bool ona = ta < b && (!p.valid || p.valid[ta] != 0);
+            const bool onc = tc < b && (!p.valid || p.valid[tc] != 0);
+            token_load<G, PER, V4>(p, ona ? ta : a, gl, ona, x0);
+            token_load<G, PER, V4>(p, onc ? tc : a, gl, onc, x1);
+            take(ta, x0);
+            take(tc, x1);
+        }
+        // over the wavefront's groups, then its 4 wavefronts
+#pragma unroll
+        for (int o = 32; o >= G; o >>= 1) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) acc[i] += __shfl_xor(acc[i], o, 64);
+            z += __shfl_xor(z, o, 64);
+            n += __shfl_xor(n, o, 64);
+        }
+        if (lane < G) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) s_p[wave][expert_of<G, V4>(gl, i)] = acc[i];
+        }
+        if (lane == 0) {
+            s_z[wave] = z;
+            s_n[wave] = n;
+        }
+        __syncthreads();
+        float* row = p.rows + (int64_t)(c + s) * (2 * p.E + 2);
+        for (int e = tid; e < p.E; e += 256) {
+            row[e] = (s_p[0][e] + s_p[1][e]) + (s_p[2][e] + s_p[3][e]);
+            ((int32_t*)row)[p.E + e] = s_cnt[e];
+            s_cnt[e] = 0;
+        }
+        if (tid == 0) {
+            ((int32_t*)row)[2 * p.E] = s_n[0] + s_n[1] + s_n[2] + s_n[3];
+            row[2 * p.E + 1] = (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]);
+        }
+        __syncthreads();
+    });
+    if (p.alone) {
+        for (int i = 0; i < p.S * p.etiles; ++i) balance_join(p, i / p.etiles, i % p.etiles);
+        balance_total(p);
+    }
+}
+
 // The gradient, one group of G lanes per token. f enters less its value at the
 // largest logit: the gradient does not change (sum_e p_e = 1), and where one
 // expert holds nearly all the probability, f_e - sum_j f_j p_j no longer cancels.
-template <int G, int PER>
+template <int G, int PER, bool V4>
 __global__ void __launch_bounds__(256) balance_bwd_kernel(BalanceArgs p) {
     constexpr int NG = 256 / G;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -295,14 +355,12 @@ __global__ void __launch_bounds__(256) balance_bwd_kernel(BalanceArgs p) {
         float f[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = gl + G * i;
+            const int e = expert_of<G, V4>(gl, i);
             f[i] = s >= 0 && e < p.E ? (float)p.counts[(int64_t)s * p.E + e] * fs : 0.f;
         }
-        for (int tb = a; tb < b; tb += NG) {
-            const int t = tb + grp;
-            const bool on = s >= 0 && t < b && (!p.valid || p.valid[t] != 0);
-            float x[PER], mx, inv, lse;
-            token_softmax<G, PER>(p, on ? t : a, gl, on, x, mx, inv, lse);
+        auto give = [&](int t, float (&x)[PER]) {
+            float inv, lse;
+            token_softmax<G, PER>(x, inv, lse);
             float ref = -INFINITY;  // x = exp(logit - max) is 1 at the largest logit
 #pragma unroll
             for (int i = 0; i < PER; ++i)
@@ -315,30 +373,75 @@ __global__ void __launch_bounds__(256) balance_bwd_kernel(BalanceArgs p) {
                 if (x[i] > 0.f) dot += x[i] * (f[i] - ref);
             }
             dot = group_sum<G>(dot);
-            if (t < b) {
+            const float zl = zc * lse;
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int e = gl + G * i;
+            for (int i = 0; i < PER; ++i) x[i] = x[i] > 0.f ? x[i] * (bc * ((f[i] - ref) - dot) + zl) : 0.f;
+            if (t >= b) return;
+            if constexpr (V4) {
+#pragma unroll
+                for (int i = 0; i < PER; i += 4) {
+                    const int e = expert_of<G, true>(gl, i);
                     if (e < p.E) {
                         const int64_t at = (int64_t)t * p.E + e;
-                        float d = x[i] > 0.f ? x[i] * (bc * ((f[i] - ref) - dot) + zc * lse) : 0.f;
-                        if (p.accumulate) d += p.dlogits[at];
+                        float4 d = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        if (p.accumulate) {
+                            const float4 o = *(const float4*)(p.dlogits + at);
+                            d.x += o.x, d.y += o.y, d.z += o.z, d.w += o.w;
+                        }
+                        *(float4*)(p.dlogits + at) = d;
+                        if (p.dlogits16)
+                            *(uint2*)(p.dlogits16 + at) = make_uint2(pack_bf16x2(d.x, d.y), pack_bf16x2(d.z, d.w));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int e = expert_of<G, false>(gl, i);
+                    if (e < p.E) {
+                        const int64_t at = (int64_t)t * p.E + e;
+                        const float d = p.accumulate ? x[i] + p.dlogits[at] : x[i];
                         p.dlogits[at] = d;
                         if (p.dlogits16) p.dlogits16[at] = (uint16_t)f32_to_bf16(d);
                     }
                 }
             }
+        };
+        for (int tb = a; tb < b; tb += 2 * NG) {
+            float x0[PER], x1[PER];
+            const int ta = tb + grp, tc = ta + NG;
+            const bool ona = s >= 0 && ta < b && (!p.valid || p.valid[ta] != 0);
+            const bool onc = s >= 0 && tc < b && (!p.valid || p.valid[tc] != 0);
+            token_load<G, PER, V4>(p, ona ? ta : a, gl, ona, x0);
+            token_load<G, PER, V4>(p, onc ? tc : a, gl, onc, x1);
+            give(ta, x0);
+            give(tc, x1);
         }
     });
 }
 
-static int balance_group(int E) { return E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64; }
+// Lanes per token and logits per lane: up to 16 logits a lane, so that a wavefront
+// works on several tokens at once and a reduction over a token takes few exchanges
+// (E = 256: 16 lanes, 4 tokens a wavefront; with 64 lanes a token 79 us instead).
+struct BalanceShape {
+    int G, PER;
+};
+static BalanceShape balance_shape(int E) {
+    if (E <= 16) return {4, 4};
+    if (E <= 32) return {8, 4};
+    if (E <= 64) return {16, 4};
+    if (E <= 128) return {16, 8};
+    if (E <= 256) return {16, 16};
+    if (E <= 512) return {32, 16};
+    return {64, MOE_MAX_E / 64};
+}
 
-// Tokens per chunk: about 1024 workgroups, at least one token per lane group.
+// Tokens per chunk: all of them where one workgroup passes over them in a few steps
+// (no further launch then), else about 2048 workgroups of whole steps.
 static int balance_chunk(int T, int E) {
-    const int ng = 256 / balance_group(E);
-    const int ct = (T + 1023) / 1024;
-    return (ct + ng - 1) / ng * ng;
+    const int step = 2 * 256 / balance_shape(E).G;
+    if (T <= 4 * step) return 4 * step;
+    const int ct = (T + 2047) / 2048;
+    return (ct + step - 1) / step * step;
 }
 
 static int balance_etiles(int E) { return (E + 31) / 32; }
@@ -349,18 +452,28 @@ size_t balance_workspace_bytes(int T, int E, int S) {
     return (size_t)(rows * (2 * E + 2) + (int64_t)S * balance_etiles(E) + S) * sizeof(float);
 }
 
-template <class F>
-static void by_experts(int E, F&& f) {
+template <bool V4, class F>
+static void by_shape(int E, F&& f) {
     using std::integral_constant;
-    if (E <= 8) f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-    else if (E <= 16) f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-    else if (E <= 32) f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-    else if (E <= 64) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    else if (E <= 128) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-    else if (E <= 256) f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
-    else if (E <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 8>{});
-    else f(integral_constant<int, 64>{}, integral_constant<int, MOE_MAX_E / 64>{});
+    const BalanceShape h = balance_shape(E);
+    const std::bool_constant<V4> v{};
+    if (h.G == 4) f(integral_constant<int, 4>{}, integral_constant<int, 4>{}, v);
+    else if (h.G == 8) f(integral_constant<int, 8>{}, integral_constant<int, 4>{}, v);
+    else if (h.G == 16 && h.PER == 4) f(integral_constant<int, 16>{}, integral_constant<int, 4>{}, v);
+    else if (h.G == 16 && h.PER == 8) f(integral_constant<int, 16>{}, integral_constant<int, 8>{}, v);
+    else if (h.G == 16) f(integral_constant<int, 16>{}, integral_constant<int, 16>{}, v);
+    else if (h.G == 32) f(integral_constant<int, 32>{}, integral_constant<int, 16>{}, v);
+    else f(integral_constant<int, 64>{}, integral_constant<int, 16>{}, v);
 }
+
+// Rows are read as 16-byte pieces when every row starts on one.
+template <class F>
+static void by_experts(int E, bool aligned, F&& f) {
+    if (E % 4 == 0 && aligned) by_shape<true>(E, f);
+    else by_shape<false>(E, f);
+}
+
+static bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 int launch_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* valid, const int32_t* seq,
                         int T, int E, int k, int S, float cb, float cz, float* loss, int32_t* counts,
@@ -370,15 +483,18 @@ int launch_balance_loss(const float* logits, const int32_t* topk_idx, const uint
     p.CT = balance_chunk(T, E);
     const int nchunks = (T + p.CT - 1) / p.CT;
     p.etiles = balance_etiles(E);
+    p.alone = nchunks == 1 && (int64_t)S * p.etiles <= 8;
     p.rows = (float*)ws;
     p.bal = p.rows + (int64_t)(nchunks + S) * (2 * E + 2);
     p.zs = p.bal + (int64_t)S * p.etiles;
     p.cb = cb, p.cz = cz, p.loss = loss, p.counts = counts, p.prob = prob, p.tokens = tokens;
-    by_experts(E, [&](auto G, auto PER) {
-        balance_chunk_kernel<decltype(G)::value, decltype(PER)::value><<<nchunks, 256, 0, s>>>(p);
+    by_experts(E, on16(logits), [&](auto G, auto PER, auto V4) {
+        balance_chunk_kernel<decltype(G)::value, decltype(PER)::value, decltype(V4)::value><<<nchunks, 256, 0, s>>>(p);
     });
-    balance_join_kernel<<<(unsigned)((int64_t)p.etiles * S), 256, 0, s>>>(p);
-    balance_loss_kernel<<<1, 256, 0, s>>>(p);
+    if (!p.alone) {
+        balance_join_kernel<<<(unsigned)((int64_t)p.etiles * S), 256, 0, s>>>(p);
+        balance_total_kernel<<<1, 256, 0, s>>>(p);
+    }
     return hipGetLastError() == hipSuccess ? 0 : -4;
 }
 
@@ -388,12 +504,13 @@ int launch_balance_loss_bwd(const float* logits, const int32_t* counts, const in
                             hipStream_t s) {
     BalanceArgs p{};
     p.logits = logits, p.valid = valid, p.seq = seq, p.T = T, p.E = E, p.k = k, p.S = S;
-    p.CT = balance_chunk(T, E);
+    const int step = 2 * 256 / balance_shape(E).G;
+    p.CT = (int)((((int64_t)T + 2047) / 2048 + step - 1) / step * step);
     p.counts = const_cast<int32_t*>(counts), p.tokens = const_cast<int32_t*>(tokens);
     p.cb = cb, p.cz = cz, p.grad = grad, p.accumulate = accumulate, p.dlogits = dlogits, p.dlogits16 = dlogits16;
     const int nchunks = (T + p.CT - 1) / p.CT;
-    by_experts(E, [&](auto G, auto PER) {
-        balance_bwd_kernel<decltype(G)::value, decltype(PER)::value><<<nchunks, 256, 0, s>>>(p);
+    by_experts(E, on16(logits) && on16(dlogits) && ((uintptr_t)dlogits16 & 7) == 0, [&](auto G, auto PER, auto V4) {
+        balance_bwd_kernel<decltype(G)::value, decltype(PER)::value, decltype(V4)::value><<<nchunks, 256, 0, s>>>(p);
     });
     return hipGetLastError() == hipSuccess ? 0 : -4;
 }

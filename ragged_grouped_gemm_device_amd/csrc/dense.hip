@@ -387,30 +387,17 @@ __global__ void __launch_bounds__(WMW * WNW * 64, 2) dense_gemm_kernel(DenseArgs
     });
 }
 
-// Joins the K splits: the partial sums of 8 output columns (gated: 8 gate and 8
-// up columns) are added in split order, then the same epilogue as the kernel's.
+// The epilogue on 8 columns of the output held by one thread: v[0] their sums over
+// K (gated: v[0] the gate and v[1] the up columns); g counts groups of 8 output
+// columns. With z_q, the 4 threads of a 32-column block are 4 neighbouring lanes.
 template <int ACT>
-__global__ void __launch_bounds__(256) dense_join_kernel(DenseArgs p) {
-    const int NO = kGated<ACT> ? p.N / 2 : p.N;
-    const int ng = NO / 8;
-    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (idx >= (int64_t)p.M * ng) return;  // z_q: whole groups of 4 threads, ng % 4 == 0
-    const int64_t m = idx / ng;
-    const int g = (int)(idx - m * ng);
+__device__ __forceinline__ void dense_finish8(const DenseArgs& p, int64_t m, int g, float (*v)[8]) {
     constexpr int H = kGated<ACT> ? 2 : 1;
+    const int NO = kGated<ACT> ? p.N / 2 : p.N;
     const int c0 = kGated<ACT> ? (g >> 2) * 64 + (g & 3) * 8 : g * 8;
-    float v[H][8];
 #pragma unroll
     for (int u = 0; u < H; ++u) {
         const int col = c0 + 32 * u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-        for (int s = 0; s < p.splits; ++s) {
-            const float4* q = (const float4*)(p.part + ((int64_t)s * p.M + m) * p.N + col);
-            const float4 a = q[0], b = q[1];
-            v[u][0] += a.x, v[u][1] += a.y, v[u][2] += a.z, v[u][3] += a.w;
-            v[u][4] += b.x, v[u][5] += b.y, v[u][6] += b.z, v[u][7] += b.w;
-        }
         if (p.bias) {
             float b[8];
             const uint4 w = *(const uint4*)(p.bias + col);
@@ -450,19 +437,214 @@ __global__ void __launch_bounds__(256) dense_join_kernel(DenseArgs p) {
     dense_store8(p, m * NO + 8 * g, y);
 }
 
+// Joins the K splits. A thread adds the partial sums of 8 output columns over every
+// L-th split; the L lanes' sums meet in LDS, lane order; then the epilogue. L = 8
+// where there are few outputs (one row), so that the splits' loads run side by side.
+template <int ACT, int L>
+__global__ void __launch_bounds__(256) dense_join_kernel(DenseArgs p) {
+    constexpr int H = kGated<ACT> ? 2 : 1;
+    constexpr int GB = 256 / L;  // groups per workgroup
+    __shared__ float s_v[L > 1 ? L : 1][L > 1 ? GB * (8 * H + 1) : 1];
+    const int ng = (kGated<ACT> ? p.N / 2 : p.N) / 8;
+    const int gi = threadIdx.x % GB, l = threadIdx.x / GB;
+    const int64_t idx = (int64_t)blockIdx.x * GB + gi;
+    const bool on = idx < (int64_t)p.M * ng;  // with z_q: whole groups of 4 threads, ng % 4 == 0
+    const int64_t m = on ? idx / ng : 0;
+    const int g = on ? (int)(idx - m * ng) : 0;
+    const int c0 = kGated<ACT> ? (g >> 2) * 64 + (g & 3) * 8 : g * 8;
+    float v[2][8];
+#pragma unroll
+    for (int u = 0; u < H; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+    if (on) {
+        const float* base = p.part + m * p.N + c0;
+        const int64_t step = (int64_t)p.M * p.N;
+#pragma unroll 4
+        for (int s = l; s < p.splits; s += L) {
+#pragma unroll
+            for (int u = 0; u < H; ++u) {
+                const float4* q = (const float4*)(base + s * step + 32 * u);
+                const float4 a = q[0], b = q[1];
+                v[u][0] += a.x, v[u][1] += a.y, v[u][2] += a.z, v[u][3] += a.w;
+                v[u][4] += b.x, v[u][5] += b.y, v[u][6] += b.z, v[u][7] += b.w;
+            }
+        }
+    }
+    if constexpr (L > 1) {
+#pragma unroll
+        for (int i = 0; i < 8 * H; ++i) s_v[l][gi * (8 * H + 1) + i] = v[i >> 3][i & 7];
+        __syncthreads();
+        if (l > 0) return;
+#pragma unroll
+        for (int i = 0; i < 8 * H; ++i)
+#pragma unroll
+            for (int k = 1; k < L; ++k) v[i >> 3][i & 7] += s_v[k][gi * (8 * H + 1) + i];
+    }
+    if (on) dense_finish8<ACT>(p, m, g, v);
+}
+
+// ------------------------------------------------------------------ few rows
+// Up to 64 rows (single tokens, decode batches): the product reads W once and does
+// little else. A workgroup owns 64 columns (32 gate and 32 up columns of a gated
+// layer) and a range of K; its 4 wavefronts take every fourth 64-deep slab of it,
+// each through LDS stages of its own, so the loop has no barrier: a wavefront waits
+// only for its own copies, ST - 1 slabs ahead of the one it multiplies. x comes in
+// the same way (XC copies of 8 rows). The wavefronts' sums
+// meet in LDS. [T = 1, K = 8192, N = 4096: bound by the read of W.]
+template <int XC>
+__global__ void __launch_bounds__(256, 1) dense_rows_kernel(DenseArgs p, int act) {
+    constexpr int MT = XC > 4 ? 2 : 1;
+    constexpr int ST = XC == 1 ? 4 : XC <= 4 ? 3 : 2;
+    constexpr int WB = 64 * 128, STAGE = WB + XC * 1024, CP = 8 + XC;
+    __shared__ __attribute__((aligned(1024))) uint8_t s_ab[4 * ST * STAGE];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int split = __builtin_amdgcn_readfirstlane(blockIdx.x / p.ntn);
+    const int n0 = __builtin_amdgcn_readfirstlane((blockIdx.x - split * p.ntn) * 64);
+    const int slabs = (p.K + DBK - 1) / DBK;
+    const int ks0 = split * p.split_slabs;
+    const int nk = min(p.split_slabs, slabs - ks0);
+    const int mine = nk > wave ? (nk - wave + 3) / 4 : 0;  // this wavefront's slabs: ks0 + wave + 4 j
+
+    const int kr = lane >> 3;  // W: k row of copy 0, 8 rows a copy; x: row of copy 0
+    const int wcol = n0 + ((lane & 7) ^ (((kr >> 1) & 1) << 2)) * 8;
+    const uint32_t w_off = wcol < p.N ? (uint32_t)((kr * p.ldb + wcol) * 2) : kMasked;
+    const uint32_t w_istep = (uint32_t)(8 * p.ldb * 2);
+    const uint8_t* mem = s_ab + wave * ST * STAGE;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS char*)mem;
+    const int64_t w_bytes = (int64_t)p.K * p.ldb * 2, x_bytes = (int64_t)p.M * p.lda * 2;
+    auto issue = [&](int j, int st) {
+        const int ks = ks0 + wave + 4 * j;
+        const i32x4_t rw = rsrc_from(p.B, w_bytes, (int64_t)ks * DBK * p.ldb * 2);
+        const i32x4_t rx = rsrc_from(p.A, x_bytes, (int64_t)ks * DBK * 2);
+        const uint32_t l0 = lds0 + st * STAGE;
+        const int left = p.K - ks * DBK;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) lds_copy16(rw, l0 + i * 1024, w_off + i * w_istep);
+#pragma unroll
+        for (int i = 0; i < XC; ++i) {
+            const int r = kr + 8 * i, c = ((lane & 7) ^ kmaj_swz(r)) * 8;
+            lds_copy16(rx, l0 + WB + i * 1024, r < p.M && c < left ? (uint32_t)((r * p.lda + c) * 2) : kMasked);
+        }
+    };
+    f32x16_t acc[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = (f32x16_t){};
+    for (int j = 0; j < ST - 1 && j < mine; ++j) issue(j, j);
+    int st = 0;
+    for (int j = 0; j < mine; ++j) {
+        // slab j has landed; the reads of slab j - 1, whose stage is filled next, are done
+        if (mine - 1 - j >= ST - 2)
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"((ST - 2) * CP) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
+        if (j + ST - 1 < mine) issue(j + ST - 1, (st + ST - 1) % ST);
+        const uint8_t* s = mem + st * STAGE;
+        static_for<4>([&](auto KS) {
+            constexpr int ks = KS;
+            bf16x8_t fx[MT], fw[2];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                // rows past the 8 XC copied ones repeat them: their products are never stored
+                const int r = (32 * i + (lane & 31)) & (8 * XC - 1);
+                fx[i] = __builtin_bit_cast(bf16x8_t, *(const uint4*)(s + WB + kmaj_byte(r, 2 * ks + (lane >> 5))));
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int lg = lane & 15;
+                const int c = 32 * u + 16 * ((lane >> 4) & 1) + 4 * (lg & 3);
+                const int k0 = 16 * ks + 8 * (lane >> 5) + (lg >> 2), k1 = k0 + 4;
+                const int o0 = k0 * 128 + (((c >> 3) ^ (((k0 >> 1) & 1) << 2)) << 4) + (c & 7) * 2;
+                const int o1 = k1 * 128 + (((c >> 3) ^ (((k1 >> 1) & 1) << 2)) << 4) + (c & 7) * 2;
+                const bf16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4_t*)(s + o0));
+                const bf16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4_t*)(s + o1));
+                fw[u] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    acc[i][u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fw[u], fx[i], acc[i][u], 0, 0, 0);
+        });
+        st = st + 1 == ST ? 0 : st + 1;
+    }
+    // join of the 4 wavefronts: 32 rows at a time, wavefront w's 8 KiB at 8192 w, the
+    // 16-byte chunks of a 256-byte row XOR-swizzled by the row
+    const int h = lane >> 5, r = lane & 31;
+    static_for<MT>([&](auto I) {
+        __syncthreads();
+        static_for<2>([&](auto J) {
+            static_for<4>([&](auto Q) {
+                const int ch = 8 * J + 2 * Q + h;
+                *(float4*)(s_ab + wave * 8192 + r * 256 + ((ch ^ (r & 15)) << 4)) = make_float4(
+                    acc[I][J][4 * Q], acc[I][J][4 * Q + 1], acc[I][J][4 * Q + 2], acc[I][J][4 * Q + 3]);
+            });
+        });
+        __syncthreads();
+        auto sum8 = [&](int row, int c8, float* v) {  // columns [8 c8, 8 c8 + 8) of the tile's row
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const uint8_t* at = s_ab + row * 256 + (((2 * c8 + q) ^ (row & 15)) << 4);
+                const float4 a = *(const float4*)at, b = *(const float4*)(at + 8192);
+                const float4 c = *(const float4*)(at + 16384), d = *(const float4*)(at + 24576);
+                v[4 * q] = (a.x + b.x) + (c.x + d.x);
+                v[4 * q + 1] = (a.y + b.y) + (c.y + d.y);
+                v[4 * q + 2] = (a.z + b.z) + (c.z + d.z);
+                v[4 * q + 3] = (a.w + b.w) + (c.w + d.w);
+            }
+        };
+        float v[2][8];
+        if (act > 1 || p.part) {
+            const int row = tid >> 3, c8 = tid & 7, col = n0 + 8 * c8;
+            const int64_t m = 32 * I + row;
+            sum8(row, c8, v[0]);
+            if (m < p.M && col < p.N) {
+                if (p.part) {
+                    float4* o = (float4*)(p.part + ((int64_t)split * p.M + m) * p.N + col);
+                    o[0] = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+                    o[1] = make_float4(v[0][4], v[0][5], v[0][6], v[0][7]);
+                } else if (act == 2) dense_finish8<2>(p, m, col / 8, v);
+                else if (act == 3) dense_finish8<3>(p, m, col / 8, v);
+                else if (act == 4) dense_finish8<4>(p, m, col / 8, v);
+                else dense_finish8<5>(p, m, col / 8, v);
+            }
+        } else if (tid < 128) {
+            const int row = tid >> 2, c8 = tid & 3;
+            const int64_t m = 32 * I + row;
+            sum8(row, c8, v[0]);
+            sum8(row, c8 + 4, v[1]);
+            if (m < p.M) {
+                if (act == 0) dense_finish8<0>(p, m, n0 / 16 + c8, v);
+                else dense_finish8<1>(p, m, n0 / 16 + c8, v);
+            }
+        }
+    });
+}
+
 // ------------------------------------------------------------------ host side
 // Tile and split of a product. Large tiles read each operand fewer times and run
 // the MFMAs with fewer LDS reads, but only pay when they fill the chip; otherwise
 // 128 x 128 tiles (two workgroups a compute unit), with K cut into pieces while
 // fewer than two workgroups a compute unit would run and a piece keeps 4 slabs.
 struct DensePlan {
-    bool big;
+    bool rows, big;
     int ntm, ntn, splits, split_slabs;
 };
 constexpr int kDenseCus = 256;
 
-static DensePlan dense_plan(int64_t M, int64_t N, int64_t K) {
+static DensePlan dense_plan(int64_t M, int64_t N, int64_t K, bool forward) {
     DensePlan d{};
+    if (forward && M <= 64) {
+        const int64_t slabs = (K + DBK - 1) / DBK;
+        d.rows = true;
+        d.ntm = 1;
+        d.ntn = (int)((N + 63) / 64);
+        const int64_t s = std::max<int64_t>(1, std::min<int64_t>(kDenseCus / d.ntn, slabs / 4));
+        d.split_slabs = (int)((slabs + s - 1) / s);
+        d.splits = (int)((slabs + d.split_slabs - 1) / d.split_slabs);
+        return d;
+    }
     const int64_t tb = ((M + 255) / 256) * ((N + 255) / 256);
     const int64_t slabs = (K + DBK - 1) / DBK;
     d.big = tb >= kDenseCus * 3 / 4;
@@ -477,14 +659,23 @@ static DensePlan dense_plan(int64_t M, int64_t N, int64_t K) {
     return d;
 }
 
-size_t dense_part_bytes(int64_t M, int64_t N, int64_t K) {
-    const DensePlan d = dense_plan(M, N, K);
+size_t dense_part_bytes(int64_t M, int64_t N, int64_t K, bool forward) {
+    const DensePlan d = dense_plan(M, N, K, forward);
     return d.splits > 1 ? (size_t)d.splits * M * N * sizeof(float) : 0;
 }
 
 template <bool A_KMAJ, bool B_KMAJ, int ACT>
 static void dense_launch(const DensePlan& d, const DenseArgs& a, hipStream_t s) {
     const unsigned grid = (unsigned)(d.ntm * d.ntn * d.splits);
+    if constexpr (A_KMAJ && !B_KMAJ) {
+        if (d.rows) {
+            if (a.M <= 8) dense_rows_kernel<1><<<grid, 256, 0, s>>>(a, ACT);
+            else if (a.M <= 16) dense_rows_kernel<2><<<grid, 256, 0, s>>>(a, ACT);
+            else if (a.M <= 32) dense_rows_kernel<4><<<grid, 256, 0, s>>>(a, ACT);
+            else dense_rows_kernel<8><<<grid, 256, 0, s>>>(a, ACT);
+            return;
+        }
+    }
     if (d.big)
         dense_gemm_kernel<256, 256, 2, 4, 2, A_KMAJ, B_KMAJ, ACT><<<grid, 512, 0, s>>>(a);
     else
@@ -493,7 +684,7 @@ static void dense_launch(const DensePlan& d, const DenseArgs& a, hipStream_t s) 
 
 template <bool A_KMAJ, bool B_KMAJ, int ACT>
 static int dense_run(DenseArgs a, void* ws, hipStream_t s) {
-    const DensePlan d = dense_plan(a.M, a.N, a.K);
+    const DensePlan d = dense_plan(a.M, a.N, a.K, A_KMAJ && !B_KMAJ);
     a.ntm = d.ntm;
     a.ntn = d.ntn;
     a.splits = d.splits;
@@ -505,7 +696,10 @@ static int dense_run(DenseArgs a, void* ws, hipStream_t s) {
         a.part = (float*)ws;
         dense_launch<A_KMAJ, B_KMAJ, 3>(d, a, s);
         const int64_t items = (int64_t)a.M * ((kGated<ACT> ? a.N / 2 : a.N) / 8);
-        dense_join_kernel<ACT><<<(unsigned)((items + 255) / 256), 256, 0, s>>>(a);
+        if (items <= 8192 && d.splits >= 4)
+            dense_join_kernel<ACT, 8><<<(unsigned)((items + 31) / 32), 256, 0, s>>>(a);
+        else
+            dense_join_kernel<ACT, 1><<<(unsigned)((items + 255) / 256), 256, 0, s>>>(a);
     }
     return hipGetLastError() == hipSuccess ? 0 : -4;
 }
