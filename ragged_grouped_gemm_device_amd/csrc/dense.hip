@@ -7,7 +7,7 @@
 //
 // One kernel template: a workgroup owns a BM x BN tile, its wavefronts 32 TM x
 // 64 pieces of it (fp32 accumulators in the MFMA layout); K moves in slabs of 64
-// through ST LDS stages filled by direct global -> LDS copies. Buffer bounds turn
+// through two LDS stages filled by direct global -> LDS copies. Buffer bounds turn
 // everything past the matrices' rows into zeros and a lane whose columns lie past
 // the end uses an offset past every buffer, so any T >= 1 and any K, N that are
 // multiples of 8 take the same path.
@@ -114,171 +114,19 @@ __device__ __forceinline__ void wait_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
 
-template <int DBM, int DBN, int WMW, int WNW, int ST, bool A_KMAJ, bool B_KMAJ, int ACT>
-__global__ void __launch_bounds__(WMW * WNW * 64, 2) dense_gemm_kernel(DenseArgs p) {
-    constexpr int NT = WMW * WNW * 64;
-    constexpr int TM = DBM / (32 * WMW), TN = DBN / (32 * WNW);
-    static_assert(TN == 2, "a wavefront owns 64 columns: 32 gate and 32 up columns of a gated layer");
-    constexpr int ABYTES = DBM * 128, STAGE = (DBM + DBN) * 128;
-    constexpr int LA = ABYTES / (NT * 16), LB = (STAGE - ABYTES) / (NT * 16);
-    static_assert(ST * STAGE >= WMW * WNW * 8192, "the epilogue stages 8 KiB per wavefront");
-    __shared__ __attribute__((aligned(1024))) uint8_t s_ab[ST * STAGE];
-
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / WNW, wn = wave % WNW;
-
-    // tile: splits outermost, then bands of 4 M tiles with the M tiles inner, each
-    // XCD taking a contiguous run so that its L2 holds a window's operand panels
-    const int per = p.ntm * p.ntn;
-    const int tt = xcd_remap(blockIdx.x, per * p.splits);
-    const int split = __builtin_amdgcn_readfirstlane(tt / per);
-    const int t = tt - split * per;
-    const int band = t / (4 * p.ntn), within = t - band * 4 * p.ntn;
-    const int bm = min(4, p.ntm - band * 4);
-    const int m0 = __builtin_amdgcn_readfirstlane((band * 4 + within % bm) * DBM);
-    const int n0 = __builtin_amdgcn_readfirstlane((within / bm) * DBN);
-    const int slabs = (p.K + DBK - 1) / DBK;
-    const int ks0 = split * p.split_slabs;
-    const int nk = min(p.split_slabs, slabs - ks0);
-
-    // Operand sources: a 64-bit base per slab, 32-bit lane offsets inside it. Copy i
-    // of the workgroup fills LDS chunks [i NT, (i + 1) NT) of 16 bytes in thread
-    // order; each lane fetches whichever global chunk the swizzled layout has there.
-    const char* a_base;
-    const char* b_base;
-    int64_t a_bytes, b_bytes, a_step, b_step;
-    uint32_t a_off, b_off, a_istep, b_istep;
-    int a_c = 0, b_c = 0;  // K-major: this lane's first k inside a slab
-    if constexpr (A_KMAJ) {
-        const int r = tid >> 3, c = (tid & 7) ^ kmaj_swz(r);
-        a_base = (const char*)(p.A + (int64_t)m0 * p.lda);
-        a_bytes = (int64_t)min(p.M - m0, DBM) * p.lda * 2;
-        a_step = DBK * 2;
-        a_off = (uint32_t)((r * p.lda + c * 8) * 2);
-        a_istep = (uint32_t)(NT / 8 * p.lda * 2);
-        a_c = c * 8;
-    } else {
-        constexpr int CPR = DBM / 8;
-        const int kr = tid / CPR, c = (tid % CPR) ^ mn_swz<DBM>(kr);
-        const int col = m0 + c * 8;
-        a_base = (const char*)p.A;
-        a_bytes = (int64_t)p.K * p.lda * 2;
-        a_step = (int64_t)DBK * p.lda * 2;
-        a_off = col < p.M ? (uint32_t)((kr * p.lda + col) * 2) : kMasked;
-        a_istep = (uint32_t)(NT / CPR * p.lda * 2);
-    }
-    if constexpr (B_KMAJ) {
-        const int r = tid >> 3, c = (tid & 7) ^ kmaj_swz(r);
-        b_base = (const char*)(p.B + (int64_t)n0 * p.ldb);
-        b_bytes = (int64_t)min(p.N - n0, DBN) * p.ldb * 2;
-        b_step = DBK * 2;
-        b_off = (uint32_t)((r * p.ldb + c * 8) * 2);
-        b_istep = (uint32_t)(NT / 8 * p.ldb * 2);
-        b_c = c * 8;
-    } else {
-        constexpr int CPR = DBN / 8;
-        const int kr = tid / CPR, c = (tid % CPR) ^ mn_swz<DBN>(kr);
-        const int col = n0 + c * 8;
-        b_base = (const char*)p.B;
-        b_bytes = (int64_t)p.K * p.ldb * 2;
-        b_step = (int64_t)DBK * p.ldb * 2;
-        b_off = col < p.N ? (uint32_t)((kr * p.ldb + col) * 2) : kMasked;
-        b_istep = (uint32_t)(NT / CPR * p.ldb * 2);
-    }
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS char*)&s_ab[0] + wave * 1024;
-    // K slab `ks` (of the whole reduction) into LDS stage `st`. In a last slab that
-    // ends inside, a K-major lane past K fetches nothing (zeros); an operand with K
-    // outermost ends at its last row by the buffer bound.
-    auto issue = [&](int ks, int st) {
-        const i32x4_t ra = rsrc_from(a_base, a_bytes, (int64_t)ks * a_step);
-        const i32x4_t rb = rsrc_from(b_base, b_bytes, (int64_t)ks * b_step);
-        const uint32_t l0 = lds0 + st * STAGE;
-        const int left = p.K - ks * DBK;
-        const bool am = A_KMAJ && a_c >= left, bmk = B_KMAJ && b_c >= left;
-#pragma unroll
-        for (int i = 0; i < LA; ++i) lds_copy16(ra, l0 + i * NT * 16, am ? kMasked : a_off + i * a_istep);
-#pragma unroll
-        for (int i = 0; i < LB; ++i) lds_copy16(rb, l0 + ABYTES + i * NT * 16, bmk ? kMasked : b_off + i * b_istep);
-    };
-
-    // MFMA operand of a 32-row (or 32-column) piece at K step ks: lane l holds index
-    // l & 31 and k = 16 ks + 8 (l >> 5) + [0, 8)
-    auto frag = [&](const uint8_t* s, auto KM, auto W, int base, int ks) -> bf16x8_t {
-        if constexpr (decltype(KM)::value) {
-            const int r = base + (lane & 31);
-            return __builtin_bit_cast(bf16x8_t, *(const uint4*)(s + kmaj_byte(r, 2 * ks + (lane >> 5))));
-        } else {
-            constexpr int w = decltype(W)::value;
-            const int lg = lane & 15;
-            const int c = base + 16 * ((lane >> 4) & 1) + 4 * (lg & 3);
-            const int k0 = 16 * ks + 8 * (lane >> 5) + (lg >> 2);
-            const int o0 = k0 * (2 * w) + (((c >> 3) ^ mn_swz<w>(k0)) << 4) + (c & 7) * 2;
-            const int k1 = k0 + 4;
-            const int o1 = k1 * (2 * w) + (((c >> 3) ^ mn_swz<w>(k1)) << 4) + (c & 7) * 2;
-            const bf16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4_t*)(s + o0));
-            const bf16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4_t*)(s + o1));
-            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
-    };
-    auto fragA = [&](const uint8_t* s, int i, int ks) {
-        return frag(s, std::bool_constant<A_KMAJ>{}, std::integral_constant<int, DBM>{}, wm * 32 * TM + 32 * i, ks);
-    };
-    auto fragB = [&](const uint8_t* s, int j, int ks) {
-        return frag(s + ABYTES, std::bool_constant<B_KMAJ>{}, std::integral_constant<int, DBN>{}, wn * 64 + 32 * j, ks);
-    };
-
-    f32x16_t acc[TM][TN];
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = (f32x16_t){};
-
-    for (int s = 0; s < ST - 1 && s < nk; ++s) issue(ks0 + s, s);
-    int st = 0;
-    for (int kt = 0; kt < nk; ++kt) {
-        // slab kt has landed, and every wavefront is done with slab kt - 1, whose
-        // stage the copies of slab kt + ST - 1 fill
-        if (nk - 1 - kt >= ST - 2) wait_barrier<(ST - 2) * (LA + LB)>();
-        else wait_barrier<0>();
-        const uint8_t* s = s_ab + st * STAGE;
-        bf16x8_t fa[2][TM], fb[2][TN];
-        fb[0][0] = fragB(s, 0, 0);
-        fa[0][0] = fragA(s, 0, 0);
-        fb[0][1] = fragB(s, 1, 0);
-#pragma unroll
-        for (int i = 1; i < TM; ++i) fa[0][i] = fragA(s, i, 0);
-        if (kt + ST - 1 < nk) issue(ks0 + kt + ST - 1, (st + ST - 1) % ST);
-        static_for<DBK / 16>([&](auto KS) {
-            constexpr int ks = KS, c = ks & 1;
-            if constexpr (ks + 1 < DBK / 16) {
-                fb[c ^ 1][0] = fragB(s, 0, ks + 1);
-                fa[c ^ 1][0] = fragA(s, 0, ks + 1);
-                fb[c ^ 1][1] = fragB(s, 1, ks + 1);
-#pragma unroll
-                for (int i = 1; i < TM; ++i) fa[c ^ 1][i] = fragA(s, i, ks + 1);
-            }
-            __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[c][j], fa[c][i], acc[i][j], 0, 0, 0);
-            __builtin_amdgcn_s_setprio(0);
-        });
-        st = st + 1 == ST ? 0 : st + 1;
-    }
-
-    // ------------------------------------------------------------ epilogue
-    // Lane l holds row l & 31 of each 32 x 32 piece and, in register 4 Q + s, column
-    // 8 Q + 4 h + s, h = l >> 5. Values leave through this wavefront's 8 KiB of LDS so
-    // that a store instruction covers whole row runs; 16-byte chunks are XOR-swizzled
-    // by the row.
-    wait_barrier<0>();
-    uint8_t* stg = s_ab + wave * 8192;
+// The epilogue of one wavefront's piece of a tile. Lane l holds row l & 31 of each 32
+// x 32 block and, in register 4 Q + s, column 8 Q + 4 h + s, h = l >> 5. Values leave
+// through the wavefront's 8 KiB of the LDS stage `stg` that the tile no longer reads
+// (the next tile's first slab goes to the other one), so that a store instruction
+// covers whole row runs; 16-byte chunks are XOR-swizzled by the row.
+template <int DBM, int DBN, int WMW, int WNW, int TM, int TN, int ACT>
+__device__ __forceinline__ void dense_epilogue(const DenseArgs& p, f32x16_t (&acc)[TM][TN], uint8_t* stg, int m0,
+                                               int n0, int split, int wm, int wn, int lane) {
+    // every wavefront has read the last slab out of the stage
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
     const int h = lane >> 5, r = lane & 31;
     const int col0 = n0 + wn * 64;
-    if (col0 >= p.N) return;  // no barrier follows: the staging is this wavefront's own
+    if (col0 >= p.N) return;
     const int NO = kGated<ACT> ? p.N / 2 : p.N;
     static_for<TM>([&](auto I) {
         const int mb = m0 + wm * 32 * TM + 32 * I;
@@ -385,6 +233,215 @@ __global__ void __launch_bounds__(WMW * WNW * 64, 2) dense_gemm_kernel(DenseArgs
         }
         wave_lds_sync();
     });
+}
+
+template <int DBM, int DBN, int WMW, int WNW, bool A_KMAJ, bool B_KMAJ, int ACT>
+__global__ void __launch_bounds__(WMW * WNW * 64, 2) dense_gemm_kernel(DenseArgs p) {
+    constexpr int NT = WMW * WNW * 64;
+    constexpr int TM = DBM / (32 * WMW), TN = DBN / (32 * WNW);
+    static_assert(TN == 2, "a wavefront owns 64 columns: 32 gate and 32 up columns of a gated layer");
+    constexpr int ABYTES = DBM * 128, STAGE = (DBM + DBN) * 128;
+    constexpr int LA = ABYTES / (NT * 16), LB = (STAGE - ABYTES) / (NT * 16);
+    static_assert(STAGE >= WMW * WNW * 8192, "the epilogue stages 8 KiB per wavefront in one LDS stage");
+    __shared__ __attribute__((aligned(1024))) uint8_t s_ab[2 * STAGE];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WNW, wn = wave % WNW;
+
+    // Tiles: splits outermost, then bands of 4 M tiles with the M tiles inner. The
+    // kernel is persistent: round r covers tiles [r nb, (r + 1) nb), of which each XCD
+    // (workgroups are dealt round robin to 8) takes a contiguous eighth, so that its
+    // L2 holds a window's operand panels.
+    const int per = p.ntm * p.ntn, total = per * p.splits;
+    const int nb = gridDim.x;  // a multiple of 8
+    const int first = (blockIdx.x & 7) * (nb >> 3) + (blockIdx.x >> 3);
+    const int slabs = (p.K + DBK - 1) / DBK;
+    struct Tile {
+        int m0, n0, split, ks0, nk;
+    };
+    auto get_tile = [&](int tt) -> Tile {
+        Tile tl;
+        tl.split = __builtin_amdgcn_readfirstlane(tt / per);
+        const int t = tt - tl.split * per;
+        const int band = t / (4 * p.ntn), within = t - band * 4 * p.ntn;
+        const int bm = min(4, p.ntm - band * 4);
+        tl.m0 = __builtin_amdgcn_readfirstlane((band * 4 + within % bm) * DBM);
+        tl.n0 = __builtin_amdgcn_readfirstlane((within / bm) * DBN);
+        tl.ks0 = tl.split * p.split_slabs;
+        tl.nk = min(p.split_slabs, slabs - tl.ks0);
+        return tl;
+    };
+
+    // Operand sources: a 64-bit base per slab, 32-bit lane offsets inside it. Copy i
+    // of the workgroup fills LDS chunks [i NT, (i + 1) NT) of 16 bytes in thread
+    // order; each lane fetches whichever global chunk the swizzled layout has there.
+    struct Src {
+        const char* a_base;
+        const char* b_base;
+        int64_t a_bytes, b_bytes;
+        uint32_t a_off, b_off;
+    };
+    constexpr int ACPR = A_KMAJ ? 8 : DBM / 8, BCPR = B_KMAJ ? 8 : DBN / 8;  // chunks per slab row
+    const int a_r = tid / ACPR, b_r = tid / BCPR;
+    const int a_c = (tid % ACPR) ^ (A_KMAJ ? kmaj_swz(a_r) : mn_swz<DBM>(a_r));
+    const int b_c = (tid % BCPR) ^ (B_KMAJ ? kmaj_swz(b_r) : mn_swz<DBN>(b_r));
+    const int64_t a_step = A_KMAJ ? DBK * 2 : (int64_t)DBK * p.lda * 2;
+    const int64_t b_step = B_KMAJ ? DBK * 2 : (int64_t)DBK * p.ldb * 2;
+    const uint32_t a_istep = (uint32_t)(NT / ACPR * p.lda * 2), b_istep = (uint32_t)(NT / BCPR * p.ldb * 2);
+    auto make_src = [&](const Tile& tl) -> Src {
+        Src sr;
+        if constexpr (A_KMAJ) {
+            sr.a_base = (const char*)(p.A + (int64_t)tl.m0 * p.lda);
+            sr.a_bytes = (int64_t)min(p.M - tl.m0, DBM) * p.lda * 2;
+            sr.a_off = (uint32_t)((a_r * p.lda + a_c * 8) * 2);
+        } else {
+            const int col = tl.m0 + a_c * 8;
+            sr.a_base = (const char*)p.A;
+            sr.a_bytes = (int64_t)p.K * p.lda * 2;
+            sr.a_off = col < p.M ? (uint32_t)((a_r * p.lda + col) * 2) : kMasked;
+        }
+        if constexpr (B_KMAJ) {
+            sr.b_base = (const char*)(p.B + (int64_t)tl.n0 * p.ldb);
+            sr.b_bytes = (int64_t)min(p.N - tl.n0, DBN) * p.ldb * 2;
+            sr.b_off = (uint32_t)((b_r * p.ldb + b_c * 8) * 2);
+        } else {
+            const int col = tl.n0 + b_c * 8;
+            sr.b_base = (const char*)p.B;
+            sr.b_bytes = (int64_t)p.K * p.ldb * 2;
+            sr.b_off = col < p.N ? (uint32_t)((b_r * p.ldb + col) * 2) : kMasked;
+        }
+        return sr;
+    };
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS char*)&s_ab[0] + wave * 1024;
+    // K slab `ks` (of the whole reduction) into LDS stage `st`: the A copies, the B
+    // copies. In a last slab that ends inside, a K-major lane past K fetches nothing
+    // (zeros); an operand with K outermost ends at its last row by the buffer bound.
+    auto issue_a = [&](const Src& sr, int ks, int st) {
+        const i32x4_t r = rsrc_from(sr.a_base, sr.a_bytes, (int64_t)ks * a_step);
+        const bool out = A_KMAJ && a_c * 8 >= p.K - ks * DBK;
+#pragma unroll
+        for (int i = 0; i < LA; ++i)
+            lds_copy16(r, lds0 + st * STAGE + i * NT * 16, out ? kMasked : sr.a_off + i * a_istep);
+    };
+    auto issue_b = [&](const Src& sr, int ks, int st) {
+        const i32x4_t r = rsrc_from(sr.b_base, sr.b_bytes, (int64_t)ks * b_step);
+        const bool out = B_KMAJ && b_c * 8 >= p.K - ks * DBK;
+#pragma unroll
+        for (int i = 0; i < LB; ++i)
+            lds_copy16(r, lds0 + st * STAGE + ABYTES + i * NT * 16, out ? kMasked : sr.b_off + i * b_istep);
+    };
+
+    // MFMA operand of a 32-row (or 32-column) piece at K step ks: lane l holds index
+    // l & 31 and k = 16 ks + 8 (l >> 5) + [0, 8)
+    auto frag = [&](const uint8_t* s, auto KM, auto W, int base, int ks) -> bf16x8_t {
+        if constexpr (decltype(KM)::value) {
+            const int r = base + (lane & 31);
+            return __builtin_bit_cast(bf16x8_t, *(const uint4*)(s + kmaj_byte(r, 2 * ks + (lane >> 5))));
+        } else {
+            constexpr int w = decltype(W)::value;
+            const int lg = lane & 15;
+            const int c = base + 16 * ((lane >> 4) & 1) + 4 * (lg & 3);
+            const int k0 = 16 * ks + 8 * (lane >> 5) + (lg >> 2);
+            const int o0 = k0 * (2 * w) + (((c >> 3) ^ mn_swz<w>(k0)) << 4) + (c & 7) * 2;
+            const int k1 = k0 + 4;
+            const int o1 = k1 * (2 * w) + (((c >> 3) ^ mn_swz<w>(k1)) << 4) + (c & 7) * 2;
+            const bf16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4_t*)(s + o0));
+            const bf16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4_t*)(s + o1));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    };
+    auto fragA = [&](int st, int i, int ks) {
+        return frag(s_ab + st * STAGE, std::bool_constant<A_KMAJ>{}, std::integral_constant<int, DBM>{},
+                    wm * 32 * TM + 32 * i, ks);
+    };
+    auto fragB = [&](int st, int j, int ks) {
+        return frag(s_ab + st * STAGE + ABYTES, std::bool_constant<B_KMAJ>{}, std::integral_constant<int, DBN>{},
+                    wn * 64 + 32 * j, ks);
+    };
+    bf16x8_t fa[2][TM], fb[2][TN];
+    // the first MFMA row's operands; the other A fragments follow behind its MFMAs
+    auto load_row0 = [&](int set, int st, int ks) {
+        fb[set][0] = fragB(st, 0, ks);
+        fa[set][0] = fragA(st, 0, ks);
+        fb[set][1] = fragB(st, 1, ks);
+    };
+    f32x16_t acc[TM][TN];
+
+    int tt = first;
+    if (tt >= total) return;
+    Tile tl = get_tile(tt);
+    Src src = make_src(tl);
+    int st = 0;  // LDS stage of the current slab
+    issue_a(src, tl.ks0, 0);
+    issue_b(src, tl.ks0, 0);
+    for (;;) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = (f32x16_t){};
+        // the next tile's first slab is fetched during this one's last
+        const int tn = tt + nb;
+        const bool have_next = tn < total;
+        Tile tl_next = tl;
+        Src src_next = src;
+        if (have_next) {
+            tl_next = get_tile(tn);
+            src_next = make_src(tl_next);
+        }
+        wait_barrier<0>();  // the first slab has landed, the previous tile's staging is read out
+        load_row0(0, st, 0);
+        for (int kt = 0; kt < tl.nk; ++kt) {
+            const bool last = kt + 1 == tl.nk;
+            static_for<DBK / 16>([&](auto KS) {
+                constexpr int ks = KS, c = ks & 1;
+                // After the barrier all wavefronts ask LDS for fragments at once: only
+                // the first row's operands go first, the rest and the next step's
+                // behind its MFMAs; the next slab's A and B copies in two steps.
+                __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[0][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[c][j], fa[c][0], acc[0][j], 0, 0, 0);
+                if constexpr (ks == 0) {
+#pragma unroll
+                    for (int i = 1; i < TM; ++i) fa[0][i] = fragA(st, i, 0);
+                }
+                if constexpr (ks + 1 < DBK / 16) {
+                    load_row0(c ^ 1, st, ks + 1);
+#pragma unroll
+                    for (int i = 1; i < TM; ++i) fa[c ^ 1][i] = fragA(st, i, ks + 1);
+                }
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[1][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[c][j], fa[c][1], acc[1][j], 0, 0, 0);
+                if constexpr (ks == 0) {
+                    if (!last) issue_a(src, tl.ks0 + kt + 1, st ^ 1);
+                    else if (have_next) issue_a(src_next, tl_next.ks0, st ^ 1);
+                }
+                if constexpr (ks == 1) {
+                    if (!last) issue_b(src, tl.ks0 + kt + 1, st ^ 1);
+                    else if (have_next) issue_b(src_next, tl_next.ks0, st ^ 1);
+                }
+#pragma unroll
+                for (int i = 2; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[c][j], fa[c][i], acc[i][j], 0, 0, 0);
+                __builtin_amdgcn_s_setprio(0);
+            });
+            if (!last) {
+                wait_barrier<0>();
+                load_row0(0, st ^ 1, 0);
+            }
+            st ^= 1;
+        }
+        dense_epilogue<DBM, DBN, WMW, WNW, TM, TN, ACT>(p, acc, s_ab + (st ^ 1) * STAGE + wave * 8192, tl.m0, tl.n0,
+                                                        tl.split, wm, wn, lane);
+        if (!have_next) break;
+        tt = tn;
+        tl = tl_next;
+        src = src_next;
+    }
 }
 
 // The epilogue on 8 columns of the output held by one thread: v[0] their sums over
@@ -666,9 +723,10 @@ size_t dense_part_bytes(int64_t M, int64_t N, int64_t K, bool forward) {
 
 template <bool A_KMAJ, bool B_KMAJ, int ACT>
 static void dense_launch(const DensePlan& d, const DenseArgs& a, hipStream_t s) {
-    const unsigned grid = (unsigned)(d.ntm * d.ntn * d.splits);
+    const int total = d.ntm * d.ntn * d.splits;
     if constexpr (A_KMAJ && !B_KMAJ) {
         if (d.rows) {
+            const unsigned grid = (unsigned)total;
             if (a.M <= 8) dense_rows_kernel<1><<<grid, 256, 0, s>>>(a, ACT);
             else if (a.M <= 16) dense_rows_kernel<2><<<grid, 256, 0, s>>>(a, ACT);
             else if (a.M <= 32) dense_rows_kernel<4><<<grid, 256, 0, s>>>(a, ACT);
@@ -676,10 +734,13 @@ static void dense_launch(const DensePlan& d, const DenseArgs& a, hipStream_t s) 
             return;
         }
     }
+    // persistent: one large or two small workgroups a compute unit, a multiple of 8
+    const int most = device_cus() * (d.big ? 1 : 2);
+    const unsigned grid = (unsigned)((std::min(total, most) + 7) / 8 * 8);
     if (d.big)
-        dense_gemm_kernel<256, 256, 2, 4, 2, A_KMAJ, B_KMAJ, ACT><<<grid, 512, 0, s>>>(a);
+        dense_gemm_kernel<256, 256, 2, 4, A_KMAJ, B_KMAJ, ACT><<<grid, 512, 0, s>>>(a);
     else
-        dense_gemm_kernel<128, 128, 2, 2, 2, A_KMAJ, B_KMAJ, ACT><<<grid, 256, 0, s>>>(a);
+        dense_gemm_kernel<128, 128, 2, 2, A_KMAJ, B_KMAJ, ACT><<<grid, 256, 0, s>>>(a);
 }
 
 template <bool A_KMAJ, bool B_KMAJ, int ACT>
