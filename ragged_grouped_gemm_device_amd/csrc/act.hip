@@ -131,19 +131,26 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(ActArgs p) {
     }
 }
 
-// dbias[c] = sum of the chunks' column sums, in a fixed order: 64 columns and 4
-// chunk lanes per workgroup.
+// dbias[c] = sum of the chunks' column sums, in a fixed order: 16 columns and 16
+// chunk lanes per workgroup, so that few columns still fill the chip.
 __global__ void __launch_bounds__(256) colsum_kernel(const float* __restrict__ part, int chunks, int N,
                                                      float* __restrict__ out) {
-    __shared__ float s_v[4][64];
-    const int cl = threadIdx.x & 63, l = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + cl;
+    __shared__ float s_v[16][17];
+    const int cl = threadIdx.x & 15, l = threadIdx.x >> 4;
+    const int c = blockIdx.x * 16 + cl;
     float v = 0.f;
-    if (c < N)
-        for (int k = l; k < chunks; k += 4) v += part[(int64_t)k * N + c];
+    if (c < N) {
+#pragma unroll 4
+        for (int k = l; k < chunks; k += 16) v += part[(int64_t)k * N + c];
+    }
     s_v[l][cl] = v;
     __syncthreads();
-    if (l == 0 && c < N) out[c] = (s_v[0][cl] + s_v[1][cl]) + (s_v[2][cl] + s_v[3][cl]);
+    if (l == 0 && c < N) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) t += s_v[k][cl];
+        out[c] = t;
+    }
 }
 
 // 16 codes a thread: 16 bytes in, 32 bytes out.
@@ -164,10 +171,10 @@ __global__ void __launch_bounds__(256) dequant_mxfp8_kernel(const uint8_t* __res
     }
 }
 
-// Row chunks of moe_act_bwd: about 2048 workgroups, at least 8 rows each.
+// Row chunks of moe_act_bwd: about 1024 workgroups, at least 8 rows each.
 static void act_chunks(int T, int N, bool gated, int& rows, int& chunks) {
     const int64_t tiles = ((gated ? N / 2 : N) / 8 + 31) / 32;
-    const int64_t r = ((int64_t)T * tiles + 2047) / 2048;
+    const int64_t r = ((int64_t)T * tiles + 1023) / 1024;
     rows = (int)std::max<int64_t>(8, (r + 7) / 8 * 8);
     chunks = (T + rows - 1) / rows;
 }
@@ -205,7 +212,7 @@ int launch_act_bwd(const uint16_t* dy, const uint16_t* z, const uint8_t* z_q, co
         default: go(std::integral_constant<int, 5>{}); break;
     }
     if (dbias && chunks > 1)
-        colsum_kernel<<<(unsigned)((N + 63) / 64), 256, 0, s>>>((const float*)ws, chunks, N, dbias);
+        colsum_kernel<<<(unsigned)((N + 15) / 16), 256, 0, s>>>((const float*)ws, chunks, N, dbias);
     return hipGetLastError() == hipSuccess ? 0 : -4;
 }
 

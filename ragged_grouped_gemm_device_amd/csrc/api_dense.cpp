@@ -56,9 +56,9 @@ extern "C" {
 
 size_t moe_linear_workspace_bytes(int T, int K, int N, int pass) {
     if (check_linear(T, K, N, MOE_ACT_NONE) != MOE_OK) return 0;
-    size_t fwd = moe::dense_part_bytes(T, N, K, true);
-    size_t bwd = std::max(moe::dense_part_bytes(T, K, N, false), moe::act_part_bytes(T, N));
-    bwd = std::max(bwd, up256((size_t)T * K * 2) + moe::dense_part_bytes(K, N, T, false));
+    size_t fwd = moe::dense_part_bytes(T, N, K);
+    size_t bwd = std::max(moe::dense_part_bytes(T, K, N), moe::act_part_bytes(T, N));
+    bwd = std::max(bwd, up256((size_t)T * K * 2) + moe::dense_part_bytes(K, N, T));
     return std::max(pass & MOE_LINEAR_FWD ? fwd : 0, pass & MOE_LINEAR_BWD ? bwd : 0);
 }
 
@@ -70,7 +70,7 @@ int moe_linear_fwd(const uint16_t* x, const uint16_t* w, const uint16_t* bias, c
     if (rc != MOE_OK) return rc;
     if (!x || !w || !y || !aligned({x, w, bias, residual, y, z, z_q})) return MOE_ERR_INVALID_ARG;
     if (act == MOE_ACT_NONE && (z || z_q)) return MOE_ERR_INVALID_ARG;
-    if (!has_space(workspace, workspace_bytes, moe::dense_part_bytes(T, N, K, true))) return MOE_ERR_WORKSPACE;
+    if (!has_space(workspace, workspace_bytes, moe::dense_part_bytes(T, N, K))) return MOE_ERR_WORKSPACE;
     return status(moe::launch_linear_fwd(x, w, bias, residual, T, K, N, act, y_f32, y, z, z_q, z_s, workspace,
                                          S(stream)));
 }
@@ -94,7 +94,7 @@ int moe_linear_dgrad(const uint16_t* dz, const uint16_t* w, const uint16_t* resi
     const int rc = check_linear(T, K, N, MOE_ACT_NONE);
     if (rc != MOE_OK) return rc;
     if (!dz || !w || !dx || !aligned({dz, w, residual, dx})) return MOE_ERR_INVALID_ARG;
-    if (!has_space(workspace, workspace_bytes, moe::dense_part_bytes(T, K, N, false))) return MOE_ERR_WORKSPACE;
+    if (!has_space(workspace, workspace_bytes, moe::dense_part_bytes(T, K, N))) return MOE_ERR_WORKSPACE;
     return status(moe::launch_linear_dgrad(dz, w, residual, T, K, N, dx, workspace, S(stream)));
 }
 
@@ -107,7 +107,7 @@ int moe_linear_wgrad(const uint16_t* x, const uint8_t* x_q, const uint8_t* x_s, 
     if (!x == !x_q || !dz || !dw || !aligned({x, x_q, dz, dw})) return MOE_ERR_INVALID_ARG;
     if (accumulate && !dw_f32) return MOE_ERR_UNSUPPORTED;
     const size_t copy = x_q ? up256((size_t)T * K * 2) : 0;
-    if (!has_space(workspace, workspace_bytes, copy + moe::dense_part_bytes(K, N, T, false))) return MOE_ERR_WORKSPACE;
+    if (!has_space(workspace, workspace_bytes, copy + moe::dense_part_bytes(K, N, T))) return MOE_ERR_WORKSPACE;
     if (x_q) {
         uint16_t* xb = (uint16_t*)workspace;
         rc = moe::launch_dequant_mxfp8(x_q, x_s, T, K, xb, S(stream));

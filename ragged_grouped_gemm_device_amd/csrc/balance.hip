@@ -103,8 +103,8 @@ __device__ __forceinline__ int expert_of(int gl, int i) {
     return V4 ? (i >> 2) * 4 * G + 4 * gl + (i & 3) : gl + G * i;
 }
 
-// One token's logits, PER a lane. Non-finite logits, experts past E and tokens
-// that are not live (on == false) count as -inf (probability 0), as in the router.
+// One token's logits, PER a lane; experts past E and tokens past the run (on ==
+// false) are -inf.
 template <int G, int PER, bool V4>
 __device__ __forceinline__ void token_load(const BalanceArgs& p, int t, int gl, bool on, float (&x)[PER]) {
     const float* row = p.logits + (int64_t)t * p.E;
@@ -125,14 +125,15 @@ __device__ __forceinline__ void token_load(const BalanceArgs& p, int t, int gl, 
     }
 }
 
-// x becomes exp(x - max); returns whether the token has a finite logit. The
-// hardware exponential's argument x log2(e) is rounded once: 2^-24 |x| relative.
+// x becomes exp(x - max); returns whether the token has a finite logit. Non-finite
+// logits, and all of a token that is not valid, count as -inf (probability 0), as in
+// the router. (`valid` only comes in here: the loads do not wait for it.) The hardware exponential's argument x log2(e) is rounded once: 2^-24 |x| relative.
 template <int G, int PER>
-__device__ __forceinline__ bool token_softmax(float (&x)[PER], float& inv, float& lse) {
+__device__ __forceinline__ bool token_softmax(float (&x)[PER], bool valid, float& inv, float& lse) {
     float mx = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        if (!isfinite(x[i])) x[i] = -INFINITY;
+        if (!valid || !isfinite(x[i])) x[i] = -INFINITY;
         mx = fmaxf(mx, x[i]);
     }
     mx = group_max<G>(mx);
@@ -253,8 +254,7 @@ __global__ void __launch_bounds__(256) balance_join_kernel(BalanceArgs p) {
 }
 __global__ void __launch_bounds__(256) balance_total_kernel(BalanceArgs p) { balance_total(p); }
 
-// A group of G lanes per token, PER logits a lane, two tokens' loads in flight. One
-// workgroup alone (small inputs) goes on to join and finish.
+// A group of G lanes per token, PER logits a lane. One workgroup alone (small inputs) goes on to join and finish.
 template <int G, int PER, bool V4>
 __global__ void __launch_bounds__(256) balance_chunk_kernel(BalanceArgs p) {
     __shared__ float s_p[4][G * PER];
@@ -275,9 +275,9 @@ __global__ void __launch_bounds__(256) balance_chunk_kernel(BalanceArgs p) {
         for (int i = 0; i < PER; ++i) acc[i] = 0.f;
         float z = 0.f;
         int n = 0;
-        auto take = [&](int t, float (&x)[PER]) {
+        auto take = [&](int t, bool valid, int first, float (&x)[PER]) {
             float inv, lse;
-            const bool some = token_softmax<G, PER>(x, inv, lse);
+            const bool some = token_softmax<G, PER>(x, valid, inv, lse);
 #pragma unroll
             for (int i = 0; i < PER; ++i) acc[i] += x[i] * inv;
             if (some) {
@@ -285,21 +285,31 @@ __global__ void __launch_bounds__(256) balance_chunk_kernel(BalanceArgs p) {
                     z += lse * lse;
                     ++n;
                 }
-                for (int j = gl; j < p.k; j += G) {
+                if (first >= 0 && first < p.E) atomicAdd(&s_cnt[first], 1);
+                for (int j = gl + G; j < p.k; j += G) {
                     const int e = p.topk_idx[(int64_t)t * p.k + j];
                     if (e >= 0 && e < p.E) atomicAdd(&s_cnt[e], 1);
                 }
             }
         };
-        for (int tb = a; tb < b; tb += 2 * NG) {
-            float x0[PER], x1[PER];
-            const int ta = tb + grp, tc = ta + NG;
-            const bool ona = ta < b && (!p.valid || p.valid[ta] != 0);
-            const bool onc = tc < b && (!p.valid || p.valid[tc] != 0);
-            token_load<G, PER, V4>(p, ona ? ta : a, gl, ona, x0);
-            token_load<G, PER, V4>(p, onc ? tc : a, gl, onc, x1);
-            take(ta, x0);
-            take(tc, x1);
+        // the loads of a group's next token are on their way while one is worked on
+        struct Token {
+            float x[PER];
+            int first;
+            bool valid;
+        } u, v;
+        auto fetch = [&](int t, Token& k) {
+            const bool on = t < b;
+            token_load<G, PER, V4>(p, on ? t : a, gl, on, k.x);
+            k.first = on && gl < p.k ? p.topk_idx[(int64_t)t * p.k + gl] : -1;
+            k.valid = !p.valid || (on && p.valid[t] != 0);
+        };
+        fetch(a + grp, u);
+        for (int t = a + grp; t - grp < b; t += 2 * NG) {
+            fetch(t + NG, v);
+            take(t, u.valid, u.first, u.x);
+            fetch(t + 2 * NG, u);
+            take(t + NG, v.valid, v.first, v.x);
         }
         // over the wavefront's groups, then its 4 wavefronts
 #pragma unroll
@@ -358,9 +368,9 @@ __global__ void __launch_bounds__(256) balance_bwd_kernel(BalanceArgs p) {
             const int e = expert_of<G, V4>(gl, i);
             f[i] = s >= 0 && e < p.E ? (float)p.counts[(int64_t)s * p.E + e] * fs : 0.f;
         }
-        auto give = [&](int t, float (&x)[PER]) {
+        auto give = [&](int t, bool valid, float (&x)[PER]) {
             float inv, lse;
-            token_softmax<G, PER>(x, inv, lse);
+            token_softmax<G, PER>(x, valid, inv, lse);
             float ref = -INFINITY;  // x = exp(logit - max) is 1 at the largest logit
 #pragma unroll
             for (int i = 0; i < PER; ++i)
@@ -406,15 +416,19 @@ __global__ void __launch_bounds__(256) balance_bwd_kernel(BalanceArgs p) {
                 }
             }
         };
-        for (int tb = a; tb < b; tb += 2 * NG) {
-            float x0[PER], x1[PER];
-            const int ta = tb + grp, tc = ta + NG;
-            const bool ona = s >= 0 && ta < b && (!p.valid || p.valid[ta] != 0);
-            const bool onc = s >= 0 && tc < b && (!p.valid || p.valid[tc] != 0);
-            token_load<G, PER, V4>(p, ona ? ta : a, gl, ona, x0);
-            token_load<G, PER, V4>(p, onc ? tc : a, gl, onc, x1);
-            give(ta, x0);
-            give(tc, x1);
+        float u[PER], v[PER];
+        bool uv, vv;
+        auto fetch = [&](int t, float (&x)[PER], bool& valid) {
+            const bool on = s >= 0 && t < b;
+            token_load<G, PER, V4>(p, on ? t : a, gl, on, x);
+            valid = !p.valid || (on && p.valid[t] != 0);
+        };
+        fetch(a + grp, u, uv);
+        for (int t = a + grp; t - grp < b; t += 2 * NG) {
+            fetch(t + NG, v, vv);
+            give(t, uv, u);
+            fetch(t + 2 * NG, u, uv);
+            give(t + NG, vv, v);
         }
     });
 }
@@ -436,11 +450,11 @@ static BalanceShape balance_shape(int E) {
 }
 
 // Tokens per chunk: all of them where one workgroup passes over them in a few steps
-// (no further launch then), else about 2048 workgroups of whole steps.
+// (no further launch then), else about 1024 workgroups of whole steps.
 static int balance_chunk(int T, int E) {
     const int step = 2 * 256 / balance_shape(E).G;
     if (T <= 4 * step) return 4 * step;
-    const int ct = (T + 2047) / 2048;
+    const int ct = (T + 1023) / 1024;
     return (ct + step - 1) / step * step;
 }
 

@@ -541,48 +541,84 @@ __global__ void __launch_bounds__(256) dense_join_kernel(DenseArgs p) {
     if (on) dense_finish8<ACT>(p, m, g, v);
 }
 
-// ------------------------------------------------------------------ few rows
-// Up to 64 rows (single tokens, decode batches): the product reads W once and does
-// little else. A workgroup owns 64 columns (32 gate and 32 up columns of a gated
-// layer) and a range of K; its 4 wavefronts take every fourth 64-deep slab of it,
-// each through LDS stages of its own, so the loop has no barrier: a wavefront waits
-// only for its own copies, ST - 1 slabs ahead of the one it multiplies. x comes in
-// the same way (XC copies of 8 rows). The wavefronts' sums
-// meet in LDS. [T = 1, K = 8192, N = 4096: bound by the read of W.]
-template <int XC>
-__global__ void __launch_bounds__(256, 1) dense_rows_kernel(DenseArgs p, int act) {
-    constexpr int MT = XC > 4 ? 2 : 1;
+// ------------------------------------------------------------------ small products
+// Few output tiles (single tokens, decode batches, small layers): here a product is
+// the time to read its operands, W above all, and the latency of its K loop. A
+// workgroup owns 64 columns (32 gate and 32 up columns of a gated layer), up to 64
+// rows and a range of K; its 4 wavefronts take every fourth 64-deep slab of it, each
+// through LDS stages of its own, so the loop has no barrier: a wavefront waits only
+// for its own copies, ST - 1 slabs ahead of the one it multiplies. XC copies of 8
+// rows (8 XC rows a tile) bring a K-major A, 8 copies an A with K outermost and B.
+// The wavefronts' sums meet in LDS. A compute unit copies about 55 B a clock into
+// LDS, so tiles this small reach 40% of the matrix rate at most, and larger products
+// take the kernel above. [T = 1, K = 8192, N = 4096: 13.3 us, 5.0 TB/s of W; as 128 x
+// 128 tiles 14.0 us and a join of 11.5 us over 16 splits.]
+template <bool A_KMAJ, bool B_KMAJ, int XC>
+__global__ void __launch_bounds__(256, 1) dense_small_kernel(DenseArgs p, int act) {
+    static_assert(A_KMAJ || XC == 8, "an A with K outermost comes 64 columns at a time");
+    constexpr int MT = XC > 4 ? 2 : 1, ROWS = 8 * XC;
     constexpr int ST = XC == 1 ? 4 : XC <= 4 ? 3 : 2;
     constexpr int WB = 64 * 128, STAGE = WB + XC * 1024, CP = 8 + XC;
     __shared__ __attribute__((aligned(1024))) uint8_t s_ab[4 * ST * STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int split = __builtin_amdgcn_readfirstlane(blockIdx.x / p.ntn);
-    const int n0 = __builtin_amdgcn_readfirstlane((blockIdx.x - split * p.ntn) * 64);
+    const int per = p.ntm * p.ntn;
+    const int split = __builtin_amdgcn_readfirstlane(blockIdx.x / per);
+    const int t = blockIdx.x - split * per;
+    const int m0 = __builtin_amdgcn_readfirstlane(t / p.ntn * ROWS);
+    const int n0 = __builtin_amdgcn_readfirstlane(t % p.ntn * 64);
     const int slabs = (p.K + DBK - 1) / DBK;
     const int ks0 = split * p.split_slabs;
     const int nk = min(p.split_slabs, slabs - ks0);
     const int mine = nk > wave ? (nk - wave + 3) / 4 : 0;  // this wavefront's slabs: ks0 + wave + 4 j
 
-    const int kr = lane >> 3;  // W: k row of copy 0, 8 rows a copy; x: row of copy 0
-    const int wcol = n0 + ((lane & 7) ^ (((kr >> 1) & 1) << 2)) * 8;
-    const uint32_t w_off = wcol < p.N ? (uint32_t)((kr * p.ldb + wcol) * 2) : kMasked;
-    const uint32_t w_istep = (uint32_t)(8 * p.ldb * 2);
+    // copy i of a slab: 8 slab rows of 128 bytes, 8 lanes each; row kr + 8 i, chunk c
+    const int kr = lane >> 3;
+    const int kc = (lane & 7) ^ (((kr >> 1) & 1) << 2);  // K outermost: chunk, the same for every i
+    const int a_col = m0 + kc * 8, b_col = n0 + kc * 8;
     const uint8_t* mem = s_ab + wave * ST * STAGE;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS char*)mem;
-    const int64_t w_bytes = (int64_t)p.K * p.ldb * 2, x_bytes = (int64_t)p.M * p.lda * 2;
+    const int64_t a_step = A_KMAJ ? DBK * 2 : (int64_t)DBK * p.lda * 2;
+    const int64_t b_step = B_KMAJ ? DBK * 2 : (int64_t)DBK * p.ldb * 2;
+    const char* a_base = (const char*)(A_KMAJ ? p.A + (int64_t)m0 * p.lda : p.A);
+    const char* b_base = (const char*)(B_KMAJ ? p.B + (int64_t)n0 * p.ldb : p.B);
+    const int64_t a_bytes = (int64_t)(A_KMAJ ? p.M - m0 : p.K) * p.lda * 2;
+    const int64_t b_bytes = (int64_t)(B_KMAJ ? p.N - n0 : p.K) * p.ldb * 2;
     auto issue = [&](int j, int st) {
         const int ks = ks0 + wave + 4 * j;
-        const i32x4_t rw = rsrc_from(p.B, w_bytes, (int64_t)ks * DBK * p.ldb * 2);
-        const i32x4_t rx = rsrc_from(p.A, x_bytes, (int64_t)ks * DBK * 2);
+        const i32x4_t rb = rsrc_from(b_base, b_bytes, ks * b_step);
+        const i32x4_t ra = rsrc_from(a_base, a_bytes, ks * a_step);
         const uint32_t l0 = lds0 + st * STAGE;
         const int left = p.K - ks * DBK;
+        // K-major: rows past the matrix end read past the resource (zeros), chunks past K are masked
+        auto offset = [&](int i, bool kmaj, int64_t ld, int col, int cols) -> uint32_t {
+            const int r = kr + 8 * i;
+            if (kmaj) {
+                const int c = ((lane & 7) ^ kmaj_swz(r)) * 8;
+                return c < left ? (uint32_t)((r * ld + c) * 2) : kMasked;
+            }
+            return col < cols ? (uint32_t)((r * ld + col) * 2) : kMasked;
+        };
 #pragma unroll
-        for (int i = 0; i < 8; ++i) lds_copy16(rw, l0 + i * 1024, w_off + i * w_istep);
+        for (int i = 0; i < 8; ++i) lds_copy16(rb, l0 + i * 1024, offset(i, B_KMAJ, p.ldb, b_col, p.N));
 #pragma unroll
-        for (int i = 0; i < XC; ++i) {
-            const int r = kr + 8 * i, c = ((lane & 7) ^ kmaj_swz(r)) * 8;
-            lds_copy16(rx, l0 + WB + i * 1024, r < p.M && c < left ? (uint32_t)((r * p.lda + c) * 2) : kMasked);
+        for (int i = 0; i < XC; ++i) lds_copy16(ra, l0 + WB + i * 1024, offset(i, A_KMAJ, p.lda, a_col, p.M));
+    };
+    // MFMA operand: index base + (lane & 31), k = 16 ks + 8 (lane >> 5) + [0, 8)
+    auto frag = [&](const uint8_t* s, auto KM, int rows, int base, int ks) -> bf16x8_t {
+        if constexpr (decltype(KM)::value) {
+            // rows past the copied ones repeat them: their products are never stored
+            const int r = (base + (lane & 31)) & (rows - 1);
+            return __builtin_bit_cast(bf16x8_t, *(const uint4*)(s + kmaj_byte(r, 2 * ks + (lane >> 5))));
+        } else {
+            const int lg = lane & 15;
+            const int c = base + 16 * ((lane >> 4) & 1) + 4 * (lg & 3);
+            const int k0 = 16 * ks + 8 * (lane >> 5) + (lg >> 2), k1 = k0 + 4;
+            const int o0 = k0 * 128 + (((c >> 3) ^ (((k0 >> 1) & 1) << 2)) << 4) + (c & 7) * 2;
+            const int o1 = k1 * 128 + (((c >> 3) ^ (((k1 >> 1) & 1) << 2)) << 4) + (c & 7) * 2;
+            const bf16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4_t*)(s + o0));
+            const bf16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4_t*)(s + o1));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     };
     f32x16_t acc[MT][2];
@@ -602,22 +638,9 @@ __global__ void __launch_bounds__(256, 1) dense_rows_kernel(DenseArgs p, int act
             constexpr int ks = KS;
             bf16x8_t fx[MT], fw[2];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                // rows past the 8 XC copied ones repeat them: their products are never stored
-                const int r = (32 * i + (lane & 31)) & (8 * XC - 1);
-                fx[i] = __builtin_bit_cast(bf16x8_t, *(const uint4*)(s + WB + kmaj_byte(r, 2 * ks + (lane >> 5))));
-            }
+            for (int i = 0; i < MT; ++i) fx[i] = frag(s + WB, std::bool_constant<A_KMAJ>{}, ROWS, 32 * i, ks);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int lg = lane & 15;
-                const int c = 32 * u + 16 * ((lane >> 4) & 1) + 4 * (lg & 3);
-                const int k0 = 16 * ks + 8 * (lane >> 5) + (lg >> 2), k1 = k0 + 4;
-                const int o0 = k0 * 128 + (((c >> 3) ^ (((k0 >> 1) & 1) << 2)) << 4) + (c & 7) * 2;
-                const int o1 = k1 * 128 + (((c >> 3) ^ (((k1 >> 1) & 1) << 2)) << 4) + (c & 7) * 2;
-                const bf16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4_t*)(s + o0));
-                const bf16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4_t*)(s + o1));
-                fw[u] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-            }
+            for (int u = 0; u < 2; ++u) fw[u] = frag(s, std::bool_constant<B_KMAJ>{}, 64, 32 * u, ks);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -654,7 +677,7 @@ __global__ void __launch_bounds__(256, 1) dense_rows_kernel(DenseArgs p, int act
         float v[2][8];
         if (act > 1 || p.part) {
             const int row = tid >> 3, c8 = tid & 7, col = n0 + 8 * c8;
-            const int64_t m = 32 * I + row;
+            const int64_t m = m0 + 32 * I + row;
             sum8(row, c8, v[0]);
             if (m < p.M && col < p.N) {
                 if (p.part) {
@@ -668,7 +691,7 @@ __global__ void __launch_bounds__(256, 1) dense_rows_kernel(DenseArgs p, int act
             }
         } else if (tid < 128) {
             const int row = tid >> 2, c8 = tid & 3;
-            const int64_t m = 32 * I + row;
+            const int64_t m = m0 + 32 * I + row;
             sum8(row, c8, v[0]);
             sum8(row, c8 + 4, v[1]);
             if (m < p.M) {
@@ -680,59 +703,75 @@ __global__ void __launch_bounds__(256, 1) dense_rows_kernel(DenseArgs p, int act
 }
 
 // ------------------------------------------------------------------ host side
-// Tile and split of a product. Large tiles read each operand fewer times and run
-// the MFMAs with fewer LDS reads, but only pay when they fill the chip; otherwise
-// 128 x 128 tiles (two workgroups a compute unit), with K cut into pieces while
-// fewer than two workgroups a compute unit would run and a piece keeps 4 slabs.
+// Tile and split of a product: the cheapest by a model of the time (us) fitted to
+// measured products between 16 x 704 x 704 and 16384 x 512 x 512 (it picks the
+// fastest of 11 candidates there, or one within about 10%):
+//   64 x 64 tiles (small kernel): a round over the compute units takes 2.2, plus 0.9 for
+//     every slab of a wavefront (a quarter of the split's slabs), 0.55 with at most 32 rows;
+//   128 x 128 tiles: 0.72 a slab for one on a compute unit, 0.95 for two side by side, and
+//     2.5 for the prologue and epilogue;
+//   256 x 256 tiles: 1.05 a slab with few of them at work up to 1.7 with all (clock and
+//     L2), and 7 for the prologue and epilogue;
+//   any: no less than 1.0 and the operands' read, at 5.2 TB/s with every compute unit at
+//     work down to 2.6 with few;
+//   splits: 1.8 for the joining launch and the partial sums' write and read at 10 TB/s
+//     (they mostly stay in the last-level cache).
+// E.g. 1000 x 2880 x 2880: 64 x 64 tiles 50.8 us, 128 x 128 37.0, in two splits 30.4,
+// 256 x 256 57.0; 8192 x 512 x 512: 20.4, 9.4, 24.7, 15.9.
 struct DensePlan {
-    bool rows, big;
+    bool small, big;
     int ntm, ntn, splits, split_slabs;
 };
 constexpr int kDenseCus = 256;
 
-static DensePlan dense_plan(int64_t M, int64_t N, int64_t K, bool forward) {
-    DensePlan d{};
-    if (forward && M <= 64) {
-        const int64_t slabs = (K + DBK - 1) / DBK;
-        d.rows = true;
-        d.ntm = 1;
-        d.ntn = (int)((N + 63) / 64);
-        const int64_t s = std::max<int64_t>(1, std::min<int64_t>(kDenseCus / d.ntn, slabs / 4));
-        d.split_slabs = (int)((slabs + s - 1) / s);
-        d.splits = (int)((slabs + d.split_slabs - 1) / d.split_slabs);
-        return d;
-    }
-    const int64_t tb = ((M + 255) / 256) * ((N + 255) / 256);
+static DensePlan dense_plan(int64_t M, int64_t N, int64_t K) {
     const int64_t slabs = (K + DBK - 1) / DBK;
-    d.big = tb >= kDenseCus * 3 / 4;
-    const int64_t e = d.big ? 256 : 128;
-    d.ntm = (int)((M + e - 1) / e);
-    d.ntn = (int)((N + e - 1) / e);
-    int64_t s = 1;
-    const int64_t tiles = (int64_t)d.ntm * d.ntn;
-    if (!d.big) s = std::max<int64_t>(1, std::min<int64_t>(2 * kDenseCus / tiles, slabs / 4));
-    d.split_slabs = (int)((slabs + s - 1) / s);
-    d.splits = (int)((slabs + d.split_slabs - 1) / d.split_slabs);
-    return d;
+    DensePlan best{};
+    double least = 0;
+    for (int kind = 0; kind < 3; ++kind) {
+        const int64_t e = 64 << kind;
+        const int64_t ntm = (M + e - 1) / e, ntn = (N + e - 1) / e;
+        for (int64_t want = 1; want <= 16 && want <= slabs; want *= 2) {
+            const int64_t ss = (slabs + want - 1) / want, s = (slabs + ss - 1) / ss;
+            const int64_t tiles = ntm * ntn * s, rounds = (tiles + kDenseCus - 1) / kDenseCus;
+            double t;
+            if (kind == 0)
+                t = (double)rounds * (2.2 + (M <= 32 ? 0.55 : 0.9) * (double)((ss + 3) / 4));
+            else if (kind == 1)
+                t = (double)ss * ((double)(rounds / 2) * 0.95 + (double)(rounds % 2) * 0.72) + 2.5 * (double)((rounds + 1) / 2);
+            else
+                {
+                const double fill = std::min(1.0, (double)tiles / kDenseCus);
+                t = (double)rounds * ((double)ss * (1.05 + 0.65 * fill * fill) + 7.0);
+            }
+            const double busy = 0.5 + 0.5 * std::min(1.0, (double)tiles / kDenseCus);
+            t = std::max(t, 1.0 + (double)(M + N) * (double)K * 2.0 / (5.2e6 * busy));
+            if (s > 1) t += 1.8 + (double)s * (double)M * (double)N * 8.0 / 10e6;
+            if (best.splits && t >= least) continue;
+            least = t;
+            best.small = kind == 0, best.big = kind == 2;
+            best.ntm = (int)ntm, best.ntn = (int)ntn, best.splits = (int)s, best.split_slabs = (int)ss;
+        }
+    }
+    return best;
 }
 
-size_t dense_part_bytes(int64_t M, int64_t N, int64_t K, bool forward) {
-    const DensePlan d = dense_plan(M, N, K, forward);
+size_t dense_part_bytes(int64_t M, int64_t N, int64_t K) {
+    const DensePlan d = dense_plan(M, N, K);
     return d.splits > 1 ? (size_t)d.splits * M * N * sizeof(float) : 0;
 }
 
 template <bool A_KMAJ, bool B_KMAJ, int ACT>
 static void dense_launch(const DensePlan& d, const DenseArgs& a, hipStream_t s) {
     const int total = d.ntm * d.ntn * d.splits;
-    if constexpr (A_KMAJ && !B_KMAJ) {
-        if (d.rows) {
-            const unsigned grid = (unsigned)total;
-            if (a.M <= 8) dense_rows_kernel<1><<<grid, 256, 0, s>>>(a, ACT);
-            else if (a.M <= 16) dense_rows_kernel<2><<<grid, 256, 0, s>>>(a, ACT);
-            else if (a.M <= 32) dense_rows_kernel<4><<<grid, 256, 0, s>>>(a, ACT);
-            else dense_rows_kernel<8><<<grid, 256, 0, s>>>(a, ACT);
-            return;
+    if (d.small) {
+        const unsigned grid = (unsigned)total;
+        if constexpr (A_KMAJ) {
+            if (a.M <= 8) return dense_small_kernel<true, B_KMAJ, 1><<<grid, 256, 0, s>>>(a, ACT);
+            if (a.M <= 16) return dense_small_kernel<true, B_KMAJ, 2><<<grid, 256, 0, s>>>(a, ACT);
+            if (a.M <= 32) return dense_small_kernel<true, B_KMAJ, 4><<<grid, 256, 0, s>>>(a, ACT);
         }
+        return dense_small_kernel<A_KMAJ, B_KMAJ, 8><<<grid, 256, 0, s>>>(a, ACT);
     }
     // persistent: one large or two small workgroups a compute unit, a multiple of 8
     const int most = device_cus() * (d.big ? 1 : 2);
@@ -745,7 +784,7 @@ static void dense_launch(const DensePlan& d, const DenseArgs& a, hipStream_t s) 
 
 template <bool A_KMAJ, bool B_KMAJ, int ACT>
 static int dense_run(DenseArgs a, void* ws, hipStream_t s) {
-    const DensePlan d = dense_plan(a.M, a.N, a.K, A_KMAJ && !B_KMAJ);
+    const DensePlan d = dense_plan(a.M, a.N, a.K);
     a.ntm = d.ntm;
     a.ntn = d.ntn;
     a.splits = d.splits;
