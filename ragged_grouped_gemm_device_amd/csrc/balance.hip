@@ -42,6 +42,7 @@ struct BalanceArgs {
     int accumulate;
     float* dlogits;
     uint16_t* dlogits16;
+    int stream;  // dlogits past the caches
 };
 
 // first and past-the-end token of sequence s, kept inside [0, T]
@@ -398,7 +399,8 @@ __global__ void __launch_bounds__(256) balance_bwd_kernel(BalanceArgs p) {
                             const float4 o = *(const float4*)(p.dlogits + at);
                             d.x += o.x, d.y += o.y, d.z += o.z, d.w += o.w;
                         }
-                        *(float4*)(p.dlogits + at) = d;
+                        if (p.stream) st_nt16(p.dlogits + at, d);
+                        else *(float4*)(p.dlogits + at) = d;
                         if (p.dlogits16)
                             *(uint2*)(p.dlogits16 + at) = make_uint2(pack_bf16x2(d.x, d.y), pack_bf16x2(d.z, d.w));
                     }
@@ -522,6 +524,7 @@ int launch_balance_loss_bwd(const float* logits, const int32_t* counts, const in
     p.CT = (int)((((int64_t)T + 2047) / 2048 + step - 1) / step * step);
     p.counts = const_cast<int32_t*>(counts), p.tokens = const_cast<int32_t*>(tokens);
     p.cb = cb, p.cz = cz, p.grad = grad, p.accumulate = accumulate, p.dlogits = dlogits, p.dlogits16 = dlogits16;
+    p.stream = (int64_t)T * E * 4 >= kDenseStreamBytes;
     const int nchunks = (T + p.CT - 1) / p.CT;
     by_experts(E, on16(logits) && on16(dlogits) && ((uintptr_t)dlogits16 & 7) == 0, [&](auto G, auto PER, auto V4) {
         balance_bwd_kernel<decltype(G)::value, decltype(PER)::value, decltype(V4)::value><<<nchunks, 256, 0, s>>>(p);

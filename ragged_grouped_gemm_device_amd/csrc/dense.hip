@@ -40,7 +40,13 @@ struct DenseArgs {
     uint8_t* z_q;  // [M, N] codes, [M, N / 32] scales, or nullptr
     uint8_t* z_s;
     float* part;  // [splits, M, N] raw sums instead of an epilogue, or nullptr
+    int stream;   // outputs past the caches
 };
+
+__device__ __forceinline__ void dense_st16(bool stream, void* at, uint4 v) {
+    if (stream) st_nt16(at, v);
+    else *(uint4*)at = v;
+}
 
 template <int ACT>
 constexpr bool kGated = ACT == 0 || ACT == 1;
@@ -99,11 +105,12 @@ __device__ __forceinline__ void dense_store8(const DenseArgs& p, int64_t at, flo
             v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
             v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
         }
-        o[0] = make_float4(v[0], v[1], v[2], v[3]);
-        o[1] = make_float4(v[4], v[5], v[6], v[7]);
+        dense_st16(p.stream, o, __builtin_bit_cast(uint4, make_float4(v[0], v[1], v[2], v[3])));
+        dense_st16(p.stream, o + 1, __builtin_bit_cast(uint4, make_float4(v[4], v[5], v[6], v[7])));
     } else {
-        *(uint4*)((uint16_t*)p.out + at) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        dense_st16(p.stream, (uint16_t*)p.out + at,
+                   make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                              pack_bf16x2(v[6], v[7])));
     }
 }
 
@@ -189,7 +196,7 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& p, f32x16_t (&ac
                     const int R = 8 * It + (lane >> 3), c = lane & 7;
                     const uint4 v = *(const uint4*)(stg + R * 128 + ((c ^ ((R >> 1) & 7)) << 4));
                     const int m = mb + R, col = col0 + 8 * c;
-                    if (m < p.M && col < p.N) *(uint4*)(p.z + (int64_t)m * p.N + col) = v;
+                    if (m < p.M && col < p.N) dense_st16(p.stream, p.z + (int64_t)m * p.N + col, v);
                 });
                 wave_lds_sync();
             }
@@ -789,6 +796,7 @@ static int dense_run(DenseArgs a, void* ws, hipStream_t s) {
     a.ntn = d.ntn;
     a.splits = d.splits;
     a.split_slabs = d.split_slabs;
+    a.stream = (int64_t)a.M * a.N * (a.out_f32 ? 4 : 2) >= kDenseStreamBytes;
     if (d.splits == 1) {
         a.part = nullptr;
         dense_launch<A_KMAJ, B_KMAJ, ACT>(d, a, s);

@@ -109,6 +109,10 @@ int launch_permute_quant_mxfp8(const uint16_t* x, const int32_t* src_of, int k, 
                                int mode, uint8_t* q_row, uint8_t* s_row, uint8_t* q_col, uint8_t* s_col,
                                hipStream_t s);
 
+// Outputs of at least this size are stored past the caches by the streaming passes:
+// a quarter of the 256 MB last-level cache, so smaller ones stay there for their reader.
+constexpr int64_t kDenseStreamBytes = (int64_t)64 << 20;
+
 // Dense linear layer (act: the MOE_ACT_* codes; N: columns of W, 2n when gated)
 size_t dense_part_bytes(int64_t M, int64_t N, int64_t K);
 int launch_linear_fwd(const uint16_t* x, const uint16_t* w, const uint16_t* bias, const uint16_t* res, int T,
