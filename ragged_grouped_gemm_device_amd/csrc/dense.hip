@@ -721,8 +721,10 @@ __global__ void __launch_bounds__(256, 1) dense_small_kernel(DenseArgs p, int ac
 //     L2), and 7 for the prologue and epilogue;
 //   any: no less than 1.0 and the operands' read, at 5.2 TB/s with every compute unit at
 //     work down to 2.6 with few;
-//   splits: 1.8 for the joining launch and the partial sums' write and read at 10 TB/s
-//     (they mostly stay in the last-level cache).
+//   splits: 1.8 for the joining launch and the partial sums' write and read, 3.5 TB/s
+//     for the two together (they mostly stay in the last-level cache).
+// 256 x 128 and 128 x 256 tiles of eight 64 x 64 wavefront pieces were never the fastest
+// (4096 x 2048 x 7168 dgrad: 112.9 us against 107.0 as 128 x 128 tiles).
 // E.g. 1000 x 2880 x 2880: 64 x 64 tiles 50.8 us, 128 x 128 37.0, in two splits 30.4,
 // 256 x 256 57.0; 8192 x 512 x 512: 20.4, 9.4, 24.7, 15.9.
 struct DensePlan {
@@ -753,7 +755,7 @@ static DensePlan dense_plan(int64_t M, int64_t N, int64_t K) {
             }
             const double busy = 0.5 + 0.5 * std::min(1.0, (double)tiles / kDenseCus);
             t = std::max(t, 1.0 + (double)(M + N) * (double)K * 2.0 / (5.2e6 * busy));
-            if (s > 1) t += 1.8 + (double)s * (double)M * (double)N * 8.0 / 10e6;
+            if (s > 1) t += 1.8 + (double)s * (double)M * (double)N * 4.0 / 3.5e6;
             if (best.splits && t >= least) continue;
             least = t;
             best.small = kind == 0, best.big = kind == 2;
