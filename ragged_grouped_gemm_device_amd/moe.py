@@ -458,7 +458,10 @@ class Buffers:
     """Device buffers of one forward + backward pass (plain torch allocations)."""
 
     def __init__(self, T: int, k: int, E: int, d: int, n: int, device="cuda", mx: bool = False,
-                 gated: bool = True):
+                 gated: bool = True, ckpt8: bool = False, h=None):
+        """ckpt8: keep the FC1 output H between forward and backward as an 8-bit checkpoint (33
+        instead of 64 bytes for 32 values); H itself is then scratch, and layers run one after the
+        other may share one: pass it as h."""
         dev = torch.device(device)
         bf, i32, f32, u8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
         self.T, self.k, self.E, self.d, self.n = T, k, E, d, n
@@ -473,7 +476,11 @@ class Buffers:
         self.route_ws = torch.empty(max(16, moe_route_workspace_bytes(T, k, E)), dtype=u8, device=dev)
         self.x_perm = torch.empty(M, d, dtype=bf, device=dev)
         n1 = 2 * n if gated else n   # FC1 width (non-gated sReLU: n)
-        self.h = torch.empty(M, n1, dtype=bf, device=dev)
+        self.h = torch.empty(M, n1, dtype=bf, device=dev) if h is None else h
+        self.ckpt8 = ckpt8
+        if ckpt8:
+            self.h_q = torch.empty(M, n1, dtype=u8, device=dev)
+            self.h_s = torch.empty(M, n1 // MOE_MX_BLOCK, dtype=u8, device=dev)
         self.a = torch.empty(M, n, dtype=bf, device=dev)
         self.y = torch.empty(M, d, dtype=bf, device=dev)
         self.out = torch.empty(T, d, dtype=bf, device=dev)
@@ -561,14 +568,93 @@ class Buffers:
         return d
 
 
+class SharedExpert:
+    """The expert every token passes, beside the routed ones: out += f(x w1) w2, with w1 [d, 2n]
+    (gated; interleaved like the routed experts' W1) or [d, n], w2 [n, d]. Between forward and
+    backward it keeps z = x w1 as an 8-bit checkpoint (ckpt8) or as bf16; f(z) is recomputed. With
+    x8 it keeps an 8-bit checkpoint of x too, and the backward needs no x."""
+
+    def __init__(self, T: int, d: int, n: int, act: int = MOE_ACT_SWIGLU, ckpt8: bool = True, x8: bool = False,
+                 device="cuda"):
+        self.act, self.x8 = act, x8
+        n1 = 2 * n if act in _GATED else n
+        new = lambda *shape, t=_BF: torch.empty(*shape, dtype=t, device=device)  # noqa: E731
+        self.z = None if ckpt8 else new(T, n1)
+        self.z_q = new(T, n1, t=_U8) if ckpt8 else None
+        self.z_s = new(T, n1 // MOE_MX_BLOCK, t=_U8) if ckpt8 else None
+        self.x_q = new(T, d, t=_U8) if x8 else None
+        self.x_s = new(T, d // MOE_MX_BLOCK, t=_U8) if x8 else None
+        self.a, self.da, self.dz = new(T, n), new(T, n), new(T, n1)
+        self.dw1, self.dw2 = new(d, n1, t=_F32), new(n, d, t=_F32)
+        size = max(16, moe_linear_workspace_bytes(T, d, n1), moe_linear_workspace_bytes(T, n, d))
+        self.ws = new(size, t=_U8)
+
+    def forward(self, x, w1, w2, out):
+        """out += f(x w1) w2."""
+        moe_linear_fwd(x, w1, self.a, self.act, z=self.z, z_q=self.z_q, z_s=self.z_s, workspace=self.ws)
+        if self.x8:
+            moe_quant_mxfp8(x, MOE_QUANT_ROWWISE, self.x_q, self.x_s)
+        moe_linear_fwd(self.a, w2, out, residual=out, workspace=self.ws)
+
+    def backward(self, x, dout, w1, w2, dx):
+        """dw1, dw2, and dx += the gradient through the shared expert."""
+        moe_linear_dgrad(dout, w2, self.da, workspace=self.ws)
+        moe_act_bwd(self.da, self.dz, self.act, z=self.z, z_q=self.z_q, z_s=self.z_s, a=self.a)
+        moe_linear_wgrad(self.a, dout, self.dw2, workspace=self.ws)
+        moe_linear_dgrad(self.dz, w1, dx, residual=dx, workspace=self.ws)
+        moe_linear_wgrad(None if self.x8 else x, self.dz, self.dw1, x_q=self.x_q, x_s=self.x_s, workspace=self.ws)
+
+
+class Router:
+    """The router's projection logits = x wg (wg [d, E], E a multiple of 8) with the balance and z
+    losses of the routing: loss [total, balance, z], counts, prob and tokens after forward; dwg
+    after backward. Sequences and padding tokens: seq_offsets [S + 1] and valid [T], kept by
+    reference (set them before a forward)."""
+
+    def __init__(self, T: int, d: int, E: int, k: int, S: int = 1, balance_coef: float = 1e-2,
+                 z_coef: float = 1e-3, device="cuda"):
+        self.k, self.balance_coef, self.z_coef = k, balance_coef, z_coef
+        new = lambda *shape, t=_F32: torch.empty(*shape, dtype=t, device=device)  # noqa: E731
+        self.logits, self.dlogits16, self.dwg = new(T, E), new(T, E, t=_BF), new(d, E)
+        self.loss, self.counts, self.prob = new(3), new(S, E, t=_I32), new(S, E)
+        self.tokens = new(S + 2, t=_I32)
+        self.valid = self.seq_offsets = None
+        self.ws = new(max(16, moe_linear_workspace_bytes(T, d, E)), t=_U8)
+        self.loss_ws = new(moe_balance_workspace_bytes(T, E, S), t=_U8)
+
+    def project(self, x, wg):
+        moe_linear_fwd(x, wg, self.logits, workspace=self.ws)
+        return self.logits
+
+    def losses(self, topk_idx):
+        moe_balance_loss(self.logits, topk_idx, self.loss, self.counts, self.prob, self.tokens, self.loss_ws,
+                         self.balance_coef, self.z_coef, valid=self.valid, seq_offsets=self.seq_offsets)
+
+    def backward(self, x, wg, dlogits, dx, grad=None):
+        """dlogits += the losses' gradient (times grad, their upstream gradient); dwg; dx += the
+        gradient through the projection (both products take dlogits rounded to bf16)."""
+        moe_balance_loss_bwd(self.logits, self.counts, self.tokens, dlogits, self.k, self.balance_coef, self.z_coef,
+                             valid=self.valid, seq_offsets=self.seq_offsets, grad=grad, accumulate=True,
+                             dlogits_bf16=self.dlogits16)
+        moe_linear_dgrad(self.dlogits16, wg, dx, residual=dx, workspace=self.ws)
+        moe_linear_wgrad(x, self.dlogits16, self.dwg, workspace=self.ws)
+
+
 def forward(buf: Buffers, x, logits, w1, w2, renorm=False, fwd_stages=MOE_STAGES_FWD, store_h=True,
-            act=MOE_ACT_SWIGLU, gather=False, mx=False):
+            act=MOE_ACT_SWIGLU, gather=False, mx=False, router=None, shared=None):
     """route -> permute -> FC1+GLU -> FC2 -> combine (all enqueued, no sync). With gather, FC1
     reads the rows of x through src_of and no permuted copy is made. With mx (buffers made with
     mx=True, quantize_weights done), X_perm is quantized row-wise (FC1 operand) and column-wise
-    (FC1 wgrad operand) in one pass and both GEMMs run on MXFP8."""
+    (FC1 wgrad operand) in one pass and both GEMMs run on MXFP8. With buffers made with ckpt8, H
+    is kept as an 8-bit checkpoint. router = (Router, wg): the logits are x wg (logits is None),
+    and the router losses follow the routing. shared = (SharedExpert, w1, w2): the shared expert's
+    output is added to out."""
+    if router is not None:
+        logits = router[0].project(x, router[1])
     moe_route_counts(logits, buf.k, buf.topk_idx, buf.topk_w, buf.counts, buf.offsets, buf.row_of,
                      buf.src_of, buf.M_cap, buf.err, buf.route_ws, renorm)
+    if router is not None:
+        router[0].losses(buf.topk_idx)
     buf.xt_from_forward = bool(mx)
     if mx:
         if gather:
@@ -585,11 +671,16 @@ def forward(buf: Buffers, x, logits, w1, w2, renorm=False, fwd_stages=MOE_STAGES
         moe_permute(x, buf.row_of, buf.src_of, buf.offsets, buf.k, buf.E, buf.x_perm)
         moe_grouped_mlp_fwd(buf.x_perm, w1, w2, buf.offsets, buf.h if store_h else None, buf.a,
                             buf.y, fwd_stages, act=act)
+    if buf.ckpt8 and store_h and (fwd_stages & MOE_STAGE_FC1):
+        moe_quant_mxfp8(buf.h, MOE_QUANT_ROWWISE, buf.h_q, buf.h_s)
     moe_combine(buf.y, buf.row_of, buf.topk_w, buf.k, buf.out)
+    if shared is not None:
+        shared[0].forward(x, *shared[1:], buf.out)
 
 
 def backward(buf: Buffers, dout, w1, w2, stages=MOE_STAGES_BWD, act=MOE_ACT_SWIGLU, logits=None,
-             renorm=False, x=None, mx=False, dgrad2_mx=True, mx_bf16_copies=True):
+             renorm=False, x=None, mx=False, dgrad2_mx=True, mx_bf16_copies=True, router=None, shared=None,
+             x_tokens=None):
     """gather dO -> dgrad2+dGLU (+dS) -> wgrad2 -> dgrad1 -> unpermute-sum -> wgrad1, and with
     the forward's logits also the router backward dS -> dlogits. With x given (the un-permuted
     input), the GEMMs read x and dO through src_of instead of permuted copies. With mx (buffers
@@ -598,7 +689,11 @@ def backward(buf: Buffers, dout, w1, w2, stages=MOE_STAGES_BWD, act=MOE_ACT_SWIG
     already did, and the GEMMs run on MXFP8 (the FC2 dgrad only with dgrad2_mx). With mx and
     mx_bf16_copies=False the FC2 dgrad writes only the MXFP8 copies of dH and A' (buf.dh and
     buf.a_w are left untouched), which is all the later MXFP8 stages read. The FC1 wgrad runs
-    last, after the unpermute-sum has read dX_perm."""
+    last, after the unpermute-sum has read dX_perm. router and shared as in forward (x_tokens:
+    the layer's input x [T, d] for their weight gradients, unless x is given or they keep an 8-bit
+    checkpoint of it): their gradients are added to dx."""
+    if buf.ckpt8 and (stages & MOE_STAGE_DGRAD2):
+        moe_dequant_mxfp8(buf.h_q, buf.h_s, buf.h)
     early, late = stages & ~MOE_STAGE_WGRAD1, stages & MOE_STAGE_WGRAD1
     if mx:
         if x is not None:
@@ -629,5 +724,12 @@ def backward(buf: Buffers, dout, w1, w2, stages=MOE_STAGES_BWD, act=MOE_ACT_SWIG
     moe_combine(buf.dx_perm, buf.row_of, None, buf.k, buf.dx)
     if late:
         bwd(late)
+    x_in = x if x is not None else x_tokens
+    if shared is not None:
+        shared[0].backward(x_in, dout, *shared[1:], buf.dx)
+    if router is not None:
+        logits = router[0].logits
     if logits is not None:
         moe_route_bwd(logits, buf.topk_idx, buf.ds, buf.dlogits, renorm)
+    if router is not None:
+        router[0].backward(x_in, router[1], buf.dlogits, buf.dx)
