@@ -13,18 +13,6 @@
 
 namespace moe {
 
-// 2^(s - 127); code 0 is the subnormal 2^-127, code 255 NaN
-__device__ __forceinline__ float e8m0_value(uint32_t s) {
-    return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7fc00000u : s << 23);
-}
-
-// 4 E4M3 codes (low byte first) times a scale
-__device__ __forceinline__ void e4m3x4_value(uint32_t w, float sc, float* v) {
-    const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
-    const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
-    v[0] = a.x * sc, v[1] = a.y * sc, v[2] = b.x * sc, v[3] = b.y * sc;
-}
-
 struct ActArgs {
     const uint16_t* dy;  // [T, NO], or nullptr: only a
     const uint16_t* z;   // [T, N], or nullptr: z_q, z_s

@@ -24,8 +24,6 @@ bool aligned(std::initializer_list<const void*> ps) {
 
 bool gated(int act) { return act == MOE_ACT_SWIGLU || act == MOE_ACT_GEGLU; }
 
-size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-
 int check_linear(int T, int K, int N, int act) {
     if (T <= 0 || K <= 0 || N <= 0) return MOE_ERR_INVALID_ARG;
     if (act < MOE_ACT_SWIGLU || act > MOE_ACT_GELU) return MOE_ERR_UNSUPPORTED;
@@ -56,9 +54,9 @@ extern "C" {
 
 size_t moe_linear_workspace_bytes(int T, int K, int N, int pass) {
     if (check_linear(T, K, N, MOE_ACT_NONE) != MOE_OK) return 0;
-    size_t fwd = moe::dense_part_bytes(T, N, K);
-    size_t bwd = std::max(moe::dense_part_bytes(T, K, N), moe::act_part_bytes(T, N));
-    bwd = std::max(bwd, up256((size_t)T * K * 2) + moe::dense_part_bytes(K, N, T));
+    const size_t fwd = moe::dense_part_bytes(T, N, K);
+    const size_t bwd = std::max({moe::dense_part_bytes(T, K, N), moe::linear_wgrad_bytes(T, K, N, true),
+                                 moe::act_part_bytes(T, N)});
     return std::max(pass & MOE_LINEAR_FWD ? fwd : 0, pass & MOE_LINEAR_BWD ? bwd : 0);
 }
 
@@ -106,16 +104,9 @@ int moe_linear_wgrad(const uint16_t* x, const uint8_t* x_q, const uint8_t* x_s, 
     if (rc != MOE_OK) return rc;
     if (!x == !x_q || !dz || !dw || !aligned({x, x_q, dz, dw})) return MOE_ERR_INVALID_ARG;
     if (accumulate && !dw_f32) return MOE_ERR_UNSUPPORTED;
-    const size_t copy = x_q ? up256((size_t)T * K * 2) : 0;
-    if (!has_space(workspace, workspace_bytes, copy + moe::dense_part_bytes(K, N, T))) return MOE_ERR_WORKSPACE;
-    if (x_q) {
-        uint16_t* xb = (uint16_t*)workspace;
-        rc = moe::launch_dequant_mxfp8(x_q, x_s, T, K, xb, S(stream));
-        if (rc) return MOE_ERR_LAUNCH;
-        x = xb;
-    }
-    return status(moe::launch_linear_wgrad(x, dz, T, K, N, dw_f32, accumulate, dw, (char*)workspace + copy,
-                                           S(stream)));
+    if (!has_space(workspace, workspace_bytes, moe::linear_wgrad_bytes(T, K, N, x_q != nullptr)))
+        return MOE_ERR_WORKSPACE;
+    return status(moe::launch_linear_wgrad(x, x_q, x_s, dz, T, K, N, dw_f32, accumulate, dw, workspace, S(stream)));
 }
 
 int moe_dequant_mxfp8(const uint8_t* q, const uint8_t* s, int64_t R, int C, uint16_t* out, moe_stream_t stream) {

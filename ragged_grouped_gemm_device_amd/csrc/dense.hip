@@ -27,6 +27,8 @@ constexpr int DBK = 64;  // K elements per slab (128 bytes)
 struct DenseArgs {
     const uint16_t* A;
     int64_t lda;
+    const uint8_t* a_q;  // A as an 8-bit checkpoint instead: codes [K, M], scales [K, M / 32]
+    const uint8_t* a_s;
     const uint16_t* B;
     int64_t ldb;
     int M, N, K;  // rows and columns of the product, reduction length
@@ -112,6 +114,33 @@ __device__ __forceinline__ void dense_store8(const DenseArgs& p, int64_t at, flo
                    make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                               pack_bf16x2(v[6], v[7])));
     }
+}
+
+// 16 columns of an 8-bit checkpoint's row on their way into an LDS slab: codes and
+// scale in registers, then two 16-byte pieces of bf16 (exact: 4 significant bits).
+struct Codes16 {
+    uint4 q;
+    uint32_t s;
+};
+__device__ __forceinline__ Codes16 codes16_load(const DenseArgs& p, int64_t row, int col) {
+    Codes16 c{make_uint4(0, 0, 0, 0), 127};
+    if (row < p.K && col < p.M) {
+        c.q = *(const uint4*)(p.a_q + row * p.lda + col);
+        c.s = p.a_s[row * (p.lda / 32) + col / 32];
+    }
+    return c;
+}
+__device__ __forceinline__ void codes16_store(const Codes16& c, uint8_t* lo, uint8_t* hi) {
+    const float sc = e8m0_value(c.s);
+    float v[16];
+    e4m3x4_value(c.q.x, sc, v);
+    e4m3x4_value(c.q.y, sc, v + 4);
+    e4m3x4_value(c.q.z, sc, v + 8);
+    e4m3x4_value(c.q.w, sc, v + 12);
+    *(uint4*)lo = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                             pack_bf16x2(v[6], v[7]));
+    *(uint4*)hi = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
+                             pack_bf16x2(v[14], v[15]));
 }
 
 // Wait until at most N vector-memory operations are in flight and every LDS
@@ -560,7 +589,7 @@ __global__ void __launch_bounds__(256) dense_join_kernel(DenseArgs p) {
 // LDS, so tiles this small reach 40% of the matrix rate at most, and larger products
 // take the kernel above. [T = 1, K = 8192, N = 4096: 13.3 us, 5.0 TB/s of W; as 128 x
 // 128 tiles 14.0 us and a join of 11.5 us over 16 splits.]
-template <bool A_KMAJ, bool B_KMAJ, int XC>
+template <bool A_KMAJ, bool B_KMAJ, int XC, bool A8>
 __global__ void __launch_bounds__(256, 1) dense_small_kernel(DenseArgs p, int act) {
     static_assert(A_KMAJ || XC == 8, "an A with K outermost comes 64 columns at a time");
     constexpr int MT = XC > 4 ? 2 : 1, ROWS = 8 * XC;
@@ -608,8 +637,26 @@ __global__ void __launch_bounds__(256, 1) dense_small_kernel(DenseArgs p, int ac
         };
 #pragma unroll
         for (int i = 0; i < 8; ++i) lds_copy16(rb, l0 + i * 1024, offset(i, B_KMAJ, p.ldb, b_col, p.N));
+        if constexpr (!A8) {
 #pragma unroll
-        for (int i = 0; i < XC; ++i) lds_copy16(ra, l0 + WB + i * 1024, offset(i, A_KMAJ, p.lda, a_col, p.M));
+            for (int i = 0; i < XC; ++i) lds_copy16(ra, l0 + WB + i * 1024, offset(i, A_KMAJ, p.lda, a_col, p.M));
+        }
+    };
+    // A from an 8-bit checkpoint: 4 pieces of 16 columns a lane, fetched a slab ahead
+    static_assert(!A8 || (!A_KMAJ && ST == 2), "K outermost, one slab ahead");
+    Codes16 codes[A8 ? 4 : 1];
+    auto fetch_a8 = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            codes[A8 ? i : 0] = codes16_load(p, (int64_t)(ks0 + wave + 4 * j) * DBK + 16 * i + (lane >> 2), m0 + (lane & 3) * 16);
+    };
+    auto put_a8 = [&](int st) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 16 * i + (lane >> 2), c = (lane & 3) * 2, x = ((r >> 1) & 1) << 2;
+            uint8_t* row = s_ab + (wave * ST + st) * STAGE + WB + r * 128;
+            codes16_store(codes[A8 ? i : 0], row + ((c ^ x) << 4), row + (((c + 1) ^ x) << 4));
+        }
     };
     // MFMA operand: index base + (lane & 31), k = 16 ks + 8 (lane >> 5) + [0, 8)
     auto frag = [&](const uint8_t* s, auto KM, int rows, int base, int ks) -> bf16x8_t {
@@ -632,6 +679,12 @@ __global__ void __launch_bounds__(256, 1) dense_small_kernel(DenseArgs p, int ac
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = (f32x16_t){};
     for (int j = 0; j < ST - 1 && j < mine; ++j) issue(j, j);
+    if constexpr (A8) {
+        if (mine > 0) {
+            fetch_a8(0);
+            put_a8(0);
+        }
+    }
     int st = 0;
     for (int j = 0; j < mine; ++j) {
         // slab j has landed; the reads of slab j - 1, whose stage is filled next, are done
@@ -639,7 +692,10 @@ __global__ void __launch_bounds__(256, 1) dense_small_kernel(DenseArgs p, int ac
             asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"((ST - 2) * CP) : "memory");
         else
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
-        if (j + ST - 1 < mine) issue(j + ST - 1, (st + ST - 1) % ST);
+        if (j + ST - 1 < mine) {
+            if constexpr (A8) fetch_a8(j + 1);
+            issue(j + ST - 1, (st + ST - 1) % ST);
+        }
         const uint8_t* s = mem + st * STAGE;
         static_for<4>([&](auto KS) {
             constexpr int ks = KS;
@@ -654,6 +710,9 @@ __global__ void __launch_bounds__(256, 1) dense_small_kernel(DenseArgs p, int ac
                 for (int u = 0; u < 2; ++u)
                     acc[i][u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fw[u], fx[i], acc[i][u], 0, 0, 0);
         });
+        if constexpr (A8) {
+            if (j + 1 < mine) put_a8(st ^ 1);
+        }
         st = st + 1 == ST ? 0 : st + 1;
     }
     // join of the 4 wavefronts: 32 rows at a time, wavefront w's 8 KiB at 8192 w, the
@@ -776,11 +835,14 @@ static void dense_launch(const DensePlan& d, const DenseArgs& a, hipStream_t s) 
     if (d.small) {
         const unsigned grid = (unsigned)total;
         if constexpr (A_KMAJ) {
-            if (a.M <= 8) return dense_small_kernel<true, B_KMAJ, 1><<<grid, 256, 0, s>>>(a, ACT);
-            if (a.M <= 16) return dense_small_kernel<true, B_KMAJ, 2><<<grid, 256, 0, s>>>(a, ACT);
-            if (a.M <= 32) return dense_small_kernel<true, B_KMAJ, 4><<<grid, 256, 0, s>>>(a, ACT);
+            if (a.M <= 8) return dense_small_kernel<true, B_KMAJ, 1, false><<<grid, 256, 0, s>>>(a, ACT);
+            if (a.M <= 16) return dense_small_kernel<true, B_KMAJ, 2, false><<<grid, 256, 0, s>>>(a, ACT);
+            if (a.M <= 32) return dense_small_kernel<true, B_KMAJ, 4, false><<<grid, 256, 0, s>>>(a, ACT);
         }
-        return dense_small_kernel<A_KMAJ, B_KMAJ, 8><<<grid, 256, 0, s>>>(a, ACT);
+        if constexpr (!A_KMAJ) {
+            if (a.a_q) return dense_small_kernel<false, B_KMAJ, 8, true><<<grid, 256, 0, s>>>(a, ACT);
+        }
+        return dense_small_kernel<A_KMAJ, B_KMAJ, 8, false><<<grid, 256, 0, s>>>(a, ACT);
     }
     // persistent: one large or two small workgroups a compute unit, a multiple of 8
     const int most = device_cus() * (d.big ? 1 : 2);
@@ -838,10 +900,28 @@ int launch_linear_dgrad(const uint16_t* dz, const uint16_t* w, const uint16_t* r
     return dense_run<true, true, 3>(a, ws, s);
 }
 
-int launch_linear_wgrad(const uint16_t* x, const uint16_t* dz, int T, int K, int N, int dw_f32, int accumulate,
-                        void* dw, void* ws, hipStream_t s) {
+// An 8-bit x is read as it is by the small kernel; larger products take a bf16 copy
+// restored into the workspace first, because converting inside the tile loop costs
+// more than the copy (16384 x 7168 x 4096: 892 us with the copy, 1260 converted in the
+// loop, 876 from bf16; 200 x 1024 x 1024: 13.1, 9.9, 10.2).
+static size_t dense_copy_bytes(int64_t T, int64_t K, int64_t N) {
+    return K % 32 || dense_plan(K, N, T).small ? 0 : (size_t)((T * K * 2 + 255) / 256 * 256);
+}
+
+size_t linear_wgrad_bytes(int T, int K, int N, bool x8) {
+    return (x8 ? dense_copy_bytes(T, K, N) : 0) + dense_part_bytes(K, N, T);
+}
+
+int launch_linear_wgrad(const uint16_t* x, const uint8_t* x_q, const uint8_t* x_s, const uint16_t* dz, int T,
+                        int K, int N, int dw_f32, int accumulate, void* dw, void* ws, hipStream_t s) {
+    if (const size_t copy = x_q ? dense_copy_bytes(T, K, N) : 0) {
+        if (launch_dequant_mxfp8(x_q, x_s, T, K, (uint16_t*)ws, s)) return -4;
+        x = (const uint16_t*)ws;
+        x_q = nullptr;
+        ws = (char*)ws + copy;
+    }
     DenseArgs a{};
-    a.A = x, a.lda = K, a.B = dz, a.ldb = N, a.M = K, a.N = N, a.K = T;
+    a.A = x, a.lda = K, a.a_q = x_q, a.a_s = x_s, a.B = dz, a.ldb = N, a.M = K, a.N = N, a.K = T;
     a.out = dw, a.out_f32 = dw_f32, a.accumulate = accumulate;
     return dense_run<false, false, 3>(a, ws, s);
 }

@@ -120,8 +120,9 @@ int launch_linear_fwd(const uint16_t* x, const uint16_t* w, const uint16_t* bias
                       void* ws, hipStream_t s);
 int launch_linear_dgrad(const uint16_t* dz, const uint16_t* w, const uint16_t* res, int T, int K, int N,
                         uint16_t* dx, void* ws, hipStream_t s);
-int launch_linear_wgrad(const uint16_t* x, const uint16_t* dz, int T, int K, int N, int dw_f32, int accumulate,
-                        void* dw, void* ws, hipStream_t s);
+int launch_linear_wgrad(const uint16_t* x, const uint8_t* x_q, const uint8_t* x_s, const uint16_t* dz, int T,
+                        int K, int N, int dw_f32, int accumulate, void* dw, void* ws, hipStream_t s);
+size_t linear_wgrad_bytes(int T, int K, int N, bool x8);
 size_t act_part_bytes(int T, int N);
 int launch_act_bwd(const uint16_t* dy, const uint16_t* z, const uint8_t* z_q, const uint8_t* z_s, int T, int N,
                    int act, uint16_t* dz, uint16_t* a, float* dbias, void* ws, hipStream_t s);

@@ -67,7 +67,8 @@ def test_gradient_product_refusals():
     assert w(None, F, None, F, 8, 64, 64, 1, 0, F, F, BIG, None) == -1          # codes without scales
     assert w(None, F, F, F, 8, 40, 64, 1, 0, F, F, BIG, None) == -2             # rows not whole blocks
     assert w(F, None, None, F, 8, 64, 64, 0, 1, F, F, BIG, None) == -2          # accumulation is fp32
-    assert w(None, F, F, F, 8, 64, 64, 1, 0, F, F, 64, None) == -3
+    assert w(None, F, F, F, 8192, 64, 64, 1, 0, F, F, 64, None) == -3
+    assert w(None, F, F, F, 1000, 2880, 5760, 1, 0, F, F, 1000 * 2880, None) == -3
     assert w(F, None, None, F, 8192, 64, 64, 1, 0, F, None, 0, None) == -3
     assert w(F, None, None, ODD, 8, 64, 64, 1, 0, F, F, BIG, None) == -1
 
@@ -93,8 +94,9 @@ def test_workspace_sizes():
     assert M.moe_linear_workspace_bytes(0, 64, 64) == 0
     assert M.moe_linear_workspace_bytes(8, 60, 64) == 0
     assert M.moe_linear_workspace_bytes(1, 8192, 4096, M.MOE_LINEAR_FWD) > 0
-    # the backward's workspace holds the restored copy of an 8-bit input
+    # a large product from an 8-bit input restores a copy of it there; a small one reads it as it is
     assert M.moe_linear_workspace_bytes(1000, 2880, 5760, M.MOE_LINEAR_BWD) >= 1000 * 2880 * 2
+    assert M.moe_linear_workspace_bytes(200, 1024, 1024, M.MOE_LINEAR_BWD) < 200 * 1024 * 2
     assert M.moe_balance_workspace_bytes(8, 4, 9) == 0
     assert M.moe_balance_workspace_bytes(8, 4, 8) > 0
 
