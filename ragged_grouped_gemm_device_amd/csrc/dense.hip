@@ -774,7 +774,8 @@ __global__ void __launch_bounds__(256, 1) dense_small_kernel(DenseArgs p, int ac
 // fastest of 11 candidates there, or one within about 10%):
 //   64 x 64 tiles (small kernel): a round over the compute units takes 2.2, plus 0.9 for
 //     every slab of a wavefront (a quarter of the split's slabs), 0.55 with at most 32 rows;
-//   128 x 128 tiles: 0.72 a slab for one on a compute unit, 0.95 for two side by side, and
+//   128 x 128 tiles: 0.72 a slab for one on a compute unit, 0.95 for two side by side (an
+//     eighth more in the dgrad, which reads W from HBM in 128-byte pieces of its rows), and
 //     2.5 for the prologue and epilogue;
 //   256 x 256 tiles: 1.05 a slab with few of them at work up to 1.7 with all (clock and
 //     L2), and 7 for the prologue and epilogue;
@@ -792,7 +793,7 @@ struct DensePlan {
 };
 constexpr int kDenseCus = 256;
 
-static DensePlan dense_plan(int64_t M, int64_t N, int64_t K) {
+static DensePlan dense_plan(int64_t M, int64_t N, int64_t K, bool dgrad) {
     const int64_t slabs = (K + DBK - 1) / DBK;
     DensePlan best{};
     double least = 0;
@@ -806,7 +807,8 @@ static DensePlan dense_plan(int64_t M, int64_t N, int64_t K) {
             if (kind == 0)
                 t = (double)rounds * (2.2 + (M <= 32 ? 0.55 : 0.9) * (double)((ss + 3) / 4));
             else if (kind == 1)
-                t = (double)ss * ((double)(rounds / 2) * 0.95 + (double)(rounds % 2) * 0.72) + 2.5 * (double)((rounds + 1) / 2);
+                t = (dgrad ? 1.12 : 1.0) * (double)ss * ((double)(rounds / 2) * 0.95 + (double)(rounds % 2) * 0.72) +
+                    2.5 * (double)((rounds + 1) / 2);
             else
                 {
                 const double fill = std::min(1.0, (double)tiles / kDenseCus);
@@ -824,8 +826,8 @@ static DensePlan dense_plan(int64_t M, int64_t N, int64_t K) {
     return best;
 }
 
-size_t dense_part_bytes(int64_t M, int64_t N, int64_t K) {
-    const DensePlan d = dense_plan(M, N, K);
+size_t dense_part_bytes(int64_t M, int64_t N, int64_t K, bool dgrad) {
+    const DensePlan d = dense_plan(M, N, K, dgrad);
     return d.splits > 1 ? (size_t)d.splits * M * N * sizeof(float) : 0;
 }
 
@@ -855,7 +857,7 @@ static void dense_launch(const DensePlan& d, const DenseArgs& a, hipStream_t s) 
 
 template <bool A_KMAJ, bool B_KMAJ, int ACT>
 static int dense_run(DenseArgs a, void* ws, hipStream_t s) {
-    const DensePlan d = dense_plan(a.M, a.N, a.K);
+    const DensePlan d = dense_plan(a.M, a.N, a.K, B_KMAJ);
     a.ntm = d.ntm;
     a.ntn = d.ntn;
     a.splits = d.splits;
@@ -905,11 +907,11 @@ int launch_linear_dgrad(const uint16_t* dz, const uint16_t* w, const uint16_t* r
 // more than the copy (16384 x 7168 x 4096: 892 us with the copy, 1260 converted in the
 // loop, 876 from bf16; 200 x 1024 x 1024: 13.1, 9.9, 10.2).
 static size_t dense_copy_bytes(int64_t T, int64_t K, int64_t N) {
-    return K % 32 || dense_plan(K, N, T).small ? 0 : (size_t)((T * K * 2 + 255) / 256 * 256);
+    return K % 32 || dense_plan(K, N, T, false).small ? 0 : (size_t)((T * K * 2 + 255) / 256 * 256);
 }
 
 size_t linear_wgrad_bytes(int T, int K, int N, bool x8) {
-    return (x8 ? dense_copy_bytes(T, K, N) : 0) + dense_part_bytes(K, N, T);
+    return (x8 ? dense_copy_bytes(T, K, N) : 0) + dense_part_bytes(K, N, T, false);
 }
 
 int launch_linear_wgrad(const uint16_t* x, const uint8_t* x_q, const uint8_t* x_s, const uint16_t* dz, int T,
