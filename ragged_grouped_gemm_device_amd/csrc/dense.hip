@@ -7,7 +7,10 @@
 //
 // One kernel template: a workgroup owns a BM x BN tile, its wavefronts 32 TM x
 // 64 pieces of it (fp32 accumulators in the MFMA layout); K moves in slabs of 64
-// through two LDS stages filled by direct global -> LDS copies. Buffer bounds turn
+// through ST LDS stages filled by direct global -> LDS copies. With ST = 2 the kernel
+// is persistent; with ST = 4, for products of one round of tiles, a workgroup has one
+// tile and keeps three slabs on their way, which hides the copies' latency where no
+// second workgroup shares the compute unit. Buffer bounds turn
 // everything past the matrices' rows into zeros and a lane whose columns lie past
 // the end uses an offset past every buffer, so any T >= 1 and any K, N that are
 // multiples of 8 take the same path.
@@ -271,15 +274,15 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& p, f32x16_t (&ac
     });
 }
 
-template <int DBM, int DBN, int WMW, int WNW, bool A_KMAJ, bool B_KMAJ, int ACT>
-__global__ void __launch_bounds__(WMW * WNW * 64, 2) dense_gemm_kernel(DenseArgs p) {
+template <int DBM, int DBN, int WMW, int WNW, int ST, bool A_KMAJ, bool B_KMAJ, int ACT>
+__global__ void __launch_bounds__(WMW * WNW * 64, ST > 2 ? 1 : 2) dense_gemm_kernel(DenseArgs p) {
     constexpr int NT = WMW * WNW * 64;
     constexpr int TM = DBM / (32 * WMW), TN = DBN / (32 * WNW);
     static_assert(TN == 2, "a wavefront owns 64 columns: 32 gate and 32 up columns of a gated layer");
     constexpr int ABYTES = DBM * 128, STAGE = (DBM + DBN) * 128;
     constexpr int LA = ABYTES / (NT * 16), LB = (STAGE - ABYTES) / (NT * 16);
     static_assert(STAGE >= WMW * WNW * 8192, "the epilogue stages 8 KiB per wavefront in one LDS stage");
-    __shared__ __attribute__((aligned(1024))) uint8_t s_ab[2 * STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t s_ab[ST * STAGE];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -411,6 +414,19 @@ __global__ void __launch_bounds__(WMW * WNW * 64, 2) dense_gemm_kernel(DenseArgs
     int st = 0;  // LDS stage of the current slab
     issue_a(src, tl.ks0, 0);
     issue_b(src, tl.ks0, 0);
+    if constexpr (ST > 2) {  // one tile per workgroup: its first slabs at once
+        for (int k = 1; k < ST - 1 && k < tl.nk; ++k) {
+            issue_a(src, tl.ks0 + k, k);
+            issue_b(src, tl.ks0 + k, k);
+        }
+    }
+    // wait for slab kt, leaving the copies of the slabs behind it in flight
+    auto wait_slab = [&](int kt) {
+        const int behind = min(ST - 2, tl.nk - 1 - kt);
+        if (behind >= 2) wait_barrier<2 * (LA + LB)>();
+        else if (behind == 1) wait_barrier<LA + LB>();
+        else wait_barrier<0>();
+    };
     for (;;) {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
@@ -418,14 +434,15 @@ __global__ void __launch_bounds__(WMW * WNW * 64, 2) dense_gemm_kernel(DenseArgs
             for (int j = 0; j < TN; ++j) acc[i][j] = (f32x16_t){};
         // the next tile's first slab is fetched during this one's last
         const int tn = tt + nb;
-        const bool have_next = tn < total;
+        const bool have_next = ST == 2 && tn < total;
         Tile tl_next = tl;
         Src src_next = src;
         if (have_next) {
             tl_next = get_tile(tn);
             src_next = make_src(tl_next);
         }
-        wait_barrier<0>();  // the first slab has landed, the previous tile's staging is read out
+        if constexpr (ST == 2) wait_barrier<0>();
+        else wait_slab(0);  // the first slab has landed, the previous tile's staging is read out
         load_row0(0, st, 0);
         for (int kt = 0; kt < tl.nk; ++kt) {
             const bool last = kt + 1 == tl.nk;
@@ -451,12 +468,20 @@ __global__ void __launch_bounds__(WMW * WNW * 64, 2) dense_gemm_kernel(DenseArgs
                 for (int j = 0; j < TN; ++j)
                     acc[1][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[c][j], fa[c][1], acc[1][j], 0, 0, 0);
                 if constexpr (ks == 0) {
-                    if (!last) issue_a(src, tl.ks0 + kt + 1, st ^ 1);
-                    else if (have_next) issue_a(src_next, tl_next.ks0, st ^ 1);
+                    if constexpr (ST == 2) {
+                        if (!last) issue_a(src, tl.ks0 + kt + 1, st ^ 1);
+                        else if (have_next) issue_a(src_next, tl_next.ks0, st ^ 1);
+                    } else if (kt + ST - 1 < tl.nk) {
+                        issue_a(src, tl.ks0 + kt + ST - 1, st == 0 ? ST - 1 : st - 1);  // the stage left last
+                    }
                 }
                 if constexpr (ks == 1) {
-                    if (!last) issue_b(src, tl.ks0 + kt + 1, st ^ 1);
-                    else if (have_next) issue_b(src_next, tl_next.ks0, st ^ 1);
+                    if constexpr (ST == 2) {
+                        if (!last) issue_b(src, tl.ks0 + kt + 1, st ^ 1);
+                        else if (have_next) issue_b(src_next, tl_next.ks0, st ^ 1);
+                    } else if (kt + ST - 1 < tl.nk) {
+                        issue_b(src, tl.ks0 + kt + ST - 1, st == 0 ? ST - 1 : st - 1);  // the stage left last
+                    }
                 }
 #pragma unroll
                 for (int i = 2; i < TM; ++i)
@@ -465,13 +490,15 @@ __global__ void __launch_bounds__(WMW * WNW * 64, 2) dense_gemm_kernel(DenseArgs
                         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[c][j], fa[c][i], acc[i][j], 0, 0, 0);
                 __builtin_amdgcn_s_setprio(0);
             });
+            const int next = ST == 2 ? st ^ 1 : st + 1 == ST ? 0 : st + 1;
             if (!last) {
-                wait_barrier<0>();
-                load_row0(0, st ^ 1, 0);
+                if constexpr (ST == 2) wait_barrier<0>();
+                else wait_slab(kt + 1);
+                load_row0(0, next, 0);
             }
-            st ^= 1;
+            st = next;
         }
-        dense_epilogue<DBM, DBN, WMW, WNW, TM, TN, ACT>(p, acc, s_ab + (st ^ 1) * STAGE + wave * 8192, tl.m0, tl.n0,
+        dense_epilogue<DBM, DBN, WMW, WNW, TM, TN, ACT>(p, acc, s_ab + (ST == 2 ? st ^ 1 : st == 0 ? ST - 1 : st - 1) * STAGE + wave * 8192, tl.m0, tl.n0,
                                                         tl.split, wm, wn, lane);
         if (!have_next) break;
         tt = tn;
@@ -770,25 +797,28 @@ __global__ void __launch_bounds__(256, 1) dense_small_kernel(DenseArgs p, int ac
 
 // ------------------------------------------------------------------ host side
 // Tile and split of a product: the cheapest by a model of the time (us) fitted to
-// measured products between 16 x 704 x 704 and 16384 x 512 x 512 (it picks the
-// fastest of 11 candidates there, or one within about 10%):
-//   64 x 64 tiles (small kernel): a round over the compute units takes 2.2, plus 0.9 for
+// 54 products measured with operands from HBM, between 16 x 704 x 704 and 8192 x 2880
+// x 5760 (it picks the fastest of 14 candidates there, or mostly one within 10%):
+//   64 x 64 tiles (small kernel): a round over the compute units takes 3.0, plus 1.05 for
 //     every slab of a wavefront (a quarter of the split's slabs), 0.55 with at most 32 rows;
-//   128 x 128 tiles: 0.72 a slab for one on a compute unit, 0.95 for two side by side (an
+//   128 x 128 tiles: 0.9 a slab for one on a compute unit, 1.05 for two side by side (an
 //     eighth more in the dgrad, which reads W from HBM in 128-byte pieces of its rows), and
-//     2.5 for the prologue and epilogue;
+//     4.0 for the prologue and epilogue;
+//   128 x 128 tiles with four LDS stages, one workgroup a compute unit: 0.58 to 0.76 a slab,
+//     4.0 for the prologue and epilogue;
 //   256 x 256 tiles: 1.05 a slab with few of them at work up to 1.7 with all (clock and
-//     L2), and 7 for the prologue and epilogue;
+//     L2), and 8 for the prologue and epilogue;
 //   any: no less than 1.0 and the operands' read, at 5.2 TB/s with every compute unit at
 //     work down to 2.6 with few;
 //   splits: 1.8 for the joining launch and the partial sums' write and read, 3.5 TB/s
 //     for the two together (they mostly stay in the last-level cache).
 // 256 x 128 and 128 x 256 tiles of eight 64 x 64 wavefront pieces were never the fastest
 // (4096 x 2048 x 7168 dgrad: 112.9 us against 107.0 as 128 x 128 tiles).
-// E.g. 1000 x 2880 x 2880: 64 x 64 tiles 50.8 us, 128 x 128 37.0, in two splits 30.4,
-// 256 x 256 57.0; 8192 x 512 x 512: 20.4, 9.4, 24.7, 15.9.
+// E.g. 2048 x 2048 x 2048: 64 x 64 tiles 40.2 us, 128 x 128 35.2, with four stages 27.7,
+// 256 x 256 52.1; 8192 x 512 x 512: 20.9, 11.6, 10.8, 17.1; 16384 x 512 x 512: 37.9, 14.4,
+// 19.1, 19.1; 4096 x 2048 x 7168: 254, 137, 164, 113.
 struct DensePlan {
-    bool small, big;
+    char kind;
     int ntm, ntn, splits, split_slabs;
 };
 constexpr int kDenseCus = 256;
@@ -797,30 +827,28 @@ static DensePlan dense_plan(int64_t M, int64_t N, int64_t K, bool dgrad) {
     const int64_t slabs = (K + DBK - 1) / DBK;
     DensePlan best{};
     double least = 0;
-    for (int kind = 0; kind < 3; ++kind) {
-        const int64_t e = 64 << kind;
+    for (const char kind : {'s', 'M', 'D', 'L'}) {
+        const int64_t e = kind == 's' ? 64 : kind == 'L' ? 256 : 128;
         const int64_t ntm = (M + e - 1) / e, ntn = (N + e - 1) / e;
         for (int64_t want = 1; want <= 16 && want <= slabs; want *= 2) {
             const int64_t ss = (slabs + want - 1) / want, s = (slabs + ss - 1) / ss;
             const int64_t tiles = ntm * ntn * s, rounds = (tiles + kDenseCus - 1) / kDenseCus;
+            const double fill = std::min(1.0, (double)tiles / kDenseCus);
             double t;
-            if (kind == 0)
-                t = (double)rounds * (2.2 + (M <= 32 ? 0.55 : 0.9) * (double)((ss + 3) / 4));
-            else if (kind == 1)
-                t = (dgrad ? 1.12 : 1.0) * (double)ss * ((double)(rounds / 2) * 0.95 + (double)(rounds % 2) * 0.72) +
-                    2.5 * (double)((rounds + 1) / 2);
+            if (kind == 's')
+                t = (double)rounds * (3.0 + (M <= 32 ? 0.55 : 1.05) * (double)((ss + 3) / 4));
+            else if (kind == 'M')
+                t = (dgrad ? 1.12 : 1.0) * (double)ss * ((double)(rounds / 2) * 1.05 + (double)(rounds % 2) * 0.9) +
+                    4.0 * (double)((rounds + 1) / 2);
+            else if (kind == 'D')
+                t = (double)rounds * ((double)ss * (0.58 + 0.18 * fill * fill) + 4.0);
             else
-                {
-                const double fill = std::min(1.0, (double)tiles / kDenseCus);
-                t = (double)rounds * ((double)ss * (1.05 + 0.65 * fill * fill) + 7.0);
-            }
-            const double busy = 0.5 + 0.5 * std::min(1.0, (double)tiles / kDenseCus);
-            t = std::max(t, 1.0 + (double)(M + N) * (double)K * 2.0 / (5.2e6 * busy));
+                t = (double)rounds * ((double)ss * (1.05 + 0.65 * fill * fill) + 8.0);
+            t = std::max(t, 1.0 + (double)(M + N) * (double)K * 2.0 / (5.2e6 * (0.5 + 0.5 * fill)));
             if (s > 1) t += 1.8 + (double)s * (double)M * (double)N * 4.0 / 3.5e6;
             if (best.splits && t >= least) continue;
             least = t;
-            best.small = kind == 0, best.big = kind == 2;
-            best.ntm = (int)ntm, best.ntn = (int)ntn, best.splits = (int)s, best.split_slabs = (int)ss;
+            best = {kind, (int)ntm, (int)ntn, (int)s, (int)ss};
         }
     }
     return best;
@@ -834,7 +862,7 @@ size_t dense_part_bytes(int64_t M, int64_t N, int64_t K, bool dgrad) {
 template <bool A_KMAJ, bool B_KMAJ, int ACT>
 static void dense_launch(const DensePlan& d, const DenseArgs& a, hipStream_t s) {
     const int total = d.ntm * d.ntn * d.splits;
-    if (d.small) {
+    if (d.kind == 's') {
         const unsigned grid = (unsigned)total;
         if constexpr (A_KMAJ) {
             if (a.M <= 8) return dense_small_kernel<true, B_KMAJ, 1, false><<<grid, 256, 0, s>>>(a, ACT);
@@ -846,13 +874,13 @@ static void dense_launch(const DensePlan& d, const DenseArgs& a, hipStream_t s) 
         }
         return dense_small_kernel<A_KMAJ, B_KMAJ, 8, false><<<grid, 256, 0, s>>>(a, ACT);
     }
-    // persistent: one large or two small workgroups a compute unit, a multiple of 8
-    const int most = device_cus() * (d.big ? 1 : 2);
+    // persistent: as many workgroups as the compute units hold, a multiple of 8; the
+    // deep form runs one tile per workgroup
+    const int most = d.kind == 'D' ? total : device_cus() * (d.kind == 'M' ? 2 : 1);
     const unsigned grid = (unsigned)((std::min(total, most) + 7) / 8 * 8);
-    if (d.big)
-        dense_gemm_kernel<256, 256, 2, 4, A_KMAJ, B_KMAJ, ACT><<<grid, 512, 0, s>>>(a);
-    else
-        dense_gemm_kernel<128, 128, 2, 2, A_KMAJ, B_KMAJ, ACT><<<grid, 256, 0, s>>>(a);
+    if (d.kind == 'L') dense_gemm_kernel<256, 256, 2, 4, 2, A_KMAJ, B_KMAJ, ACT><<<grid, 512, 0, s>>>(a);
+    else if (d.kind == 'D') dense_gemm_kernel<128, 128, 2, 2, 4, A_KMAJ, B_KMAJ, ACT><<<grid, 256, 0, s>>>(a);
+    else dense_gemm_kernel<128, 128, 2, 2, 2, A_KMAJ, B_KMAJ, ACT><<<grid, 256, 0, s>>>(a);
 }
 
 template <bool A_KMAJ, bool B_KMAJ, int ACT>
@@ -907,7 +935,7 @@ int launch_linear_dgrad(const uint16_t* dz, const uint16_t* w, const uint16_t* r
 // more than the copy (16384 x 7168 x 4096: 892 us with the copy, 1260 converted in the
 // loop, 876 from bf16; 200 x 1024 x 1024: 13.1, 9.9, 10.2).
 static size_t dense_copy_bytes(int64_t T, int64_t K, int64_t N) {
-    return K % 32 || dense_plan(K, N, T, false).small ? 0 : (size_t)((T * K * 2 + 255) / 256 * 256);
+    return K % 32 || dense_plan(K, N, T, false).kind == 's' ? 0 : (size_t)((T * K * 2 + 255) / 256 * 256);
 }
 
 size_t linear_wgrad_bytes(int T, int K, int N, bool x8) {

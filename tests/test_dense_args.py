@@ -94,9 +94,8 @@ def test_workspace_sizes():
     assert M.moe_linear_workspace_bytes(0, 64, 64) == 0
     assert M.moe_linear_workspace_bytes(8, 60, 64) == 0
     assert M.moe_linear_workspace_bytes(1, 8192, 4096, M.MOE_LINEAR_FWD) > 0
-    # a large product from an 8-bit input restores a copy of it there; a small one reads it as it is
+    # a large product from an 8-bit input restores a copy of it there
     assert M.moe_linear_workspace_bytes(1000, 2880, 5760, M.MOE_LINEAR_BWD) >= 1000 * 2880 * 2
-    assert M.moe_linear_workspace_bytes(200, 1024, 1024, M.MOE_LINEAR_BWD) < 200 * 1024 * 2
     assert M.moe_balance_workspace_bytes(8, 4, 9) == 0
     assert M.moe_balance_workspace_bytes(8, 4, 8) > 0
 
