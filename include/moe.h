@@ -64,6 +64,8 @@ extern "C" {
 #define MOE_MAX_EXPERTS 1024
 #define MOE_MAX_WIDTH (1 << 20) /* largest d and FC1 width (2n, or n for sReLU) */
 
+#define MOE_MAX_ROWS (1 << 30)  /* largest T of the dense entry points */
+
 /* status codes */
 #define MOE_OK 0
 #define MOE_ERR_INVALID_ARG (-1)  /* NULL/negative/misaligned argument      */
@@ -428,8 +430,8 @@ int moe_permute_quant_mxfp8(const uint16_t* x, const int32_t* src_of, int T, int
  * A linear layer is z = x W + b, y = f(z) + r with x [T, K], W [K, N], z [T, N]
  * and y, r [T, NO]: NO = N, or N / 2 for the gated activations, whose columns
  * are interleaved as in w1 above (32 gate columns, then their 32 up columns).
- * K and N are multiples of 8 (N of 64 when gated) up to MOE_MAX_WIDTH; T >= 1
- * is any row count. Pointers to tensors of 16-bit values or codes, and the
+ * K and N are multiples of 8 (N of 64 when gated) up to MOE_MAX_WIDTH; T is any
+ * row count from 1 to MOE_MAX_ROWS. Pointers to tensors of 16-bit values or codes, and the
  * workspace, are 16-byte aligned. Outputs must not overlap inputs, except that
  * a residual may be the output itself.
  *
@@ -527,7 +529,7 @@ size_t moe_balance_workspace_bytes(int T, int E, int S);
  *   with a live token, then all live tokens) (out).
  *   Sums are joined in a fixed order: the same inputs give the same bits.
  *   workspace: moe_balance_workspace_bytes(T, E, S) bytes.
- * Requires 1 <= k <= E <= MOE_MAX_EXPERTS, 1 <= S <= T.
+ * Requires 1 <= k <= E <= MOE_MAX_EXPERTS, 1 <= S <= T <= MOE_MAX_ROWS.
  */
 int moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* valid,
                      const int32_t* seq_offsets, int T, int E, int k, int S, float balance_coef, float z_coef,

@@ -26,6 +26,7 @@ bool gated(int act) { return act == MOE_ACT_SWIGLU || act == MOE_ACT_GEGLU; }
 
 int check_linear(int T, int K, int N, int act) {
     if (T <= 0 || K <= 0 || N <= 0) return MOE_ERR_INVALID_ARG;
+    if (T > MOE_MAX_ROWS) return MOE_ERR_UNSUPPORTED;  // row numbers past a tile's end stay 32-bit
     if (act < MOE_ACT_SWIGLU || act > MOE_ACT_GELU) return MOE_ERR_UNSUPPORTED;
     if (K % 8 || N % 8 || (gated(act) && N % (2 * MOE_GLU_INTERLEAVE))) return MOE_ERR_UNSUPPORTED;
     if (K > MOE_MAX_WIDTH || N > MOE_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
@@ -117,6 +118,7 @@ int moe_dequant_mxfp8(const uint8_t* q, const uint8_t* s, int64_t R, int C, uint
 
 static int check_balance(int T, int E, int k, int S) {
     if (T <= 0 || E <= 0 || E > MOE_MAX_EXPERTS || k <= 0 || k > E || S <= 0 || S > T) return MOE_ERR_INVALID_ARG;
+    if (T > MOE_MAX_ROWS || (int64_t)S * ((E + 31) / 32) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 

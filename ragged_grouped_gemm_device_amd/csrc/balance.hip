@@ -155,8 +155,8 @@ __device__ __forceinline__ bool token_softmax(float (&x)[PER], bool valid, float
 // Joins the chunks' rows of sequence s for experts [32 et, 32 et + 32); all 256
 // threads of a workgroup, also one after another for several (s, et).
 __device__ __forceinline__ void balance_join(const BalanceArgs& p, int s, int et) {
-    __shared__ float s_p[8][33], s_z[256];
-    __shared__ int s_c[8][33], s_n[256];
+    __shared__ float s_p[8][33], s_z[4];
+    __shared__ int s_c[8][33], s_n[4];
     const int tid = threadIdx.x, el = tid & 31, l = tid >> 5;
     const int e = et * 32 + el;
     const int a = seq_at(p, s), b = seq_at(p, s + 1);
@@ -176,17 +176,15 @@ __device__ __forceinline__ void balance_join(const BalanceArgs& p, int s, int et
     }
     s_p[l][el] = pe;
     s_c[l][el] = ce;
-    s_n[tid] = n;
-    s_z[tid] = z;
-    __syncthreads();
-    for (int o = 128; o > 0; o >>= 1) {
-        if (tid < o) {
-            s_n[tid] += s_n[tid + o];
-            s_z[tid] += s_z[tid + o];
-        }
-        __syncthreads();
+    z = wave_sum(z);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o, 64);
+    if ((tid & 63) == 0) {
+        s_n[tid >> 6] = n;
+        s_z[tid >> 6] = z;
     }
-    n = s_n[0];
+    __syncthreads();
+    n = s_n[0] + s_n[1] + s_n[2] + s_n[3];
     if (tid < 64) {
         float v = 0.f;
         if (tid < 32 && e < p.E) {
@@ -207,7 +205,7 @@ __device__ __forceinline__ void balance_join(const BalanceArgs& p, int s, int et
             p.bal[(int64_t)s * p.etiles + et] = v;
             if (et == 0) {
                 p.tokens[s] = n;
-                p.zs[s] = s_z[0];
+                p.zs[s] = (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]);
             }
         }
     }
@@ -216,8 +214,8 @@ __device__ __forceinline__ void balance_join(const BalanceArgs& p, int s, int et
 
 // The losses from the joined sums (one workgroup of 256 threads).
 __device__ __forceinline__ void balance_total(const BalanceArgs& p) {
-    __shared__ double s_b[256], s_z[256];
-    __shared__ int s_n[256], s_live[256];
+    __shared__ double s_b[4], s_z[4];
+    __shared__ int s_n[4], s_live[4];
     const int tid = threadIdx.x;
     double b = 0.0, z = 0.0;
     int n = 0, live = 0;
@@ -228,24 +226,26 @@ __device__ __forceinline__ void balance_total(const BalanceArgs& p) {
         n += m;
         live += m > 0;
     }
-    s_b[tid] = b, s_z[tid] = z, s_n[tid] = n, s_live[tid] = live;
-    __syncthreads();
-    for (int o = 128; o > 0; o >>= 1) {
-        if (tid < o) {
-            s_b[tid] += s_b[tid + o];
-            s_z[tid] += s_z[tid + o];
-            s_n[tid] += s_n[tid + o];
-            s_live[tid] += s_live[tid + o];
-        }
-        __syncthreads();
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        b += __shfl_xor(b, o, 64);
+        z += __shfl_xor(z, o, 64);
+        n += __shfl_xor(n, o, 64);
+        live += __shfl_xor(live, o, 64);
     }
+    if ((tid & 63) == 0) s_b[tid >> 6] = b, s_z[tid >> 6] = z, s_n[tid >> 6] = n, s_live[tid >> 6] = live;
+    __syncthreads();
     if (tid == 0) {
-        const double bal = s_live[0] ? s_b[0] / s_live[0] : 0.0, zl = s_n[0] ? s_z[0] / s_n[0] : 0.0;
+        b = (s_b[0] + s_b[1]) + (s_b[2] + s_b[3]);
+        z = (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]);
+        n = s_n[0] + s_n[1] + s_n[2] + s_n[3];
+        live = s_live[0] + s_live[1] + s_live[2] + s_live[3];
+        const double bal = live ? b / live : 0.0, zl = n ? z / n : 0.0;
         p.loss[0] = (float)(p.cb * bal + p.cz * zl);
         p.loss[1] = (float)bal;
         p.loss[2] = (float)zl;
-        p.tokens[p.S] = s_live[0];
-        p.tokens[p.S + 1] = s_n[0];
+        p.tokens[p.S] = live;
+        p.tokens[p.S + 1] = n;
     }
 }
 

@@ -24,6 +24,7 @@ MOE_ALIGN = 128
 MOE_MX_BLOCK = 32
 MOE_GLU_INTERLEAVE = 32
 MOE_MAX_EXPERTS = 1024
+MOE_MAX_ROWS = 1 << 30
 MOE_ACT_SWIGLU = 0
 MOE_ACT_GEGLU = 1
 MOE_ACT_SRELU = 2   # non-gated relu(h)^2: FC1 width n
@@ -339,7 +340,8 @@ def moe_linear_fwd(x, w, y, act=MOE_ACT_NONE, bias=None, residual=None, z=None, 
     _operand(z_q, (T, N), _U8, "z_q", dev)
     _operand(z_s, (T, N // MOE_MX_BLOCK), _U8, "z_s", dev)
     ws, nws = _space(workspace, dev)
-    rc = _lib().moe_linear_fwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), T, K, N, act, int(y.dtype == _F32),
+    rc = _lib().moe_linear_fwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), T, K, N, act,
+                               int(y is not None and y.dtype is _F32),
                                _ptr(y), _ptr(z), _ptr(z_q), _ptr(z_s), ws, nws, _stream())
     _check("moe_linear_fwd", rc)
 
@@ -347,7 +349,9 @@ def moe_linear_fwd(x, w, y, act=MOE_ACT_NONE, bias=None, residual=None, z=None, 
 def moe_act_bwd(dy, dz, act=MOE_ACT_NONE, z=None, z_q=None, z_s=None, a=None, dbias=None, workspace=None):
     """dz = dy f'(z) with z as bf16 or from its 8-bit checkpoint; optionally a = f(z) and dbias =
     column sums of dz. dz (and dy, when only a is wanted) may be None."""
-    ref = next(t for t in (z, z_q, dy) if t is not None)
+    ref = next((t for t in (z, z_q, dy) if t is not None), None)
+    if ref is None:
+        raise ValueError("neither dy nor z is given")
     dev = _device(ref)
     T, N = ref.shape
     out = (T, N // 2 if act in _GATED else N)

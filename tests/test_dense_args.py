@@ -26,7 +26,7 @@ def _fwd(x=F, w=F, bias=None, res=None, T=8, K=64, N=64, act=3, f32=0, y=F, z=No
 @pytest.mark.parametrize("kw, want", [
     (dict(x=None), -1), (dict(w=None), -1), (dict(y=None), -1), (dict(T=0), -1), (dict(K=0), -1), (dict(N=-8), -1),
     (dict(act=6), -2), (dict(act=-1), -2), (dict(K=60), -2), (dict(N=60), -2), (dict(act=0, N=96), -2),
-    (dict(K=(1 << 20) + 8), -2), (dict(T=(1 << 31) - 1, N=1 << 20), -2),
+    (dict(K=(1 << 20) + 8), -2), (dict(T=1 << 30, N=1 << 20), -2), (dict(T=(1 << 30) + 1, K=8, N=8), -2),
     (dict(x=ODD), -1), (dict(w=ODD), -1), (dict(y=ODD), -1), (dict(bias=ODD), -1), (dict(res=ODD), -1),
     (dict(act=4, z=ODD), -1), (dict(act=4, zq=ODD, zs=F), -1), (dict(act=4, zq=F), -1), (dict(act=4, zs=F), -1),
     (dict(act=4, N=40, zq=F, zs=F), -2), (dict(act=3, z=F), -1), (dict(act=3, zq=F, zs=F), -1),
@@ -85,6 +85,7 @@ def test_dequant_and_balance_refusals():
                dict(S=2), dict(lg=None)):
         assert f(**kw) == -1, kw
     assert f(n=16) == -3 and f(ws=None) == -3 and f(ws=ODD) == -3
+    assert f(T=(1 << 30) + 1, E=1, k=1) == -2 and f(T=1 << 28, E=1024, S=1 << 28, seq=F) == -2
     b = lambda T=8, E=4, k=2, S=1, seq=None, d=F: lib.moe_balance_loss_bwd(  # noqa: E731
         F, F, F, None, seq, T, E, k, S, 1.0, 1.0, None, 0, d, None, None)
     assert b(T=0) == -1 and b(k=5) == -1 and b(S=2) == -1 and b(S=9, seq=F) == -1 and b(d=None) == -1
@@ -124,6 +125,8 @@ def test_binding_refuses_operands_of_another_shape_type_or_layout():
         M.moe_linear_dgrad(y, w, torch.zeros(5, 64, dtype=bf))
     with pytest.raises(ValueError):
         M.moe_act_bwd(y, None, M.MOE_ACT_NONE, dbias=torch.zeros(64))
+    with pytest.raises(ValueError):
+        M.moe_act_bwd(None, y)
     lg, idx = torch.zeros(6, 4), torch.zeros(6, 2, dtype=torch.int32)
     one = dict(loss=torch.zeros(3), counts=torch.zeros(1, 4, dtype=torch.int32), prob=torch.zeros(1, 4),
                tokens=torch.zeros(3, dtype=torch.int32), workspace=torch.zeros(4096, dtype=torch.uint8),

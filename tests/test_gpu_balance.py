@@ -154,3 +154,27 @@ def test_same_bits_and_counts_of_the_router(M):
     assert np.array_equal(a["counts"][0], counts.cpu().numpy())
     for key in a:
         assert np.array_equal(a[key], b[key]), key
+
+
+def test_one_sequence_inside_the_batch_and_rows_off_16_bytes(M):
+    """S = 1 with offsets (tokens before and behind it get gradient 0), and logits and gradients
+    that start 4 bytes past a 16-byte boundary (element loads instead of 16-byte pieces)."""
+    _, lg, idx = _case(120, 16, 3, 9)
+    offs = np.array([17, 101], np.int32)
+    _check(_run(M, lg, idx, offs=offs), lg, idx, offs=offs)
+    T, E = lg.shape
+    want = _run(M, lg, idx)
+    hold = torch.empty(T * E + 1, device="cuda")
+    off = hold[1:].view(T, E)
+    off.copy_(torch.from_numpy(lg))
+    g = torch.empty(T * E + 1, device="cuda")[1:].view(T, E)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    loss, counts, prob, tokens = torch.empty(3, device="cuda"), torch.empty(1, E, **i32), torch.empty(1, E, device="cuda"), torch.empty(3, **i32)
+    ws = torch.empty(M.moe_balance_workspace_bytes(T, E, 1), dtype=torch.uint8, device="cuda")
+    M.moe_balance_loss(off, torch.from_numpy(idx).cuda(), loss, counts, prob, tokens, ws, 0.3, 0.02)
+    M.moe_balance_loss_bwd(off, counts, tokens, g, 3, 0.3, 0.02)
+    torch.cuda.synchronize()
+    # another lane takes each expert, so the sums' order may differ: P above, 26 2^-23 + n 2^-24
+    assert np.abs(g.cpu().numpy() - want["dlogits"]).max() <= 1e-4 * np.abs(want["dlogits"]).max()
+    assert np.abs(loss.cpu().numpy() - want["loss"]).max() <= 3e-5 * want["loss"].max()
+    assert np.array_equal(counts.cpu().numpy(), want["counts"])

@@ -259,3 +259,83 @@ def test_other_stream_device_and_refusals(M):
         M.moe_linear_fwd(x, w, y1, workspace=_space(M, 48, 1024, 256))
     side.synchronize()
     assert torch.equal(y0, y1)
+
+
+def test_infinities_and_nan_stay_in_their_rows_and_columns(M):
+    """Nothing that lies past the end of K, of a tile or of the rows meets a non-finite value."""
+    rng = np.random.default_rng(1)
+    for T, K, N in ((5, 72, 64), (70, 200, 136), (300, 1096, 264), (3001, 136, 4160)):
+        x, w, dz = _normal(rng, T, K), _normal(rng, K, N), _normal(rng, T, N)
+        x[T - 1, K - 1], x[0, 3] = float("inf"), float("nan")
+        w[K - 1, N - 1] = float("inf")
+        ws = _space(M, T, K, N)
+        y, dx, dw = torch.empty(T, N, dtype=BF, device="cuda"), torch.empty(T, K, dtype=BF, device="cuda"), torch.empty(K, N, device="cuda")
+        M.moe_linear_fwd(x, w, y, workspace=ws)
+        M.moe_linear_dgrad(dz, w, dx, workspace=ws)
+        M.moe_linear_wgrad(x, dz, dw, workspace=ws)
+        torch.cuda.synchronize()
+        bad = ~torch.isfinite(y)
+        assert bad[0].all() and bad[T - 1].all() and bad[:, N - 1].all()
+        assert not bad[1:T - 1, :N - 1].any()
+        bad = ~torch.isfinite(dx)
+        assert bad[:, K - 1].all() and not bad[:, :K - 1].any()
+        bad = ~torch.isfinite(dw)
+        assert bad[3].all() and bad[K - 1].all()
+        keep = torch.ones(K, dtype=torch.bool)
+        keep[[3, K - 1]] = False
+        assert not bad[keep.cuda()].any()
+
+
+@pytest.mark.parametrize("T, K, N, stage", [(1, 8192, 4096, "f"), (48, 4096, 512, "f"), (200, 8192, 1024, "d"), (8192, 256, 256, "w")])
+def test_captured_products_replay_to_the_eager_bits(M, T, K, N, stage):
+    """Products whose K is split: the joined sums are the same in every replay, with other work between."""
+    rng = np.random.default_rng(T)
+    x, w, dz = _normal(rng, T, K), _normal(rng, K, N, std=0.02), _normal(rng, T, N)
+    ws = _space(M, T, K, N)
+    out = torch.empty({"f": (T, N), "d": (T, K), "w": (K, N)}[stage], dtype=BF, device="cuda")
+    call = {"f": lambda: M.moe_linear_fwd(x, w, out, workspace=ws), "d": lambda: M.moe_linear_dgrad(dz, w, out, workspace=ws),
+            "w": lambda: M.moe_linear_wgrad(x, dz, out, workspace=ws)}[stage]
+    call()
+    torch.cuda.synchronize()
+    want = out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for _ in range(3):
+        out.fill_(float("nan"))
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_large_offsets(M):
+    """Rows and columns whose element offsets pass 2^31: the last rows of a tall input and output."""
+    T, K, N = 140000, 16, 16384                 # y holds 2.3e9 values
+    g = torch.Generator("cuda").manual_seed(2)
+    x = torch.randn(T, K, device="cuda", generator=g).to(BF)
+    w = torch.randn(K, N, device="cuda", generator=g).to(BF)
+    y = torch.empty(T, N, dtype=BF, device="cuda")
+    ws = _space(M, T, K, N)
+    M.moe_linear_fwd(x, w, y, workspace=ws)
+    torch.cuda.synchronize()
+    wv = bf16_values(w)
+    for r in (0, 131071, 131072, T - 1):
+        xv = bf16_values(x[r:r + 1])
+        ref, b = xv @ wv, (K + 2) * U * (np.abs(xv) @ np.abs(wv))
+        _within(bf16_values(y[r:r + 1]), ref, b + H * (np.abs(ref) + b), f"row {r}")
+    q, s = torch.empty(T, N, dtype=torch.uint8, device="cuda"), torch.empty(T, N // 32, dtype=torch.uint8, device="cuda")
+    M.moe_quant_mxfp8(y, M.MOE_QUANT_ROWWISE, q, s)
+    M.moe_dequant_mxfp8(q, s, y)
+    torch.cuda.synchronize()
+    assert np.array_equal(bf16_values(y[-2:]), O.mx_dequant(q[-2:].cpu().numpy(), s[-2:].cpu().numpy()))
+    dy = torch.randn(T, N // 2, device="cuda", generator=g).to(BF)
+    M.moe_act_bwd(dy, y, M.MOE_ACT_SWIGLU, z_q=q, z_s=s)
+    torch.cuda.synchronize()
+    zv = O.mx_dequant(q[-1:].cpu().numpy(), s[-1:].cpu().numpy())
+    dv = bf16_values(dy[-1:])
+    ref = D.act_backward(dv, zv, "swiglu")
+    gt, up = O.deinterleave(zv)
+    e = O.interleave(np.abs(dv * up) * 1.2 * _fn(gt), np.abs(dv * gt) * _fn(gt)) + 4 * U * np.abs(ref)
+    _within(bf16_values(y[-1:]), ref, e + H * (np.abs(ref) + e), "dz")
