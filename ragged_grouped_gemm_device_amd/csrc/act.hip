@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(ActArgs p) {
         for (int i = 0; i < 8; ++i) {
             if constexpr (G) {
                 float f, df;
-                glu_gate_grad<ACT>(z[0][i], f, df);
+                dense_act_grad<ACT>(z[0][i], f, df);
                 a[i] = f * z[1][i];
                 o[0][i] = d[i] * z[1][i] * df;
                 o[1][i] = d[i] * f;

@@ -237,7 +237,7 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& p, f32x16_t (&ac
             static_for<4>([&](auto Q) {
                 float v[4];
 #pragma unroll
-                for (int s = 0; s < 4; ++s) v[s] = glu_gate<ACT>(acc[I][0][4 * Q + s]) * acc[I][1][4 * Q + s];
+                for (int s = 0; s < 4; ++s) v[s] = dense_act<ACT>(acc[I][0][4 * Q + s]) * acc[I][1][4 * Q + s];
                 const int ch = 2 * Q + h;
                 *(float4*)(stg + r * 128 + ((ch ^ (r & 7)) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
             });
@@ -255,7 +255,7 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& p, f32x16_t (&ac
                 static_for<4>([&](auto Q) {
                     float v[4];
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) v[s] = plain_act<ACT>(acc[I][J][4 * Q + s]);
+                    for (int s = 0; s < 4; ++s) v[s] = dense_act<ACT>(acc[I][J][4 * Q + s]);
                     const int ch = 8 * J + 2 * Q + h;
                     *(float4*)(stg + r * 256 + ((ch ^ (r & 15)) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
                 });
@@ -551,8 +551,8 @@ __device__ __forceinline__ void dense_finish8(const DenseArgs& p, int64_t m, int
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if constexpr (kGated<ACT>) y[i] = glu_gate<ACT>(v[0][i]) * v[1][i];
-        else y[i] = plain_act<ACT>(v[0][i]);
+        if constexpr (kGated<ACT>) y[i] = dense_act<ACT>(v[0][i]) * v[1][i];
+        else y[i] = dense_act<ACT>(v[0][i]);
     }
     dense_store8(p, m * NO + 8 * g, y);
 }

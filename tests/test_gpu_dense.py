@@ -339,3 +339,23 @@ def test_large_offsets(M):
     gt, up = O.deinterleave(zv)
     e = O.interleave(np.abs(dv * up) * 1.2 * _fn(gt), np.abs(dv * gt) * _fn(gt)) + 4 * U * np.abs(ref)
     _within(bf16_values(y[-1:]), ref, e + H * (np.abs(ref) + e), "dz")
+
+
+def test_gelu_keeps_its_tail(M):
+    """GELU in fp32 on exact arguments: relative precision far into the negative tail. exp's
+    argument x^2 / 2 is rounded twice (2^-23 of it in all, times log2 e in the base-2 form);
+    polynomial, reciprocal, exponential and products add less than 2^-19."""
+    v = torch.linspace(-12.5, 12.5, 4001).to(BF).cuda()
+    x = torch.zeros(4001, 8, dtype=BF, device="cuda")
+    x[:, 0] = v
+    w = torch.zeros(8, 64, dtype=BF, device="cuda")
+    w[0] = 1.0
+    y = torch.empty(4001, 64, device="cuda")
+    M.moe_linear_fwd(x, w, y, M.MOE_ACT_GELU, workspace=_space(M, 4001, 8, 64))
+    torch.cuda.synchronize()
+    from scipy.special import ndtr
+    vv = bf16_values(v)
+    ref = vv * ndtr(vv)
+    bound = np.abs(ref) * (2.0**-19 + vv * vv / 2 * 2.0**-22)
+    _within(y[:, 0].cpu().numpy(), ref, bound, "gelu")
+    _within(y[:, 63].cpu().numpy(), ref, bound, "gelu")
