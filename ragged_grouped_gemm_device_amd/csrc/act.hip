@@ -160,10 +160,15 @@ __global__ void __launch_bounds__(256) dequant_mxfp8_kernel(const uint8_t* __res
     }
 }
 
-// Row chunks of moe_act_bwd: about 1024 workgroups, at least 8 rows each.
-static void act_chunks(int T, int N, bool gated, int& rows, int& chunks) {
+// Row chunks of moe_act_bwd, at least 8 rows each: about 8192 workgroups, but fewer
+// where each leaves a row of column sums, 1024 of the gated form and 2048 of the others,
+// whose threads have half as much in flight. [16384, 4096] SwiGLU without dbias 59.5 us
+// with 1024 workgroups, 61.0, 56.0, 52.2 with 2048, 4096, 8192; with dbias 62.3, 64.5,
+// 62.3, 62.7. SiLU with dbias 73.3, 68.5, 71.5, 68.8.
+static void act_chunks(int T, int N, bool gated, bool sums, int& rows, int& chunks) {
     const int64_t tiles = ((gated ? N / 2 : N) / 8 + 31) / 32;
-    const int64_t r = ((int64_t)T * tiles + 1023) / 1024;
+    const int64_t target = !sums ? 8192 : gated ? 1024 : 2048;
+    const int64_t r = ((int64_t)T * tiles + target - 1) / target;
     rows = (int)std::max<int64_t>(8, (r + 7) / 8 * 8);
     chunks = (T + rows - 1) / rows;
 }
@@ -172,7 +177,7 @@ size_t act_part_bytes(int T, int N) {
     size_t most = 0;
     for (int gated = 0; gated < 2; ++gated) {
         int rows, chunks;
-        act_chunks(T, N, gated, rows, chunks);
+        act_chunks(T, N, gated, true, rows, chunks);
         most = std::max(most, chunks > 1 ? (size_t)chunks * N * sizeof(float) : 0);
     }
     return most;
@@ -182,7 +187,7 @@ int launch_act_bwd(const uint16_t* dy, const uint16_t* z, const uint8_t* z_q, co
                    int act, uint16_t* dz, uint16_t* a, float* dbias, void* ws, hipStream_t s) {
     const bool gated = act < 2;
     int rows, chunks;
-    act_chunks(T, N, gated, rows, chunks);
+    act_chunks(T, N, gated, dbias != nullptr, rows, chunks);
     ActArgs p{};
     p.dy = dy, p.z = z, p.z_q = z_q, p.z_s = z_s, p.T = T, p.N = N, p.dz = dz, p.a = a, p.rows = rows;
     p.part = !dbias ? nullptr : chunks > 1 ? (float*)ws : dbias;
