@@ -55,8 +55,8 @@ extern "C" {
 
 size_t moe_linear_workspace_bytes(int T, int K, int N, int pass) {
     if (check_linear(T, K, N, MOE_ACT_NONE) != MOE_OK) return 0;
-    const size_t fwd = moe::dense_part_bytes(T, N, K, false);
-    const size_t bwd = std::max({moe::dense_part_bytes(T, K, N, true), moe::linear_wgrad_bytes(T, K, N, true),
+    const size_t fwd = moe::dense_part_bytes(T, N, K, moe::kForward);
+    const size_t bwd = std::max({moe::dense_part_bytes(T, K, N, moe::kDgrad), moe::linear_wgrad_bytes(T, K, N, true),
                                  moe::act_part_bytes(T, N)});
     return std::max(pass & MOE_LINEAR_FWD ? fwd : 0, pass & MOE_LINEAR_BWD ? bwd : 0);
 }
@@ -69,7 +69,7 @@ int moe_linear_fwd(const uint16_t* x, const uint16_t* w, const uint16_t* bias, c
     if (rc != MOE_OK) return rc;
     if (!x || !w || !y || !aligned({x, w, bias, residual, y, z, z_q})) return MOE_ERR_INVALID_ARG;
     if (act == MOE_ACT_NONE && (z || z_q)) return MOE_ERR_INVALID_ARG;
-    if (!has_space(workspace, workspace_bytes, moe::dense_part_bytes(T, N, K, false))) return MOE_ERR_WORKSPACE;
+    if (!has_space(workspace, workspace_bytes, moe::dense_part_bytes(T, N, K, moe::kForward))) return MOE_ERR_WORKSPACE;
     return status(moe::launch_linear_fwd(x, w, bias, residual, T, K, N, act, y_f32, y, z, z_q, z_s, workspace,
                                          S(stream)));
 }
@@ -93,7 +93,7 @@ int moe_linear_dgrad(const uint16_t* dz, const uint16_t* w, const uint16_t* resi
     const int rc = check_linear(T, K, N, MOE_ACT_NONE);
     if (rc != MOE_OK) return rc;
     if (!dz || !w || !dx || !aligned({dz, w, residual, dx})) return MOE_ERR_INVALID_ARG;
-    if (!has_space(workspace, workspace_bytes, moe::dense_part_bytes(T, K, N, true))) return MOE_ERR_WORKSPACE;
+    if (!has_space(workspace, workspace_bytes, moe::dense_part_bytes(T, K, N, moe::kDgrad))) return MOE_ERR_WORKSPACE;
     return status(moe::launch_linear_dgrad(dz, w, residual, T, K, N, dx, workspace, S(stream)));
 }
 

@@ -8,12 +8,11 @@
 // One kernel template: a workgroup owns a BM x BN tile, its wavefronts 32 TM x
 // 64 pieces of it (fp32 accumulators in the MFMA layout); K moves in slabs of 64
 // through ST LDS stages filled by direct global -> LDS copies. With ST = 2 the kernel
-// is persistent; with ST = 4, for products of one round of tiles, a workgroup has one
-// tile and keeps three slabs on their way, which hides the copies' latency where no
-// second workgroup shares the compute unit. Buffer bounds turn
-// everything past the matrices' rows into zeros and a lane whose columns lie past
-// the end uses an offset past every buffer, so any T >= 1 and any K, N that are
-// multiples of 8 take the same path.
+// is persistent; with ST = 3 or 4 a workgroup has one tile and keeps two or three slabs
+// on their way, which hides the copies' latency where no second workgroup shares the
+// compute unit. Buffer bounds turn everything past the matrices' rows into zeros and a
+// lane whose columns lie past the end uses an offset past every buffer, so any T >= 1
+// and any K, N that are multiples of 8 take the same path.
 //
 // The epilogue adds the bias to the fp32 accumulators (z), optionally stores z as
 // bf16 or as MXFP8 codes of its bf16 value, applies the activation to the fp32 z,
@@ -281,7 +280,8 @@ __global__ void __launch_bounds__(WMW * WNW * 64, ST > 2 ? 1 : 2) dense_gemm_ker
     static_assert(TN == 2, "a wavefront owns 64 columns: 32 gate and 32 up columns of a gated layer");
     constexpr int ABYTES = DBM * 128, STAGE = (DBM + DBN) * 128;
     constexpr int LA = ABYTES / (NT * 16), LB = (STAGE - ABYTES) / (NT * 16);
-    static_assert(STAGE >= WMW * WNW * 8192, "the epilogue stages 8 KiB per wavefront in one LDS stage");
+    static_assert((ST == 2 ? 1 : ST) * STAGE >= WMW * WNW * 8192,
+                  "the epilogue stages 8 KiB per wavefront, in one LDS stage where the next tile fills the other");
     __shared__ __attribute__((aligned(1024))) uint8_t s_ab[ST * STAGE];
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(WMW * WNW * 64, ST > 2 ? 1 : 2) dense_gemm_ker
             }
             st = next;
         }
-        dense_epilogue<DBM, DBN, WMW, WNW, TM, TN, ACT>(p, acc, s_ab + (ST == 2 ? st ^ 1 : st == 0 ? ST - 1 : st - 1) * STAGE + wave * 8192, tl.m0, tl.n0,
+        dense_epilogue<DBM, DBN, WMW, WNW, TM, TN, ACT>(p, acc, s_ab + (ST == 2 ? st ^ 1 : 0) * STAGE + wave * 8192, tl.m0, tl.n0,
                                                         tl.split, wm, wn, lane);
         if (!have_next) break;
         tt = tn;
@@ -797,39 +797,42 @@ __global__ void __launch_bounds__(256, 1) dense_small_kernel(DenseArgs p, int ac
 
 // ------------------------------------------------------------------ host side
 // Tile and split of a product: the cheapest by a model of the time (us) fitted to
-// 54 products measured with operands from HBM, between 16 x 704 x 704 and 8192 x 2880
-// x 5760 (it picks the fastest of 14 candidates there, or mostly one within 10%):
-//   64 x 64 tiles (small kernel): a round over the compute units takes 3.0, plus 1.05 for
-//     every slab of a wavefront (a quarter of the split's slabs), 0.55 with at most 32 rows;
-//   128 x 128 tiles: 0.9 a slab for one on a compute unit, 1.05 for two side by side (an
-//     eighth more in the dgrad, which reads W from HBM in 128-byte pieces of its rows), and
-//     4.0 for the prologue and epilogue;
-//   128 x 128 tiles with four LDS stages, one workgroup a compute unit: 0.58 to 0.76 a slab,
-//     4.0 for the prologue and epilogue;
-//   256 x 256 tiles: 1.05 a slab with few of them at work up to 1.7 with all (clock and
-//     L2), and 8 for the prologue and epilogue;
+// 54 products measured with operands from HBM, between 16 x 704 x 704 and 16384 x 7168
+// x 4096 (it picks the fastest of 14 candidates there, or mostly one within 8%):
+//   's' 64 x 64 tiles (small kernel): a round over the compute units takes 3.0, plus 1.05
+//       for every slab of a wavefront (a quarter of the split's slabs), 0.55 with at most
+//       32 rows;
+//   'M' 128 x 128 tiles, two stages: 0.85 a slab for one on a compute unit, 0.95 for two
+//       side by side (an eighth more in the dgrad, which reads W from HBM in 128-byte
+//       pieces of its rows), 3.5 for the prologue and epilogue;
+//   'D' 128 x 128 tiles, four stages, one on a compute unit: 0.53 to 0.73 a slab, 4.0;
+//   'H' 256 x 128 tiles, three stages, one on a compute unit: 0.82 to 0.92 a slab, 5.0 (9.0
+//       in the forward, whose activation no neighbour's products cover: 1000 x 2880 x 5760
+//       51.1 us with GeGLU, M 47.2; without an activation 45.4 and 49.6);
+//   'L' 256 x 256 tiles, two stages: 1.05 a slab with few of them at work up to 1.7 with
+//       all (clock and L2), 8.0;
 //   any: no less than 1.0 and the operands' read, at 5.2 TB/s with every compute unit at
-//     work down to 2.6 with few;
-//   splits: 1.8 for the joining launch and the partial sums' write and read, 3.5 TB/s
-//     for the two together (they mostly stay in the last-level cache).
-// 256 x 128 and 128 x 256 tiles of eight 64 x 64 wavefront pieces were never the fastest
-// (4096 x 2048 x 7168 dgrad: 112.9 us against 107.0 as 128 x 128 tiles).
-// E.g. 2048 x 2048 x 2048: 64 x 64 tiles 40.2 us, 128 x 128 35.2, with four stages 27.7,
-// 256 x 256 52.1; 8192 x 512 x 512: 20.9, 11.6, 10.8, 17.1; 16384 x 512 x 512: 37.9, 14.4,
-// 19.1, 19.1; 4096 x 2048 x 7168: 254, 137, 164, 113.
+//       work down to 2.6 with few;
+//   splits: 1.8 for the joining launch and the partial sums' write and read, 3.5 TB/s for
+//       the two together (they mostly stay in the last-level cache).
+// E.g. forward 2048 x 2048 x 2048: s 40.6 us, M 35.4, D 25.7, H 32.8, L 52.0; forward
+// 16384 x 512 x 512: 37.8, 15.0, 19.2, 15.0, 19.1; dgrad 8192 x 2880 x 5760: 679, 287, 325,
+// 254, 288; forward 4096 x 2048 x 7168: 256, 133, 154, 135, 114. 128 x 256 tiles measured
+// like 256 x 128; with two stages instead of three neither was ever the fastest.
 struct DensePlan {
     char kind;
     int ntm, ntn, splits, split_slabs;
 };
 constexpr int kDenseCus = 256;
 
-static DensePlan dense_plan(int64_t M, int64_t N, int64_t K, bool dgrad) {
+static DensePlan dense_plan(int64_t M, int64_t N, int64_t K, DensePass pass) {
     const int64_t slabs = (K + DBK - 1) / DBK;
     DensePlan best{};
     double least = 0;
-    for (const char kind : {'s', 'M', 'D', 'L'}) {
-        const int64_t e = kind == 's' ? 64 : kind == 'L' ? 256 : 128;
-        const int64_t ntm = (M + e - 1) / e, ntn = (N + e - 1) / e;
+    for (const char kind : {'s', 'M', 'D', 'H', 'L'}) {
+        const int64_t er = kind == 's' ? 64 : kind == 'L' || kind == 'H' ? 256 : 128;
+        const int64_t ec = kind == 's' ? 64 : kind == 'L' ? 256 : 128;
+        const int64_t ntm = (M + er - 1) / er, ntn = (N + ec - 1) / ec;
         for (int64_t want = 1; want <= 16 && want <= slabs; want *= 2) {
             const int64_t ss = (slabs + want - 1) / want, s = (slabs + ss - 1) / ss;
             const int64_t tiles = ntm * ntn * s, rounds = (tiles + kDenseCus - 1) / kDenseCus;
@@ -838,12 +841,14 @@ static DensePlan dense_plan(int64_t M, int64_t N, int64_t K, bool dgrad) {
             if (kind == 's')
                 t = (double)rounds * (3.0 + (M <= 32 ? 0.55 : 1.05) * (double)((ss + 3) / 4));
             else if (kind == 'M')
-                t = (dgrad ? 1.12 : 1.0) * (double)ss * ((double)(rounds / 2) * 1.05 + (double)(rounds % 2) * 0.9) +
-                    4.0 * (double)((rounds + 1) / 2);
+                t = (pass == kDgrad ? 1.12 : 1.0) * (double)ss * ((double)(rounds / 2) * 0.95 + (double)(rounds % 2) * 0.85) +
+                    3.5 * (double)((rounds + 1) / 2);
             else if (kind == 'D')
-                t = (double)rounds * ((double)ss * (0.58 + 0.18 * fill * fill) + 4.0);
-            else
+                t = (double)rounds * ((double)ss * (0.53 + 0.2 * fill * fill) + 4.0);
+            else if (kind == 'L')
                 t = (double)rounds * ((double)ss * (1.05 + 0.65 * fill * fill) + 8.0);
+            else
+                t = (double)rounds * ((double)ss * (0.82 + 0.1 * fill * fill) + (pass == kForward ? 9.0 : 5.0));
             t = std::max(t, 1.0 + (double)(M + N) * (double)K * 2.0 / (5.2e6 * (0.5 + 0.5 * fill)));
             if (s > 1) t += 1.8 + (double)s * (double)M * (double)N * 4.0 / 3.5e6;
             if (best.splits && t >= least) continue;
@@ -854,8 +859,8 @@ static DensePlan dense_plan(int64_t M, int64_t N, int64_t K, bool dgrad) {
     return best;
 }
 
-size_t dense_part_bytes(int64_t M, int64_t N, int64_t K, bool dgrad) {
-    const DensePlan d = dense_plan(M, N, K, dgrad);
+size_t dense_part_bytes(int64_t M, int64_t N, int64_t K, DensePass pass) {
+    const DensePlan d = dense_plan(M, N, K, pass);
     return d.splits > 1 ? (size_t)d.splits * M * N * sizeof(float) : 0;
 }
 
@@ -876,16 +881,17 @@ static void dense_launch(const DensePlan& d, const DenseArgs& a, hipStream_t s) 
     }
     // persistent: as many workgroups as the compute units hold, a multiple of 8; the
     // deep form runs one tile per workgroup
-    const int most = d.kind == 'D' ? total : device_cus() * (d.kind == 'M' ? 2 : 1);
+    const int most = d.kind == 'M' ? 2 * device_cus() : d.kind == 'L' ? device_cus() : total;
     const unsigned grid = (unsigned)((std::min(total, most) + 7) / 8 * 8);
     if (d.kind == 'L') dense_gemm_kernel<256, 256, 2, 4, 2, A_KMAJ, B_KMAJ, ACT><<<grid, 512, 0, s>>>(a);
     else if (d.kind == 'D') dense_gemm_kernel<128, 128, 2, 2, 4, A_KMAJ, B_KMAJ, ACT><<<grid, 256, 0, s>>>(a);
+    else if (d.kind == 'H') dense_gemm_kernel<256, 128, 4, 2, 3, A_KMAJ, B_KMAJ, ACT><<<grid, 512, 0, s>>>(a);
     else dense_gemm_kernel<128, 128, 2, 2, 2, A_KMAJ, B_KMAJ, ACT><<<grid, 256, 0, s>>>(a);
 }
 
 template <bool A_KMAJ, bool B_KMAJ, int ACT>
 static int dense_run(DenseArgs a, void* ws, hipStream_t s) {
-    const DensePlan d = dense_plan(a.M, a.N, a.K, B_KMAJ);
+    const DensePlan d = dense_plan(a.M, a.N, a.K, !A_KMAJ ? kWgrad : B_KMAJ ? kDgrad : kForward);
     a.ntm = d.ntm;
     a.ntn = d.ntn;
     a.splits = d.splits;
@@ -935,11 +941,11 @@ int launch_linear_dgrad(const uint16_t* dz, const uint16_t* w, const uint16_t* r
 // more than the copy (16384 x 7168 x 4096: 892 us with the copy, 1260 converted in the
 // loop, 876 from bf16; 200 x 1024 x 1024: 13.1, 9.9, 10.2).
 static size_t dense_copy_bytes(int64_t T, int64_t K, int64_t N) {
-    return K % 32 || dense_plan(K, N, T, false).kind == 's' ? 0 : (size_t)((T * K * 2 + 255) / 256 * 256);
+    return K % 32 || dense_plan(K, N, T, kWgrad).kind == 's' ? 0 : (size_t)((T * K * 2 + 255) / 256 * 256);
 }
 
 size_t linear_wgrad_bytes(int T, int K, int N, bool x8) {
-    return (x8 ? dense_copy_bytes(T, K, N) : 0) + dense_part_bytes(K, N, T, false);
+    return (x8 ? dense_copy_bytes(T, K, N) : 0) + dense_part_bytes(K, N, T, kWgrad);
 }
 
 int launch_linear_wgrad(const uint16_t* x, const uint8_t* x_q, const uint8_t* x_s, const uint16_t* dz, int T,
