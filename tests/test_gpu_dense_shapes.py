@@ -41,7 +41,15 @@ def _close(got, ref, bound, what):
     assert not bad.any(), (what, int(bad.sum()), bad.nonzero()[:3].tolist())
 
 
+# shapes for which each tile form (and its split) is chosen for one of the three products
+CHOSEN = [(5000, 3000, 1000), (600, 4096, 8192), (136, 3000, 4160), (3001, 4160, 136), (1030, 1544, 2880),
+          (2048, 2048, 2048), (4096, 2048, 4096), (1020, 2880, 5760), (2300, 4096, 2304), (1100, 2056, 1152),
+          (1500, 1032, 2112), (4100, 136, 1088), (20, 4168, 4104), (300, 4096, 64), (600, 8192, 8192)]
+
+
 def _shape(rng, i):
+    if i >= 48:
+        return CHOSEN[i - 48]
     log = lambda lo, hi, step: max(step, int(lo * (hi / lo) ** rng.random()) // step * step)  # noqa: E731
     if i % 4 == 0:
         return log(1, 80, 1), log(8, 6000, 8), log(8, 6000, 8)       # few rows
@@ -50,10 +58,11 @@ def _shape(rng, i):
     return log(8, 3000, 1), log(8, 3000, 8), log(8, 3000, 8)
 
 
-@pytest.mark.parametrize("i", range(48))
+@pytest.mark.parametrize("i", range(48 + len(CHOSEN)))
 def test_random_shapes(M, i):
     rng = random.Random(i)
     T, K, N = _shape(rng, i)
+    rng.random()
     act, srelu = ("srelu", True) if rng.random() < 0.5 else ("none", False)
     print(f"shape {i}: T={T} K={K} N={N} act={act}", flush=True)
     g = torch.Generator("cuda").manual_seed(i)
@@ -160,3 +169,33 @@ def test_random_losses_keep_to_their_buffers(M, i):
     got = o["d"][lo:hi].double().sum(1)
     scale = o["d"][lo:hi].double().abs().sum(1)
     assert ((got - want).abs() <= 2.0**-16 * (scale + want.abs()) + 1e-30).all()
+
+
+@pytest.mark.parametrize("T, K, N", CHOSEN)
+def test_gated_epilogue_of_every_tile_form(M, T, K, N):
+    """SwiGLU with bias, residual and 8-bit checkpoint where each tile form runs: z against 64 bits,
+    y against f of the fp32 sums (f and its slope in g are bounded by |g| and 1.1; the exponential is
+    off by (2 |g| + 2) 2^-23), codes against the quantizer."""
+    N = N // 64 * 64
+    g = torch.Generator("cuda").manual_seed(T)
+    new = lambda *s, std=1.0: (torch.randn(*s, device="cuda", generator=g) * std).to(BF)  # noqa: E731
+    x, w, b, r = new(T, K), new(K, N, std=K**-0.5), new(N), new(T, N // 2)
+    y, z = Guarded((T, N // 2), BF), Guarded((T, N), BF)
+    zq, zs = Guarded((T, N), torch.uint8), Guarded((T, N // 32), torch.uint8)
+    ws = Guarded((max(16, M.moe_linear_workspace_bytes(T, K, N)),), torch.uint8)
+    M.moe_linear_fwd(x, w, y.t, M.MOE_ACT_SWIGLU, b, r, z=z.t, z_q=zq.t, z_s=zs.t, workspace=ws.t)
+    q, s = torch.empty_like(zq.t), torch.empty_like(zs.t)
+    M.moe_quant_mxfp8(z.t, M.MOE_QUANT_ROWWISE, q, s)
+    torch.cuda.synchronize()
+    assert all(o.whole() for o in (y, z, zq, zs, ws))
+    assert torch.equal(q, zq.t) and torch.equal(s, zs.t)
+    z0 = x.double() @ w.double() + b.double()
+    zb = (K + 2) * U * (x.double().abs() @ w.double().abs() + b.double().abs())
+    _close(z.t, z0, zb + H * (z0.abs() + zb), "z")
+    halves = lambda v: [v.reshape(T, -1, 2, 32)[:, :, j].reshape(T, -1) for j in (0, 1)]  # noqa: E731
+    (gt, up), (gb, ub) = halves(z0), halves(zb)
+    f = gt * torch.sigmoid(gt)
+    fb = 1.2 * gb + (2 * gt.abs() + 8) * 2 * U * gt.abs()
+    ref = f * up + r.double()
+    bound = fb * (up.abs() + ub) + f.abs() * ub + 4 * U * (f * up).abs() + 2 * U * r.double().abs()
+    _close(y.t, ref, bound + H * (ref.abs() + bound), "y")
