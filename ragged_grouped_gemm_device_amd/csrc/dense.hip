@@ -44,6 +44,9 @@ struct DenseArgs {
     uint8_t* z_q;  // [M, N] codes, [M, N / 32] scales, or nullptr
     uint8_t* z_s;
     float* part;  // [splits, M, N] raw sums instead of an epilogue, or nullptr
+    // with tail_splits > 1: tiles from tail_first on have K cut into tail_splits pieces of
+    // tail_slabs, whose raw sums go to part as [piece][tile - tail_first][rows, columns]
+    int tail_first, tail_splits, tail_slabs;
     int stream;   // outputs past the caches
 };
 
@@ -159,7 +162,7 @@ __device__ __forceinline__ void wait_barrier() {
 // covers whole row runs; 16-byte chunks are XOR-swizzled by the row.
 template <int DBM, int DBN, int WMW, int WNW, int TM, int TN, int ACT>
 __device__ __forceinline__ void dense_epilogue(const DenseArgs& p, f32x16_t (&acc)[TM][TN], uint8_t* stg, int m0,
-                                               int n0, int split, int wm, int wn, int lane) {
+                                               int n0, int split, int tail, int wm, int wn, int lane) {
     // every wavefront has read the last slab out of the stage
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
     const int h = lane >> 5, r = lane & 31;
@@ -169,7 +172,7 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& p, f32x16_t (&ac
     static_for<TM>([&](auto I) {
         const int mb = m0 + wm * 32 * TM + 32 * I;
         if (mb >= p.M) return;
-        if (ACT == 3 && p.part) {  // raw sums of this split
+        if (ACT == 3 && (p.splits > 1 || tail >= 0)) {  // raw sums of this split
             static_for<TN>([&](auto J) {
                 static_for<4>([&](auto Q) {
                     const int ch = 8 * J + 2 * Q + h;
@@ -178,12 +181,14 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& p, f32x16_t (&ac
                 });
             });
             wave_lds_sync();
-            float* out = p.part + (int64_t)split * p.M * p.N;
+            float* out = tail >= 0 ? p.part + (int64_t)tail * DBM * DBN - ((int64_t)m0 * DBN + n0)
+                                   : p.part + (int64_t)split * p.M * p.N;
+            const int64_t ld = tail >= 0 ? DBN : p.N;
             static_for<8>([&](auto It) {
                 const int R = 4 * It + (lane >> 4), c = lane & 15;
                 const float4 v = *(const float4*)(stg + R * 256 + ((c ^ (R & 15)) << 4));
                 const int m = mb + R, col = col0 + 4 * c;
-                if (m < p.M && col < p.N) *(float4*)(out + (int64_t)m * p.N + col) = v;
+                if (m < p.M && col < p.N) *(float4*)(out + (int64_t)m * ld + col) = v;
             });
             wave_lds_sync();
             return;
@@ -292,23 +297,37 @@ __global__ void __launch_bounds__(WMW * WNW * 64, ST > 2 ? 1 : 2) dense_gemm_ker
     // kernel is persistent: round r covers tiles [r nb, (r + 1) nb), of which each XCD
     // (workgroups are dealt round robin to 8) takes a contiguous eighth, so that its
     // L2 holds a window's operand panels.
-    const int per = p.ntm * p.ntn, total = per * p.splits;
+    // A last round that would leave most compute units idle has its tiles' K cut into
+    // pieces instead (gradient products on large tiles).
+    constexpr bool TAIL = ACT == 3 && ST == 2 && DBM == 256;
+    const int per = p.ntm * p.ntn;
+    const int total = TAIL && p.tail_splits > 1 ? p.tail_first + (per - p.tail_first) * p.tail_splits : per * p.splits;
     const int nb = gridDim.x;  // a multiple of 8
     const int first = (blockIdx.x & 7) * (nb >> 3) + (blockIdx.x >> 3);
     const int slabs = (p.K + DBK - 1) / DBK;
     struct Tile {
-        int m0, n0, split, ks0, nk;
+        int m0, n0, split, tail, ks0, nk;
     };
     auto get_tile = [&](int tt) -> Tile {
         Tile tl;
-        tl.split = __builtin_amdgcn_readfirstlane(tt / per);
-        const int t = tt - tl.split * per;
+        int t, each = p.split_slabs;
+        if (TAIL && p.tail_splits > 1) {
+            const int v = tt - p.tail_first, rem = per - p.tail_first;
+            tl.tail = v < 0 ? -1 : v;
+            tl.split = v < 0 ? 0 : __builtin_amdgcn_readfirstlane(v / rem);
+            t = v < 0 ? tt : p.tail_first + v - tl.split * rem;
+            if (v >= 0) each = p.tail_slabs;
+        } else {
+            tl.tail = -1;
+            tl.split = __builtin_amdgcn_readfirstlane(tt / per);
+            t = tt - tl.split * per;
+        }
         const int band = t / (4 * p.ntn), within = t - band * 4 * p.ntn;
         const int bm = min(4, p.ntm - band * 4);
         tl.m0 = __builtin_amdgcn_readfirstlane((band * 4 + within % bm) * DBM);
         tl.n0 = __builtin_amdgcn_readfirstlane((within / bm) * DBN);
-        tl.ks0 = tl.split * p.split_slabs;
-        tl.nk = min(p.split_slabs, slabs - tl.ks0);
+        tl.ks0 = tl.split * each;
+        tl.nk = min(each, slabs - tl.ks0);
         return tl;
     };
 
@@ -499,7 +518,7 @@ __global__ void __launch_bounds__(WMW * WNW * 64, ST > 2 ? 1 : 2) dense_gemm_ker
             st = next;
         }
         dense_epilogue<DBM, DBN, WMW, WNW, TM, TN, ACT>(p, acc, s_ab + (ST == 2 ? st ^ 1 : 0) * STAGE + wave * 8192, tl.m0, tl.n0,
-                                                        tl.split, wm, wn, lane);
+                                                        tl.split, tl.tail, wm, wn, lane);
         if (!have_next) break;
         tt = tn;
         tl = tl_next;
@@ -602,6 +621,30 @@ __global__ void __launch_bounds__(256) dense_join_kernel(DenseArgs p) {
             for (int k = 1; k < L; ++k) v[i >> 3][i & 7] += s_v[k][gi * (8 * H + 1) + i];
     }
     if (on) dense_finish8<ACT>(p, m, g, v);
+}
+
+// Joins the pieces of the last round's tiles (256 x 256): a thread adds 8 columns of a
+// row, piece order.
+__global__ void __launch_bounds__(256) dense_tail_join_kernel(DenseArgs p) {
+    const int rem = p.ntm * p.ntn - p.tail_first;
+    const int r = blockIdx.x >> 5;  // 32 workgroups a tile, 8 rows each
+    const int t = p.tail_first + r;
+    const int band = t / (4 * p.ntn), within = t - band * 4 * p.ntn;
+    const int bm = min(4, p.ntm - band * 4);
+    const int row = (blockIdx.x & 31) * 8 + (threadIdx.x >> 5), c = (threadIdx.x & 31) * 8;
+    const int64_t m = (int64_t)(band * 4 + within % bm) * 256 + row;
+    const int col = within / bm * 256 + c;
+    if (m >= p.M || col >= p.N) return;
+    const float* at = p.part + ((int64_t)r * 256 + row) * 256 + c;
+    const int64_t step = (int64_t)rem * 65536;
+    float v[2][8] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.tail_splits; ++s) {
+        const float4 a = *(const float4*)(at + s * step), b = *(const float4*)(at + s * step + 4);
+        v[0][0] += a.x, v[0][1] += a.y, v[0][2] += a.z, v[0][3] += a.w;
+        v[0][4] += b.x, v[0][5] += b.y, v[0][6] += b.z, v[0][7] += b.w;
+    }
+    dense_finish8<3>(p, m, col / 8, v);
 }
 
 // ------------------------------------------------------------------ small products
@@ -822,6 +865,7 @@ __global__ void __launch_bounds__(256, 1) dense_small_kernel(DenseArgs p, int ac
 struct DensePlan {
     char kind;
     int ntm, ntn, splits, split_slabs;
+    int tail_first, tail_splits, tail_slabs;  // tail_splits > 1: see DenseArgs
 };
 constexpr int kDenseCus = 256;
 
@@ -853,20 +897,39 @@ static DensePlan dense_plan(int64_t M, int64_t N, int64_t K, DensePass pass) {
             if (s > 1) t += 1.8 + (double)s * (double)M * (double)N * 4.0 / 3.5e6;
             if (best.splits && t >= least) continue;
             least = t;
-            best = {kind, (int)ntm, (int)ntn, (int)s, (int)ss};
+            best = {kind, (int)ntm, (int)ntn, (int)s, (int)ss, 0, 1, 0};
+        }
+        // a part of a round left over: its tiles' K in pieces over all compute units
+        const int64_t tiles = ntm * ntn, whole = tiles / kDenseCus, rem = tiles % kDenseCus;
+        if (kind != 'L' || pass == kForward || whole == 0 || rem == 0) continue;
+        for (int64_t want = 2; want <= 16 && want <= slabs; ++want) {
+            const int64_t ss = (slabs + want - 1) / want, s = (slabs + ss - 1) / ss;
+            const int64_t units = rem * s, rounds = (units + kDenseCus - 1) / kDenseCus;
+            const double fill = std::min(1.0, (double)units / kDenseCus);
+            const double t = (double)whole * ((double)slabs * 1.7 + 8.0) +
+                             (double)rounds * ((double)ss * (1.05 + 0.65 * fill * fill) + 8.0) + 1.8 +
+                             (double)units * 65536.0 * 4.0 / 3.5e6;
+            if (t >= least) continue;
+            least = t;
+            best = {kind, (int)ntm, (int)ntn, 1, (int)slabs, (int)(whole * kDenseCus), (int)s, (int)ss};
         }
     }
     return best;
 }
 
+static int tiles_left(const DensePlan& d) { return d.ntm * d.ntn - d.tail_first; }
+
 size_t dense_part_bytes(int64_t M, int64_t N, int64_t K, DensePass pass) {
     const DensePlan d = dense_plan(M, N, K, pass);
+    if (d.tail_splits > 1)
+        return (size_t)tiles_left(d) * d.tail_splits * 65536 * sizeof(float);
     return d.splits > 1 ? (size_t)d.splits * M * N * sizeof(float) : 0;
 }
 
 template <bool A_KMAJ, bool B_KMAJ, int ACT>
 static void dense_launch(const DensePlan& d, const DenseArgs& a, hipStream_t s) {
-    const int total = d.ntm * d.ntn * d.splits;
+    const int tiles = d.ntm * d.ntn;
+    const int total = d.tail_splits > 1 ? d.tail_first + (tiles - d.tail_first) * d.tail_splits : tiles * d.splits;
     if (d.kind == 's') {
         const unsigned grid = (unsigned)total;
         if constexpr (A_KMAJ) {
@@ -897,9 +960,11 @@ static int dense_run(DenseArgs a, void* ws, hipStream_t s) {
     a.splits = d.splits;
     a.split_slabs = d.split_slabs;
     a.stream = (int64_t)a.M * a.N * (a.out_f32 ? 4 : 2) >= kDenseStreamBytes;
+    a.tail_first = d.tail_first, a.tail_splits = d.tail_splits, a.tail_slabs = d.tail_slabs;
     if (d.splits == 1) {
-        a.part = nullptr;
+        a.part = d.tail_splits > 1 ? (float*)ws : nullptr;
         dense_launch<A_KMAJ, B_KMAJ, ACT>(d, a, s);
+        if (d.tail_splits > 1) dense_tail_join_kernel<<<(unsigned)(tiles_left(d) * 32), 256, 0, s>>>(a);
     } else {
         a.part = (float*)ws;
         dense_launch<A_KMAJ, B_KMAJ, 3>(d, a, s);
