@@ -155,12 +155,38 @@ __device__ __forceinline__ void wait_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
 
+// The epilogue's other form: the raw sums of a piece of K, to `out` [row][col] of row
+// length `ld`.
+template <int TM, int TN>
+__device__ __forceinline__ void dense_raw_sums(const DenseArgs& p, f32x16_t (&acc)[TM][TN], uint8_t* stg, float* out,
+                                               int64_t ld, int mb, int col0, int lane) {
+    const int h = lane >> 5, r = lane & 31;
+    static_for<TM>([&](auto I) {
+        if (mb + 32 * I >= p.M) return;
+        static_for<TN>([&](auto J) {
+            static_for<4>([&](auto Q) {
+                const int ch = 8 * J + 2 * Q + h;
+                *(float4*)(stg + r * 256 + ((ch ^ (r & 15)) << 4)) = make_float4(
+                    acc[I][J][4 * Q], acc[I][J][4 * Q + 1], acc[I][J][4 * Q + 2], acc[I][J][4 * Q + 3]);
+            });
+        });
+        wave_lds_sync();
+        static_for<8>([&](auto It) {
+            const int R = 4 * It + (lane >> 4), c = lane & 15;
+            const float4 v = *(const float4*)(stg + R * 256 + ((c ^ (R & 15)) << 4));
+            const int m = mb + 32 * I + R, col = col0 + 4 * c;
+            if (m < p.M && col < p.N) *(float4*)(out + (int64_t)m * ld + col) = v;
+        });
+        wave_lds_sync();
+    });
+}
+
 // The epilogue of one wavefront's piece of a tile. Lane l holds row l & 31 of each 32
 // x 32 block and, in register 4 Q + s, column 8 Q + 4 h + s, h = l >> 5. Values leave
 // through the wavefront's 8 KiB of the LDS stage `stg` that the tile no longer reads
 // (the next tile's first slab goes to the other one), so that a store instruction
 // covers whole row runs; 16-byte chunks are XOR-swizzled by the row.
-template <int DBM, int DBN, int WMW, int WNW, int TM, int TN, int ACT>
+template <int DBM, int DBN, int WMW, int WNW, int TM, int TN, int ACT, bool TAIL>
 __device__ __forceinline__ void dense_epilogue(const DenseArgs& p, f32x16_t (&acc)[TM][TN], uint8_t* stg, int m0,
                                                int n0, int split, int tail, int wm, int wn, int lane) {
     // every wavefront has read the last slab out of the stage
@@ -168,31 +194,16 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& p, f32x16_t (&ac
     const int h = lane >> 5, r = lane & 31;
     const int col0 = n0 + wn * 64;
     if (col0 >= p.N) return;
+    const int mb0 = m0 + wm * 32 * TM;
+    if (TAIL && tail >= 0)
+        return dense_raw_sums(p, acc, stg, p.part + (int64_t)tail * DBM * DBN - ((int64_t)m0 * DBN + n0), DBN, mb0,
+                              col0, lane);
+    if (ACT == 3 && p.splits > 1)
+        return dense_raw_sums(p, acc, stg, p.part + (int64_t)split * p.M * p.N, p.N, mb0, col0, lane);
     const int NO = kGated<ACT> ? p.N / 2 : p.N;
     static_for<TM>([&](auto I) {
-        const int mb = m0 + wm * 32 * TM + 32 * I;
+        const int mb = mb0 + 32 * I;
         if (mb >= p.M) return;
-        if (ACT == 3 && (p.splits > 1 || tail >= 0)) {  // raw sums of this split
-            static_for<TN>([&](auto J) {
-                static_for<4>([&](auto Q) {
-                    const int ch = 8 * J + 2 * Q + h;
-                    *(float4*)(stg + r * 256 + ((ch ^ (r & 15)) << 4)) = make_float4(
-                        acc[I][J][4 * Q], acc[I][J][4 * Q + 1], acc[I][J][4 * Q + 2], acc[I][J][4 * Q + 3]);
-                });
-            });
-            wave_lds_sync();
-            float* out = tail >= 0 ? p.part + (int64_t)tail * DBM * DBN - ((int64_t)m0 * DBN + n0)
-                                   : p.part + (int64_t)split * p.M * p.N;
-            const int64_t ld = tail >= 0 ? DBN : p.N;
-            static_for<8>([&](auto It) {
-                const int R = 4 * It + (lane >> 4), c = lane & 15;
-                const float4 v = *(const float4*)(stg + R * 256 + ((c ^ (R & 15)) << 4));
-                const int m = mb + R, col = col0 + 4 * c;
-                if (m < p.M && col < p.N) *(float4*)(out + (int64_t)m * ld + col) = v;
-            });
-            wave_lds_sync();
-            return;
-        }
         if (p.bias) {
             static_for<TN>([&](auto J) {
                 static_for<4>([&](auto Q) {
@@ -278,7 +289,7 @@ __device__ __forceinline__ void dense_epilogue(const DenseArgs& p, f32x16_t (&ac
     });
 }
 
-template <int DBM, int DBN, int WMW, int WNW, int ST, bool A_KMAJ, bool B_KMAJ, int ACT>
+template <int DBM, int DBN, int WMW, int WNW, int ST, bool A_KMAJ, bool B_KMAJ, int ACT, bool TAIL = false>
 __global__ void __launch_bounds__(WMW * WNW * 64, ST > 2 ? 1 : 2) dense_gemm_kernel(DenseArgs p) {
     constexpr int NT = WMW * WNW * 64;
     constexpr int TM = DBM / (32 * WMW), TN = DBN / (32 * WNW);
@@ -297,11 +308,11 @@ __global__ void __launch_bounds__(WMW * WNW * 64, ST > 2 ? 1 : 2) dense_gemm_ker
     // kernel is persistent: round r covers tiles [r nb, (r + 1) nb), of which each XCD
     // (workgroups are dealt round robin to 8) takes a contiguous eighth, so that its
     // L2 holds a window's operand panels.
-    // A last round that would leave most compute units idle has its tiles' K cut into
-    // pieces instead (gradient products on large tiles).
-    constexpr bool TAIL = ACT == 3 && ST == 2 && DBM == 256;
+    // TAIL: a last round that would leave many compute units idle has its tiles' K cut
+    // into pieces instead. A form of its own: with the raw sums' branch in it the
+    // epilogue spills up to 34 registers (SwiGLU 32768 x 8192 x 4096: 1840 us, 1800).
     const int per = p.ntm * p.ntn;
-    const int total = TAIL && p.tail_splits > 1 ? p.tail_first + (per - p.tail_first) * p.tail_splits : per * p.splits;
+    const int total = TAIL ? p.tail_first + (per - p.tail_first) * p.tail_splits : per * p.splits;
     const int nb = gridDim.x;  // a multiple of 8
     const int first = (blockIdx.x & 7) * (nb >> 3) + (blockIdx.x >> 3);
     const int slabs = (p.K + DBK - 1) / DBK;
@@ -311,7 +322,7 @@ __global__ void __launch_bounds__(WMW * WNW * 64, ST > 2 ? 1 : 2) dense_gemm_ker
     auto get_tile = [&](int tt) -> Tile {
         Tile tl;
         int t, each = p.split_slabs;
-        if (TAIL && p.tail_splits > 1) {
+        if (TAIL) {
             const int v = tt - p.tail_first, rem = per - p.tail_first;
             tl.tail = v < 0 ? -1 : v;
             tl.split = v < 0 ? 0 : __builtin_amdgcn_readfirstlane(v / rem);
@@ -517,8 +528,8 @@ __global__ void __launch_bounds__(WMW * WNW * 64, ST > 2 ? 1 : 2) dense_gemm_ker
             }
             st = next;
         }
-        dense_epilogue<DBM, DBN, WMW, WNW, TM, TN, ACT>(p, acc, s_ab + (ST == 2 ? st ^ 1 : 0) * STAGE + wave * 8192, tl.m0, tl.n0,
-                                                        tl.split, tl.tail, wm, wn, lane);
+        dense_epilogue<DBM, DBN, WMW, WNW, TM, TN, ACT, TAIL>(p, acc, s_ab + (ST == 2 ? st ^ 1 : 0) * STAGE + wave * 8192,
+                                                              tl.m0, tl.n0, tl.split, tl.tail, wm, wn, lane);
         if (!have_next) break;
         tt = tn;
         tl = tl_next;
@@ -623,28 +634,35 @@ __global__ void __launch_bounds__(256) dense_join_kernel(DenseArgs p) {
     if (on) dense_finish8<ACT>(p, m, g, v);
 }
 
-// Joins the pieces of the last round's tiles (256 x 256): a thread adds 8 columns of a
-// row, piece order.
+// Joins the pieces of the last round's tiles (256 x 256): a thread adds 8 output
+// columns of a row (gated: their gate and up columns), piece order; then the epilogue.
+template <int ACT>
 __global__ void __launch_bounds__(256) dense_tail_join_kernel(DenseArgs p) {
+    constexpr int H = kGated<ACT> ? 2 : 1, G = 32 / H;  // groups of 8 outputs in a tile's row
+    constexpr int RB = 256 / G;                         // rows a workgroup
     const int rem = p.ntm * p.ntn - p.tail_first;
-    const int r = blockIdx.x >> 5;  // 32 workgroups a tile, 8 rows each
+    const int r = blockIdx.x / (256 / RB);
     const int t = p.tail_first + r;
     const int band = t / (4 * p.ntn), within = t - band * 4 * p.ntn;
     const int bm = min(4, p.ntm - band * 4);
-    const int row = (blockIdx.x & 31) * 8 + (threadIdx.x >> 5), c = (threadIdx.x & 31) * 8;
+    const int row = blockIdx.x % (256 / RB) * RB + threadIdx.x / G, g = threadIdx.x % G;
+    const int c = kGated<ACT> ? (g >> 2) * 64 + (g & 3) * 8 : g * 8;
     const int64_t m = (int64_t)(band * 4 + within % bm) * 256 + row;
-    const int col = within / bm * 256 + c;
-    if (m >= p.M || col >= p.N) return;
+    const int n0 = within / bm * 256;
+    if (m >= p.M || n0 + c >= p.N) return;
     const float* at = p.part + ((int64_t)r * 256 + row) * 256 + c;
     const int64_t step = (int64_t)rem * 65536;
     float v[2][8] = {};
 #pragma unroll 4
     for (int s = 0; s < p.tail_splits; ++s) {
-        const float4 a = *(const float4*)(at + s * step), b = *(const float4*)(at + s * step + 4);
-        v[0][0] += a.x, v[0][1] += a.y, v[0][2] += a.z, v[0][3] += a.w;
-        v[0][4] += b.x, v[0][5] += b.y, v[0][6] += b.z, v[0][7] += b.w;
+#pragma unroll
+        for (int u = 0; u < H; ++u) {
+            const float4 a = *(const float4*)(at + s * step + 32 * u), b = *(const float4*)(at + s * step + 32 * u + 4);
+            v[u][0] += a.x, v[u][1] += a.y, v[u][2] += a.z, v[u][3] += a.w;
+            v[u][4] += b.x, v[u][5] += b.y, v[u][6] += b.z, v[u][7] += b.w;
+        }
     }
-    dense_finish8<3>(p, m, col / 8, v);
+    dense_finish8<ACT>(p, m, n0 / (8 * H) + g, v);
 }
 
 // ------------------------------------------------------------------ small products
@@ -857,7 +875,11 @@ __global__ void __launch_bounds__(256, 1) dense_small_kernel(DenseArgs p, int ac
 //   any: no less than 1.0 and the operands' read, at 5.2 TB/s with every compute unit at
 //       work down to 2.6 with few;
 //   splits: 1.8 for the joining launch and the partial sums' write and read, 3.5 TB/s for
-//       the two together (they mostly stay in the last-level cache).
+//       the two together (they mostly stay in the last-level cache);
+//   'L' with a part of a round left over: only those tiles' K in pieces (wgrad 8192 x 2880
+//       x 5760, 276 tiles: 261 us, 370 as two rounds, 346 as M; 32768 x 2880 x 5760: 936,
+//       1506, 1460; forward 4300 x 6000 x 4160: 222, 302 as two rounds; 9000 x 2880 x 5760:
+//       259, 267; dgrad 4300 x 4104 x 4160: 147, 187).
 // E.g. forward 2048 x 2048 x 2048: s 40.6 us, M 35.4, D 25.7, H 32.8, L 52.0; forward
 // 16384 x 512 x 512: 37.8, 15.0, 19.2, 15.0, 19.1; dgrad 8192 x 2880 x 5760: 679, 287, 325,
 // 254, 288; forward 4096 x 2048 x 7168: 256, 133, 154, 135, 114. 128 x 256 tiles measured
@@ -901,7 +923,7 @@ static DensePlan dense_plan(int64_t M, int64_t N, int64_t K, DensePass pass) {
         }
         // a part of a round left over: its tiles' K in pieces over all compute units
         const int64_t tiles = ntm * ntn, whole = tiles / kDenseCus, rem = tiles % kDenseCus;
-        if (kind != 'L' || pass == kForward || whole == 0 || rem == 0) continue;
+        if (kind != 'L' || whole == 0 || rem == 0) continue;
         for (int64_t want = 2; want <= 16 && want <= slabs; ++want) {
             const int64_t ss = (slabs + want - 1) / want, s = (slabs + ss - 1) / ss;
             const int64_t units = rem * s, rounds = (units + kDenseCus - 1) / kDenseCus;
@@ -946,7 +968,8 @@ static void dense_launch(const DensePlan& d, const DenseArgs& a, hipStream_t s) 
     // deep form runs one tile per workgroup
     const int most = d.kind == 'M' ? 2 * device_cus() : d.kind == 'L' ? device_cus() : total;
     const unsigned grid = (unsigned)((std::min(total, most) + 7) / 8 * 8);
-    if (d.kind == 'L') dense_gemm_kernel<256, 256, 2, 4, 2, A_KMAJ, B_KMAJ, ACT><<<grid, 512, 0, s>>>(a);
+    if (d.tail_splits > 1) dense_gemm_kernel<256, 256, 2, 4, 2, A_KMAJ, B_KMAJ, ACT, true><<<grid, 512, 0, s>>>(a);
+    else if (d.kind == 'L') dense_gemm_kernel<256, 256, 2, 4, 2, A_KMAJ, B_KMAJ, ACT><<<grid, 512, 0, s>>>(a);
     else if (d.kind == 'D') dense_gemm_kernel<128, 128, 2, 2, 4, A_KMAJ, B_KMAJ, ACT><<<grid, 256, 0, s>>>(a);
     else if (d.kind == 'H') dense_gemm_kernel<256, 128, 4, 2, 3, A_KMAJ, B_KMAJ, ACT><<<grid, 512, 0, s>>>(a);
     else dense_gemm_kernel<128, 128, 2, 2, 2, A_KMAJ, B_KMAJ, ACT><<<grid, 256, 0, s>>>(a);
@@ -964,7 +987,8 @@ static int dense_run(DenseArgs a, void* ws, hipStream_t s) {
     if (d.splits == 1) {
         a.part = d.tail_splits > 1 ? (float*)ws : nullptr;
         dense_launch<A_KMAJ, B_KMAJ, ACT>(d, a, s);
-        if (d.tail_splits > 1) dense_tail_join_kernel<<<(unsigned)(tiles_left(d) * 32), 256, 0, s>>>(a);
+        if (d.tail_splits > 1)
+            dense_tail_join_kernel<ACT><<<(unsigned)(tiles_left(d) * (kGated<ACT> ? 16 : 32)), 256, 0, s>>>(a);
     } else {
         a.part = (float*)ws;
         dense_launch<A_KMAJ, B_KMAJ, 3>(d, a, s);

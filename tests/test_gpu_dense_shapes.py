@@ -44,7 +44,8 @@ def _close(got, ref, bound, what):
 # shapes for which each tile form (and its split) is chosen for one of the three products
 CHOSEN = [(5000, 3000, 1000), (600, 4096, 8192), (136, 3000, 4160), (3001, 4160, 136), (1030, 1544, 2880),
           (2048, 2048, 2048), (4096, 2048, 4096), (1020, 2880, 5760), (2300, 4096, 2304), (1100, 2056, 1152),
-          (1500, 1032, 2112), (4100, 136, 1088), (20, 4168, 4104), (300, 4096, 64), (600, 8192, 8192), (6000, 4200, 4104), (4200, 4200, 6000)]
+          (1500, 1032, 2112), (4100, 136, 1088), (20, 4168, 4104), (300, 4096, 64), (600, 8192, 8192),
+          (6000, 4200, 4104), (4200, 4200, 6000), (4300, 4104, 4168), (4996, 4000, 4160)]
 
 
 def _shape(rng, i):
