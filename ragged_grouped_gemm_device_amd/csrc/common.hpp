@@ -101,11 +101,11 @@ __device__ __forceinline__ void normal_cdf(float x, float& cdf, float& e) {
 
 // Activations of the dense linear layer: ACT 2 squared ReLU, 3 identity, 4 SiLU, 5
 // GELU; the gate activation of a gated layer (ACT 0, 1) is SiLU or GELU. And with the
-// derivative.
+// derivative. A NaN stays one (no maximum with 0, which would take the 0).
 template <int ACT>
 __device__ __forceinline__ float dense_act(float x) {
     if constexpr (ACT == 2) {
-        const float r = fmaxf(x, 0.f);
+        const float r = x < 0.f ? 0.f : x;
         return r * r;
     } else if constexpr (ACT == 3) {
         return x;
@@ -120,7 +120,9 @@ __device__ __forceinline__ float dense_act(float x) {
 template <int ACT>
 __device__ __forceinline__ void dense_act_grad(float x, float& f, float& df) {
     if constexpr (ACT == 2) {
-        plain_act_grad<2>(x, f, df);
+        const float r = x < 0.f ? 0.f : x;
+        f = r * r;
+        df = 2.f * r;
     } else if constexpr (ACT == 3) {
         f = x;
         df = 1.f;

@@ -359,3 +359,27 @@ def test_gelu_keeps_its_tail(M):
     bound = np.abs(ref) * (2.0**-19 + vv * vv / 2 * 2.0**-22)
     _within(y[:, 0].cpu().numpy(), ref, bound, "gelu")
     _within(y[:, 63].cpu().numpy(), ref, bound, "gelu")
+
+
+@pytest.mark.parametrize("T", [3, 300])
+@pytest.mark.parametrize("act", ["swiglu", "geglu", "srelu", "silu", "gelu", "none"])
+def test_a_nan_passes_every_activation(M, act, T):
+    """NaN in a row of x reaches all of that row's y, z, dz and a, and no other row."""
+    rng = np.random.default_rng(3)
+    K, N = 72, 128
+    code, NO = {"swiglu": 0, "geglu": 1, "srelu": 2, "none": 3, "silu": 4, "gelu": 5}[act], 64 if "glu" in act else 128
+    x, w, dy = _normal(rng, T, K), _normal(rng, K, N), _normal(rng, T, NO)
+    x[1, 7] = float("nan")
+    ws = _space(M, T, K, N)
+    y, z = torch.empty(T, NO, dtype=BF, device="cuda"), torch.empty(T, N, dtype=BF, device="cuda")
+    keep = {} if act == "none" else {"z": z}
+    M.moe_linear_fwd(x, w, y, code, workspace=ws, **keep)
+    outs = [y]
+    if act != "none":
+        dz, a = torch.empty_like(z), torch.empty_like(y)
+        M.moe_act_bwd(dy, dz, code, z=z, a=a)
+        outs += [z, dz, a]
+    torch.cuda.synchronize()
+    for o in outs:
+        bad = torch.isnan(o)
+        assert bad[1].all() and int(bad.sum()) == o.shape[1], act
