@@ -241,7 +241,9 @@ __device__ __forceinline__ void balance_total(const BalanceArgs& p) {
         n = s_n[0] + s_n[1] + s_n[2] + s_n[3];
         live = s_live[0] + s_live[1] + s_live[2] + s_live[3];
         const double bal = live ? b / live : 0.0, zl = n ? z / n : 0.0;
-        p.loss[0] = (float)(p.cb * bal + p.cz * zl);
+        // a term that is switched off stays out, also where it is infinite (logits of
+        // 1e20 and more, such as a mask's lowest value in all of a row)
+        p.loss[0] = (float)((p.cb != 0.f ? p.cb * bal : 0.0) + (p.cz != 0.f ? p.cz * zl : 0.0));
         p.loss[1] = (float)bal;
         p.loss[2] = (float)zl;
         p.tokens[p.S] = live;

@@ -178,3 +178,16 @@ def test_one_sequence_inside_the_batch_and_rows_off_16_bytes(M):
     assert np.abs(g.cpu().numpy() - want["dlogits"]).max() <= 1e-4 * np.abs(want["dlogits"]).max()
     assert np.abs(loss.cpu().numpy() - want["loss"]).max() <= 3e-5 * want["loss"].max()
     assert np.array_equal(counts.cpu().numpy(), want["counts"])
+
+
+def test_a_term_switched_off_stays_out(M):
+    """A row of the type's lowest value: its squared log-sum-exp passes fp32, but with z_coef = 0 the
+    loss is the balance loss alone, and the gradient finite."""
+    _, lg, idx = _case(64, 8, 2, 6)
+    lg[5] = np.finfo(np.float32).min
+    for T in (64, 5000):
+        x, i = np.resize(lg, (T, 8)), np.resize(idx, (T, 2))
+        got = _run(M, x, i, cz=0.0)
+        assert np.isinf(got["loss"][2]) and np.isfinite(got["dlogits"]).all()
+        # fp32(0.3) and the stored loss[1] are each off by 2^-24 of themselves, as is the product
+        assert abs(got["loss"][0] - 0.3 * got["loss"][1]) <= 3.1 * U * 0.3 * got["loss"][1]
