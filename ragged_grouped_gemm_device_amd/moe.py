@@ -311,6 +311,12 @@ def _device(t):
     return dev
 
 
+def _rows(T):
+    """Refuses a row count that the C ABI's 32-bit one would not hold."""
+    if T > MOE_MAX_ROWS:
+        raise ValueError(f"{T} rows; at most {MOE_MAX_ROWS}")
+
+
 def _space(ws, device):
     """(address, bytes) of a workspace tensor."""
     if ws is None:
@@ -330,6 +336,7 @@ def moe_linear_fwd(x, w, y, act=MOE_ACT_NONE, bias=None, residual=None, z=None, 
     for the backward pass (as bf16, as an 8-bit checkpoint)."""
     dev = _device(x)
     (T, K), N = x.shape, w.shape[1]
+    _rows(T)
     out = (T, N // 2 if act in _GATED else N)
     _operand(x, (T, K), _BF, "x", dev)
     _operand(w, (K, N), _BF, "w", dev)
@@ -354,6 +361,7 @@ def moe_act_bwd(dy, dz, act=MOE_ACT_NONE, z=None, z_q=None, z_s=None, a=None, db
         raise ValueError("neither dy nor z is given")
     dev = _device(ref)
     T, N = ref.shape
+    _rows(T)
     out = (T, N // 2 if act in _GATED else N)
     _operand(dy, out, _BF, "dy", dev)
     _operand(z, (T, N), _BF, "z", dev)
@@ -372,6 +380,7 @@ def moe_linear_dgrad(dz, w, dx, residual=None, workspace=None):
     """dx = dz w^T + residual (residual may be dx itself)."""
     dev = _device(dz)
     T, (K, N) = dz.shape[0], w.shape
+    _rows(T)
     _operand(dz, (T, N), _BF, "dz", dev)
     _operand(w, (K, N), _BF, "w", dev)
     _operand(dx, (T, K), _BF, "dx", dev)
@@ -386,6 +395,7 @@ def moe_linear_wgrad(x, dz, dw, x_q=None, x_s=None, accumulate=False, workspace=
     checkpoint x_q, x_s."""
     dev = _device(dz)
     (T, N), K = dz.shape, dw.shape[0]
+    _rows(T)
     _operand(x, (T, K), _BF, "x", dev)
     _operand(x_q, (T, K), _U8, "x_q", dev)
     _operand(x_s, (T, K // MOE_MX_BLOCK), _U8, "x_s", dev)
@@ -421,6 +431,7 @@ def moe_balance_loss(logits, topk_idx, loss, counts, prob, tokens, workspace, ba
     probabilities [S, E] and live tokens [S + 2] that the backward reads."""
     dev = _device(logits)
     (T, E), k, S = logits.shape, topk_idx.shape[1], counts.shape[0]
+    _rows(T)
     _operand(logits, (T, E), _F32, "logits", dev)
     _operand(topk_idx, (T, k), _I32, "topk_idx", dev)
     _operand(valid, (T,), _U8, "valid", dev, torch.bool)
@@ -442,6 +453,7 @@ def moe_balance_loss_bwd(logits, counts, tokens, dlogits, k, balance_coef, z_coe
     to) dlogits; grad: the loss's upstream gradient (one fp32 value on the device)."""
     dev = _device(logits)
     (T, E), S = logits.shape, counts.shape[0]
+    _rows(T)
     _operand(logits, (T, E), _F32, "logits", dev)
     _operand(counts, (S, E), _I32, "counts", dev)
     _operand(tokens, (S + 2,), _I32, "tokens", dev)
@@ -480,6 +492,9 @@ class Buffers:
         self.route_ws = torch.empty(max(16, moe_route_workspace_bytes(T, k, E)), dtype=u8, device=dev)
         self.x_perm = torch.empty(M, d, dtype=bf, device=dev)
         n1 = 2 * n if gated else n   # FC1 width (non-gated sReLU: n)
+        if h is not None and not (h.shape == (M, n1) and h.dtype is bf and h.is_contiguous()
+                                  and h.device.type == dev.type and dev.index in (None, h.device.index)):
+            raise ValueError(f"h: {h.dtype} {tuple(h.shape)} on {h.device}; expected a dense {bf} {(M, n1)} on {dev}")
         self.h = torch.empty(M, n1, dtype=bf, device=dev) if h is None else h
         self.ckpt8 = ckpt8
         if ckpt8:

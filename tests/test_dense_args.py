@@ -139,3 +139,32 @@ def test_binding_refuses_operands_of_another_shape_type_or_layout():
             M.moe_balance_loss(lg, idx, **{**one, **bad})
     with pytest.raises(ValueError):
         M.moe_balance_loss(lg, idx.long(), **one)
+
+
+def test_binding_refuses_more_rows_than_the_abi_counts():
+    """Row counts past 32 bits would wrap to another, valid one (meta tensors: nothing is allocated)."""
+    n, bf = (1 << 32) + 8, torch.bfloat16
+    new = lambda *s, t=bf: torch.empty(*s, dtype=t, device="meta")  # noqa: E731
+    with pytest.raises(ValueError, match="rows"):
+        M.moe_linear_fwd(new(n, 8), new(8, 8), new(n, 8))
+    with pytest.raises(ValueError, match="rows"):
+        M.moe_act_bwd(new(n, 8), new(n, 8))
+    with pytest.raises(ValueError, match="rows"):
+        M.moe_linear_dgrad(new(n, 8), new(8, 8), new(n, 8))
+    with pytest.raises(ValueError, match="rows"):
+        M.moe_linear_wgrad(new(n, 8), new(n, 8), new(8, 8))
+    i32, f32 = torch.int32, torch.float32
+    with pytest.raises(ValueError, match="rows"):
+        M.moe_balance_loss(new(n, 4, t=f32), new(n, 2, t=i32), new(3, t=f32), new(1, 4, t=i32), new(1, 4, t=f32),
+                           new(3, t=i32), new(64, t=torch.uint8), 1.0, 1.0)
+    with pytest.raises(ValueError, match="rows"):
+        M.moe_balance_loss_bwd(new(n, 4, t=f32), new(1, 4, t=i32), new(3, t=i32), new(n, 4, t=f32), 2, 1.0, 1.0)
+
+
+def test_buffers_refuse_a_scratch_of_another_shape_or_type():
+    cap = M.moe_capacity_rows(8, 2, 4)
+    ok = torch.empty(cap, 128, dtype=torch.bfloat16)
+    assert M.Buffers(8, 2, 4, 64, 64, device="cpu", ckpt8=True, h=ok).h is ok
+    for bad in (ok[:-1], ok[:, :64], ok.float(), ok.t().contiguous().t()):
+        with pytest.raises(ValueError, match="h:"):
+            M.Buffers(8, 2, 4, 64, 64, device="cpu", ckpt8=True, h=bad)
