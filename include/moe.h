@@ -517,7 +517,8 @@ size_t moe_balance_workspace_bytes(int T, int E, int S);
  *     f_se = E counts[s, e] / (k n_s),  P_se = mean of p_e over the live tokens,
  *     B = mean over the sequences with a live token of sum_e f_se P_se,
  *     Z = mean over all live tokens of (log sum_e exp logits[t, e])^2,
- *     loss[0] = balance_coef B + z_coef Z, loss[1] = B, loss[2] = Z.
+ *     loss[0] = balance_coef B + z_coef Z, loss[1] = B, loss[2] = Z
+ *   (a term whose coefficient is 0 stays out of loss[0], also where it is infinite).
  *   A token is live unless valid[t] == 0, it lies outside [seq_offsets[0],
  *   seq_offsets[S]), or it has no finite logit. Non-finite logits have
  *   probability 0, as in the router. Without a live token every loss is 0.

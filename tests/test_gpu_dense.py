@@ -286,7 +286,8 @@ def test_infinities_and_nan_stay_in_their_rows_and_columns(M):
         assert not bad[keep.cuda()].any()
 
 
-@pytest.mark.parametrize("T, K, N, stage", [(1, 8192, 4096, "f"), (48, 4096, 512, "f"), (200, 8192, 1024, "d"), (8192, 256, 256, "w")])
+@pytest.mark.parametrize("T, K, N, stage", [(1, 8192, 4096, "f"), (48, 4096, 512, "f"), (200, 8192, 1024, "d"), (8192, 256, 256, "w"),
+                                            (4300, 4104, 4168, "f"), (4300, 4104, 4168, "w")])
 def test_captured_products_replay_to_the_eager_bits(M, T, K, N, stage):
     """Products whose K is split: the joined sums are the same in every replay, with other work between."""
     rng = np.random.default_rng(T)
