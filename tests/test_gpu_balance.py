@@ -97,7 +97,8 @@ def test_one_sequence(M, T, E, k):
     _check(_run(M, lg, idx, half=True), lg, idx)
 
 
-@pytest.mark.parametrize("T, E, k, S", [(10, 4, 2, 10), (100, 8, 2, 7), (1000, 32, 8, 16), (700, 60, 4, 33), (2100, 256, 8, 9)])
+@pytest.mark.parametrize("T, E, k, S", [(10, 4, 2, 10), (100, 8, 2, 7), (1000, 32, 8, 16), (700, 60, 4, 33), (2100, 256, 8, 9),
+                                        (128, 64, 4, 128), (130, 8, 2, 64), (1, 5, 2, 1), (2, 300, 3, 2), (3000, 7, 1, 2999)])
 def test_ragged_masked_sequences(M, T, E, k, S):
     rng, lg, idx = _case(T, E, k, T * S)
     offs = np.sort(rng.integers(0, T + 1, S + 1)).astype(np.int32)   # empty ones, and tokens outside all of them
