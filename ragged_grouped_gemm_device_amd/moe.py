@@ -127,8 +127,10 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream():
+def _stream(device=0):
     # the current stream's handle without building a torch.cuda.Stream (0.1 instead of 2.7 us)
+    if device < 0:   # operands that agree with each other, but are none of a kernel's
+        raise ValueError("the operands are not on a GPU")
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
@@ -349,7 +351,7 @@ def moe_linear_fwd(x, w, y, act=MOE_ACT_NONE, bias=None, residual=None, z=None, 
     ws, nws = _space(workspace, dev)
     rc = _lib().moe_linear_fwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), T, K, N, act,
                                int(y is not None and y.dtype is _F32),
-                               _ptr(y), _ptr(z), _ptr(z_q), _ptr(z_s), ws, nws, _stream())
+                               _ptr(y), _ptr(z), _ptr(z_q), _ptr(z_s), ws, nws, _stream(dev))
     _check("moe_linear_fwd", rc)
 
 
@@ -372,7 +374,7 @@ def moe_act_bwd(dy, dz, act=MOE_ACT_NONE, z=None, z_q=None, z_s=None, a=None, db
     _operand(dbias, (N,), _F32, "dbias", dev)
     ws, nws = _space(workspace, dev)
     rc = _lib().moe_act_bwd(_ptr(dy), _ptr(z), _ptr(z_q), _ptr(z_s), T, N, act, _ptr(dz), _ptr(a), _ptr(dbias),
-                            ws, nws, _stream())
+                            ws, nws, _stream(dev))
     _check("moe_act_bwd", rc)
 
 
@@ -387,7 +389,7 @@ def moe_linear_dgrad(dz, w, dx, residual=None, workspace=None):
     _operand(residual, (T, K), _BF, "residual", dev)
     ws, nws = _space(workspace, dev)
     _check("moe_linear_dgrad", _lib().moe_linear_dgrad(_ptr(dz), _ptr(w), _ptr(residual), T, K, N, _ptr(dx), ws,
-                                                       nws, _stream()))
+                                                       nws, _stream(dev)))
 
 
 def moe_linear_wgrad(x, dz, dw, x_q=None, x_s=None, accumulate=False, workspace=None):
@@ -404,7 +406,7 @@ def moe_linear_wgrad(x, dz, dw, x_q=None, x_s=None, accumulate=False, workspace=
     ws, nws = _space(workspace, dev)
     _check("moe_linear_wgrad", _lib().moe_linear_wgrad(_ptr(x), _ptr(x_q), _ptr(x_s), _ptr(dz), T, K, N,
                                                        int(dw.dtype == _F32), int(bool(accumulate)), _ptr(dw), ws,
-                                                       nws, _stream()))
+                                                       nws, _stream(dev)))
 
 
 def moe_dequant_mxfp8(q, s, out):
@@ -414,7 +416,7 @@ def moe_dequant_mxfp8(q, s, out):
     _operand(q, (R, Cc), _U8, "q", dev)
     _operand(s, (R, Cc // MOE_MX_BLOCK), _U8, "s", dev)
     _operand(out, (R, Cc), _BF, "out", dev)
-    _check("moe_dequant_mxfp8", _lib().moe_dequant_mxfp8(_ptr(q), _ptr(s), R, Cc, _ptr(out), _stream()))
+    _check("moe_dequant_mxfp8", _lib().moe_dequant_mxfp8(_ptr(q), _ptr(s), R, Cc, _ptr(out), _stream(dev)))
 
 
 def moe_balance_workspace_bytes(T: int, E: int, S: int = 1) -> int:
@@ -443,7 +445,7 @@ def moe_balance_loss(logits, topk_idx, loss, counts, prob, tokens, workspace, ba
     ws, nws = _space(workspace, dev)
     rc = _lib().moe_balance_loss(_ptr(logits), _ptr(topk_idx), _ptr(valid), _ptr(seq_offsets), T, E, k, S,
                                  balance_coef, z_coef, _ptr(loss), _ptr(counts), _ptr(prob), _ptr(tokens), ws, nws,
-                                 _stream())
+                                 _stream(dev))
     _check("moe_balance_loss", rc)
 
 
@@ -465,7 +467,7 @@ def moe_balance_loss_bwd(logits, counts, tokens, dlogits, k, balance_coef, z_coe
         _operand(grad.reshape(1), (1,), _F32, "grad", dev)
     rc = _lib().moe_balance_loss_bwd(_ptr(logits), _ptr(counts), _ptr(tokens), _ptr(valid), _ptr(seq_offsets), T, E,
                                      k, S, balance_coef, z_coef, _ptr(grad), int(bool(accumulate)), _ptr(dlogits),
-                                     _ptr(dlogits_bf16), _stream())
+                                     _ptr(dlogits_bf16), _stream(dev))
     _check("moe_balance_loss_bwd", rc)
 
 

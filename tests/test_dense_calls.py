@@ -1,0 +1,55 @@
+"""What the binding of the dense half lets through to the library: a stub takes the calls (CPU)."""
+import pytest
+import torch
+
+from ragged_grouped_gemm_device_amd import moe as M
+
+BF, F32, I32, U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+class Stub:
+    """Records the entry points that a call reaches, and answers that all is well."""
+
+    def __init__(self):
+        self.reached = []
+
+    def __getattr__(self, name):
+        return lambda *a: self.reached.append(name) or 0
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    stub = Stub()
+    monkeypatch.setattr(M, "_lib", lambda: stub)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    return stub
+
+
+def _z(*shape, t=BF, dev="cpu"):
+    return torch.zeros(*shape, dtype=t, device=dev)
+
+
+def _calls(dev):
+    z = lambda *s, t=BF: _z(*s, t=t, dev=dev)  # noqa: E731
+    ws = z(4096, t=U8)
+    losses = (z(3, t=F32), z(1, 8, t=I32), z(1, 8, t=F32), z(3, t=I32))
+    return {
+        "moe_linear_fwd": lambda: M.moe_linear_fwd(z(4, 64), z(64, 128), z(4, 128), workspace=ws),
+        "moe_act_bwd": lambda: M.moe_act_bwd(z(4, 128), z(4, 128), M.MOE_ACT_SILU, z=z(4, 128)),
+        "moe_linear_dgrad": lambda: M.moe_linear_dgrad(z(4, 128), z(64, 128), z(4, 64), workspace=ws),
+        "moe_linear_wgrad": lambda: M.moe_linear_wgrad(z(4, 64), z(4, 128), z(64, 128, t=F32), workspace=ws),
+        "moe_dequant_mxfp8": lambda: M.moe_dequant_mxfp8(z(4, 64, t=U8), z(4, 2, t=U8), z(4, 64)),
+        "moe_balance_loss": lambda: M.moe_balance_loss(z(6, 8, t=F32), z(6, 2, t=I32), *losses, ws, 1.0, 1.0),
+        "moe_balance_loss_bwd": lambda: M.moe_balance_loss_bwd(z(6, 8, t=F32), losses[1], losses[3], z(6, 8, t=F32), 2,
+                                                               1.0, 1.0),
+    }
+
+
+@pytest.mark.parametrize("dev", ["cpu", "meta"])
+@pytest.mark.parametrize("name", list(_calls("meta")))
+def test_operands_that_are_all_off_the_gpu_are_refused(lib, name, dev):
+    """The library gets addresses: a host one must not reach a kernel, even where every operand agrees."""
+    with pytest.raises(ValueError, match="GPU"):
+        _calls(dev)[name]()
+    assert lib.reached == []
