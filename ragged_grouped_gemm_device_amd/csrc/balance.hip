@@ -257,9 +257,13 @@ __device__ __forceinline__ void balance_total(const BalanceArgs& p) {
     }
 }
 
+// At most kJoinBlocks workgroups: a launch of 2^32 threads and more is cut off without an error.
+constexpr int64_t kJoinBlocks = 1 << 20;
 __global__ void __launch_bounds__(256) balance_join_kernel(BalanceArgs p) {
-    const int s = blockIdx.x / p.etiles;
-    balance_join(p, s, blockIdx.x - s * p.etiles);
+    for (int64_t i = blockIdx.x; i < (int64_t)p.S * p.etiles; i += gridDim.x) {
+        const int s = (int)i / p.etiles;
+        balance_join(p, s, (int)i - s * p.etiles);
+    }
 }
 __global__ void __launch_bounds__(256) balance_total_kernel(BalanceArgs p) { balance_total(p); }
 
@@ -526,7 +530,7 @@ int launch_balance_loss(const float* logits, const int32_t* topk_idx, const uint
         balance_chunk_kernel<decltype(G)::value, decltype(PER)::value, decltype(V4)::value><<<nchunks, 256, 0, s>>>(p);
     });
     if (!p.alone) {
-        balance_join_kernel<<<(unsigned)((int64_t)p.etiles * S), 256, 0, s>>>(p);
+        balance_join_kernel<<<(unsigned)std::min((int64_t)p.etiles * S, kJoinBlocks), 256, 0, s>>>(p);
         balance_total_kernel<<<1, 256, 0, s>>>(p);
     }
     return hipGetLastError() == hipSuccess ? 0 : -4;
