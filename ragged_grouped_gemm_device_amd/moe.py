@@ -648,6 +648,8 @@ class Router:
         return self.logits
 
     def losses(self, topk_idx):
+        if topk_idx.shape[1] != self.k:   # the backward's f_se divides by self.k
+            raise ValueError(f"topk_idx: {topk_idx.shape[1]} experts a token; the router was made with k = {self.k}")
         moe_balance_loss(self.logits, topk_idx, self.loss, self.counts, self.prob, self.tokens, self.loss_ws,
                          self.balance_coef, self.z_coef, valid=self.valid, seq_offsets=self.seq_offsets)
 

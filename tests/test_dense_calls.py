@@ -53,3 +53,11 @@ def test_operands_that_are_all_off_the_gpu_are_refused(lib, name, dev):
     with pytest.raises(ValueError, match="GPU"):
         _calls(dev)[name]()
     assert lib.reached == []
+
+
+def test_router_losses_refuse_another_k(lib):
+    """The forward would count topk_idx's k experts a token, and the backward divide by the Router's k."""
+    router = M.Router(6, 64, 8, 1, device="cpu")
+    with pytest.raises(ValueError, match="k = 1"):
+        router.losses(_z(6, 2, t=I32))
+    assert "moe_balance_loss" not in lib.reached
