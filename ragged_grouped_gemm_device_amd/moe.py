@@ -715,6 +715,9 @@ def backward(buf: Buffers, dout, w1, w2, stages=MOE_STAGES_BWD, act=MOE_ACT_SWIG
     last, after the unpermute-sum has read dX_perm. router and shared as in forward (x_tokens:
     the layer's input x [T, d] for their weight gradients, unless x is given or they keep an 8-bit
     checkpoint of it): their gradients are added to dx."""
+    x_in = x if x is not None else x_tokens
+    if x_in is None and (router is not None or (shared is not None and not shared[0].x8)):
+        raise ValueError("the router's and the shared expert's weight gradients need x or x_tokens")
     if buf.ckpt8 and (stages & MOE_STAGE_DGRAD2):
         moe_dequant_mxfp8(buf.h_q, buf.h_s, buf.h)
     early, late = stages & ~MOE_STAGE_WGRAD1, stages & MOE_STAGE_WGRAD1
@@ -747,7 +750,6 @@ def backward(buf: Buffers, dout, w1, w2, stages=MOE_STAGES_BWD, act=MOE_ACT_SWIG
     moe_combine(buf.dx_perm, buf.row_of, None, buf.k, buf.dx)
     if late:
         bwd(late)
-    x_in = x if x is not None else x_tokens
     if shared is not None:
         shared[0].backward(x_in, dout, *shared[1:], buf.dx)
     if router is not None:

@@ -61,3 +61,26 @@ def test_router_losses_refuse_another_k(lib):
     with pytest.raises(ValueError, match="k = 1"):
         router.losses(_z(6, 2, t=I32))
     assert "moe_balance_loss" not in lib.reached
+
+
+@pytest.mark.parametrize("which", ["router", "shared", "both"])
+def test_backward_without_the_input_that_it_needs_starts_nothing(lib, which):
+    """The weight gradients of the router and the shared expert read x: refused before any launch, not
+    after the routed experts' backward and a half-done dx."""
+    buf = M.Buffers(8, 2, 8, 64, 64, device="cpu")
+    kw = {}
+    if which != "shared":
+        kw["router"] = (M.Router(8, 64, 8, 2, device="cpu"), _z(64, 8))
+    if which != "router":
+        kw["shared"] = (M.SharedExpert(8, 64, 32, device="cpu"), _z(64, 64), _z(32, 64))
+    lib.reached.clear()
+    with pytest.raises(ValueError, match="x_tokens"):
+        M.backward(buf, _z(8, 64), _z(8, 64, 128), _z(8, 64, 64), **kw)
+    assert lib.reached == []
+
+
+def test_backward_of_a_shared_expert_with_its_own_copy_of_x_needs_none(lib):
+    buf = M.Buffers(8, 2, 8, 64, 64, device="cpu")
+    shared = M.SharedExpert(8, 64, 32, x8=True, device="cpu")
+    with pytest.raises(ValueError, match="GPU"):        # as far as the first product, on host tensors here
+        M.backward(buf, _z(8, 64), _z(8, 64, 128), _z(8, 64, 64), shared=(shared, _z(64, 64), _z(32, 64)))
