@@ -8,8 +8,7 @@
 // All are bound by HBM traffic: 16-byte accesses, one pass.
 #include <algorithm>
 
-#include "gemm_common.hpp"
-#include "mx_common.hpp"
+#include "dense_common.hpp"
 
 namespace moe {
 

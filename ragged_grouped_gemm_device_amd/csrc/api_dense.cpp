@@ -9,7 +9,7 @@
 #include <initializer_list>
 
 #include "../../include/moe.h"
-#include "launch.hpp"
+#include "dense_launch.hpp"
 
 namespace {
 

@@ -21,7 +21,7 @@
 // (58 us, 4.6 TB/s).
 #include <algorithm>
 
-#include "gemm_common.hpp"
+#include "dense_common.hpp"
 
 namespace moe {
 

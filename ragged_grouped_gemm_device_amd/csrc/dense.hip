@@ -26,8 +26,7 @@
 // cycles); the read of W with few rows (the small products below).
 #include <algorithm>
 
-#include "gemm_common.hpp"
-#include "mx_common.hpp"
+#include "dense_common.hpp"
 
 namespace moe {
 

@@ -224,18 +224,6 @@ __device__ __forceinline__ void mx_store_row32(const uint32_t w[4], int lane, ui
     *(uint4*)(q + 16 * h) = h ? make_uint4(r0, w[2], r1, w[3]) : make_uint4(w[0], r0, w[1], r1);
 }
 
-// 2^(s - 127); code 0 is the subnormal 2^-127, code 255 NaN
-__device__ __forceinline__ float e8m0_value(uint32_t s) {
-    return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7fc00000u : s << 23);
-}
-
-// 4 E4M3 codes (low byte first) times a scale
-__device__ __forceinline__ void e4m3x4_value(uint32_t w, float sc, float* v) {
-    const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
-    const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
-    v[0] = a.x * sc, v[1] = a.y * sc, v[2] = b.x * sc, v[3] = b.y * sc;
-}
-
 // Row-wise MXFP8 block of one row of a 32 x 32 block held the MFMA way: this
 // lane has 16 of the row's 32 bf16 values (pk[j / 2], 16-bit slot j: column
 // 8 (j / 4) + 4 h + j % 4, h = lane / 32), the lane l ^ 32 the other 16. The
