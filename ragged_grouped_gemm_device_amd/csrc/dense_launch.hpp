@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "dense_plan.hpp"
+
 namespace moe {
 
 // Outputs of at least this size are stored past the caches by the streaming passes:
@@ -12,7 +14,6 @@ namespace moe {
 constexpr int64_t kDenseStreamBytes = (int64_t)64 << 20;
 
 // Dense linear layer (act: the MOE_ACT_* codes; N: columns of W, 2n when gated)
-enum DensePass { kForward, kDgrad, kWgrad };
 size_t dense_part_bytes(int64_t M, int64_t N, int64_t K, DensePass pass);
 int launch_linear_fwd(const uint16_t* x, const uint16_t* w, const uint16_t* bias, const uint16_t* res, int T,
                       int K, int N, int act, int y_f32, void* y, uint16_t* z, uint8_t* z_q, uint8_t* z_s,
