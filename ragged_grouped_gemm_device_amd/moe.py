@@ -313,10 +313,12 @@ def _device(t):
     return dev
 
 
-def _rows(T):
-    """Refuses a row count that the C ABI's 32-bit one would not hold."""
+def _sizes(T, *others):
+    """Refuses a row count, and other sizes, that the C ABI's 32 bits would not hold."""
     if T > MOE_MAX_ROWS:
         raise ValueError(f"{T} rows; at most {MOE_MAX_ROWS}")
+    if max(others) > 0x7fffffff:
+        raise ValueError(f"a size of {max(others)}, past 32 bits")
 
 
 def _space(ws, device):
@@ -338,7 +340,7 @@ def moe_linear_fwd(x, w, y, act=MOE_ACT_NONE, bias=None, residual=None, z=None, 
     for the backward pass (as bf16, as an 8-bit checkpoint)."""
     dev = _device(x)
     (T, K), N = x.shape, w.shape[1]
-    _rows(T)
+    _sizes(T, K, N)
     out = (T, N // 2 if act in _GATED else N)
     _operand(x, (T, K), _BF, "x", dev)
     _operand(w, (K, N), _BF, "w", dev)
@@ -363,7 +365,7 @@ def moe_act_bwd(dy, dz, act=MOE_ACT_NONE, z=None, z_q=None, z_s=None, a=None, db
         raise ValueError("neither dy nor z is given")
     dev = _device(ref)
     T, N = ref.shape
-    _rows(T)
+    _sizes(T, N)
     out = (T, N // 2 if act in _GATED else N)
     _operand(dy, out, _BF, "dy", dev)
     _operand(z, (T, N), _BF, "z", dev)
@@ -382,7 +384,7 @@ def moe_linear_dgrad(dz, w, dx, residual=None, workspace=None):
     """dx = dz w^T + residual (residual may be dx itself)."""
     dev = _device(dz)
     T, (K, N) = dz.shape[0], w.shape
-    _rows(T)
+    _sizes(T, K, N)
     _operand(dz, (T, N), _BF, "dz", dev)
     _operand(w, (K, N), _BF, "w", dev)
     _operand(dx, (T, K), _BF, "dx", dev)
@@ -397,7 +399,7 @@ def moe_linear_wgrad(x, dz, dw, x_q=None, x_s=None, accumulate=False, workspace=
     checkpoint x_q, x_s."""
     dev = _device(dz)
     (T, N), K = dz.shape, dw.shape[0]
-    _rows(T)
+    _sizes(T, K, N)
     _operand(x, (T, K), _BF, "x", dev)
     _operand(x_q, (T, K), _U8, "x_q", dev)
     _operand(x_s, (T, K // MOE_MX_BLOCK), _U8, "x_s", dev)
@@ -413,6 +415,7 @@ def moe_dequant_mxfp8(q, s, out):
     """bf16 values of row-wise MXFP8 codes (restores an 8-bit checkpoint)."""
     dev = _device(q)
     R, Cc = q.shape
+    _sizes(0, Cc)   # R is 64-bit
     _operand(q, (R, Cc), _U8, "q", dev)
     _operand(s, (R, Cc // MOE_MX_BLOCK), _U8, "s", dev)
     _operand(out, (R, Cc), _BF, "out", dev)
@@ -433,7 +436,7 @@ def moe_balance_loss(logits, topk_idx, loss, counts, prob, tokens, workspace, ba
     probabilities [S, E] and live tokens [S + 2] that the backward reads."""
     dev = _device(logits)
     (T, E), k, S = logits.shape, topk_idx.shape[1], counts.shape[0]
-    _rows(T)
+    _sizes(T, E, k, S)
     _operand(logits, (T, E), _F32, "logits", dev)
     _operand(topk_idx, (T, k), _I32, "topk_idx", dev)
     _operand(valid, (T,), _U8, "valid", dev, torch.bool)
@@ -455,7 +458,7 @@ def moe_balance_loss_bwd(logits, counts, tokens, dlogits, k, balance_coef, z_coe
     to) dlogits; grad: the loss's upstream gradient (one fp32 value on the device)."""
     dev = _device(logits)
     (T, E), S = logits.shape, counts.shape[0]
-    _rows(T)
+    _sizes(T, E, k, S)
     _operand(logits, (T, E), _F32, "logits", dev)
     _operand(counts, (S, E), _I32, "counts", dev)
     _operand(tokens, (S + 2,), _I32, "tokens", dev)

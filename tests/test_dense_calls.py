@@ -84,3 +84,35 @@ def test_backward_of_a_shared_expert_with_its_own_copy_of_x_needs_none(lib):
     shared = M.SharedExpert(8, 64, 32, x8=True, device="cpu")
     with pytest.raises(ValueError, match="GPU"):        # as far as the first product, on host tensors here
         M.backward(buf, _z(8, 64), _z(8, 64, 128), _z(8, 64, 64), shared=(shared, _z(64, 64), _z(32, 64)))
+
+
+BIG = 1 << 32
+
+
+@pytest.mark.parametrize("name, call", [
+    ("moe_linear_fwd", lambda z: M.moe_linear_fwd(z(1, BIG + 64), z(BIG + 64, 8), z(1, 8))),
+    ("moe_linear_fwd", lambda z: M.moe_linear_fwd(z(1, 64), z(64, BIG + 8), z(1, BIG + 8))),
+    ("moe_act_bwd", lambda z: M.moe_act_bwd(z(1, BIG + 8), z(1, BIG + 8))),
+    ("moe_linear_dgrad", lambda z: M.moe_linear_dgrad(z(1, BIG + 8), z(8, BIG + 8), z(1, 8))),
+    ("moe_linear_dgrad", lambda z: M.moe_linear_dgrad(z(1, 8), z(BIG + 8, 8), z(1, BIG + 8))),
+    ("moe_linear_wgrad", lambda z: M.moe_linear_wgrad(z(1, BIG + 8), z(1, 8), z(BIG + 8, 8))),
+    ("moe_linear_wgrad", lambda z: M.moe_linear_wgrad(z(1, 8), z(1, BIG + 8), z(8, BIG + 8))),
+    ("moe_dequant_mxfp8", lambda z: M.moe_dequant_mxfp8(z(1, BIG + 32, t=U8), z(1, BIG // 32 + 1, t=U8), z(1, BIG + 32))),
+    ("moe_balance_loss", lambda z: M.moe_balance_loss(z(4, BIG + 8, t=F32), z(4, 2, t=I32), z(3, t=F32), z(1, BIG + 8, t=I32),
+                                                      z(1, BIG + 8, t=F32), z(3, t=I32), z(64, t=U8), 1.0, 1.0)),
+    ("moe_balance_loss", lambda z: M.moe_balance_loss(z(4, 8, t=F32), z(4, BIG + 2, t=I32), z(3, t=F32), z(1, 8, t=I32),
+                                                      z(1, 8, t=F32), z(3, t=I32), z(64, t=U8), 1.0, 1.0)),
+    ("moe_balance_loss", lambda z: M.moe_balance_loss(z(4, 8, t=F32), z(4, 2, t=I32), z(3, t=F32), z(BIG + 1, 8, t=I32),
+                                                      z(BIG + 1, 8, t=F32), z(BIG + 3, t=I32), z(64, t=U8), 1.0, 1.0)),
+    ("moe_balance_loss_bwd", lambda z: M.moe_balance_loss_bwd(z(4, 8, t=F32), z(1, 8, t=I32), z(3, t=I32), z(4, 8, t=F32), BIG + 2,
+                                                              1.0, 1.0)),
+])
+def test_sizes_past_32_bits_are_refused(lib, monkeypatch, name, call):
+    """They would wrap to another, valid size, as the row counts would (meta tensors: nothing is allocated;
+    taken for the first GPU's, as tensors of this size would be there)."""
+    monkeypatch.setattr(M, "_device", lambda t: 0)
+    monkeypatch.setattr(M, "_operand", lambda *a: None)
+    monkeypatch.setattr(M, "_space", lambda *a: (None, 0))
+    with pytest.raises(ValueError, match="32 bits"):
+        call(lambda *s, t=BF: torch.empty(*s, dtype=t, device="meta"))
+    assert lib.reached == []
