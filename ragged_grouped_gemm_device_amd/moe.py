@@ -630,10 +630,11 @@ class SharedExpert:
 
 
 class Router:
-    """The router's projection logits = x wg (wg [d, E], E a multiple of 8) with the balance and z
-    losses of the routing: loss [total, balance, z], counts, prob and tokens after forward; dwg
-    after backward. Sequences and padding tokens: seq_offsets [S + 1] and valid [T], kept by
-    reference (set them before a forward)."""
+    """The router's projection logits = x wg (wg [d, E]) with the balance and z losses of the
+    routing: loss [total, balance, z], counts, prob and tokens after forward; dwg after backward.
+    Sequences and padding tokens: seq_offsets [S + 1] and valid [T], kept by reference (set them
+    before a forward). The products take widths in steps of 8: with another E they work on copies
+    with columns of zeros behind it."""
 
     def __init__(self, T: int, d: int, E: int, k: int, S: int = 1, balance_coef: float = 1e-2,
                  z_coef: float = 1e-3, device="cuda"):
@@ -643,11 +644,25 @@ class Router:
         self.loss, self.counts, self.prob = new(3), new(S, E, t=_I32), new(S, E)
         self.tokens = new(S + 2, t=_I32)
         self.valid = self.seq_offsets = None
-        self.ws = new(max(16, moe_linear_workspace_bytes(T, d, E)), t=_U8)
+        self.wide = None
+        N = -(-E // 8) * 8
+        if N != E:   # wg, logits, dlogits16 and dwg as the products take them
+            self.wide = (new(d, N, t=_BF).zero_(), new(T, N), new(T, N, t=_BF).zero_(), new(d, N))
+        self.ws = new(max(16, moe_linear_workspace_bytes(T, d, N)), t=_U8)
         self.loss_ws = new(moe_balance_workspace_bytes(T, E, S), t=_U8)
 
+    def _weight(self, wg):
+        if self.wide is None:
+            return wg
+        _operand(wg, self.dwg.shape, _BF, "wg", self.logits.get_device())
+        self.wide[0][:, :wg.shape[1]].copy_(wg)
+        return self.wide[0]
+
     def project(self, x, wg):
-        moe_linear_fwd(x, wg, self.logits, workspace=self.ws)
+        wg, out = self._weight(wg), self.logits if self.wide is None else self.wide[1]
+        moe_linear_fwd(x, wg, out, workspace=self.ws)
+        if out is not self.logits:
+            self.logits.copy_(out[:, :self.logits.shape[1]])
         return self.logits
 
     def losses(self, topk_idx):
@@ -662,8 +677,14 @@ class Router:
         moe_balance_loss_bwd(self.logits, self.counts, self.tokens, dlogits, self.k, self.balance_coef, self.z_coef,
                              valid=self.valid, seq_offsets=self.seq_offsets, grad=grad, accumulate=True,
                              dlogits_bf16=self.dlogits16)
-        moe_linear_dgrad(self.dlogits16, wg, dx, residual=dx, workspace=self.ws)
-        moe_linear_wgrad(x, self.dlogits16, self.dwg, workspace=self.ws)
+        wg, E = self._weight(wg), self.logits.shape[1]
+        d16, dwg = (self.dlogits16, self.dwg) if self.wide is None else self.wide[2:]
+        if d16 is not self.dlogits16:
+            d16[:, :E].copy_(self.dlogits16)
+        moe_linear_dgrad(d16, wg, dx, residual=dx, workspace=self.ws)
+        moe_linear_wgrad(x, d16, dwg, workspace=self.ws)
+        if dwg is not self.dwg:
+            self.dwg.copy_(dwg[:, :E])
 
 
 def forward(buf: Buffers, x, logits, w1, w2, renorm=False, fwd_stages=MOE_STAGES_FWD, store_h=True,
