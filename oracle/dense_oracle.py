@@ -1,12 +1,12 @@
 """fp64 oracle of the dense half of the layer: the linear layer with its
 activation, the backward pass, and the router losses. Plain numpy, written from
-the formulas; shares the codecs and the activations of moe_oracle only.
+the formulas; shares the activations and the interleave of moe_oracle only.
 """
 from __future__ import annotations
 
 import numpy as np
 
-from .moe_oracle import deinterleave, gelu, gelu_grad, interleave, mx_dequant, sigmoid, silu
+from .moe_oracle import deinterleave, gelu, gelu_grad, interleave, sigmoid, silu
 
 GATED = ("swiglu", "geglu")
 ACTS = ("swiglu", "geglu", "srelu", "none", "silu", "gelu")  # index: the library's code
@@ -104,8 +104,3 @@ def balance_loss(logits, topk_idx, valid=None, seq_offsets=None, balance_coef=1.
         d[t] += z_coef * 2 * lse[t] / ntot * p[t]
     return {"loss": np.array([balance_coef * bal + z_coef * z, bal, z]), "counts": counts, "prob": prob,
             "tokens": np.concatenate([n, [nlive, ntot]]), "dlogits": d}
-
-
-def checkpoint_values(q, s):
-    """Values of a row-wise 8-bit checkpoint."""
-    return mx_dequant(q, s)

@@ -36,7 +36,11 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
 // A workgroup takes 32 groups of 8 output columns (gated: with their 8 gate and
 // 8 up columns) and `rows` rows, 8 rows at a time; a thread keeps its columns'
 // sums of dz (fp32, before the rounding) in registers over the rows, joined over
-// the 8 row lanes in LDS in a fixed order.
+// the 8 row lanes in LDS in a fixed order. dz leaves as bf16 because both gradient
+// products read it on the bf16 matrix cores: each of its values moves by up to 2^-8, and
+// dx and dw, an fp32 dw too, are with it off by 0.23 to 0.24% in norm (0.17% from
+// rounding dx or dw itself to bf16). An fp32 dz would need the products on fp32 matrix
+// instructions, a sixteenth of the bf16 rate.
 template <int ACT, bool Z8>
 __global__ void __launch_bounds__(256) act_bwd_kernel(ActArgs p) {
     constexpr bool G = ACT < 2;

@@ -23,7 +23,9 @@ constexpr int DBK = 64;  // K elements per slab (128 bytes)
 //   'D' 128 x 128 tiles, four stages, one on a compute unit: 0.53 to 0.73 a slab, 4.0;
 //   'H' 256 x 128 tiles, three stages, one on a compute unit: 0.82 to 0.92 a slab, 5.0 (9.0
 //       in the forward, whose activation no neighbour's products cover: 1000 x 2880 x 5760
-//       51.1 us with GeGLU, M 47.2; without an activation 45.4 and 49.6);
+//       51.1 us with GeGLU, M 47.2). The plan does not see the activation: a forward without
+//       one would be 8% faster as H there (45.4 and 49.6) and takes M all the same. About
+//       one forward shape in 2000 takes H (10959 x 3360 x 320);
 //   'L' 256 x 256 tiles, two stages: 1.05 a slab with few of them at work up to 1.7 with
 //       all (clock and L2), 8.0;
 //   any: no less than 1.0 and the operands' read, at 5.2 TB/s with every compute unit at

@@ -596,7 +596,9 @@ class SharedExpert:
     """The expert every token passes, beside the routed ones: out += f(x w1) w2, with w1 [d, 2n]
     (gated; interleaved like the routed experts' W1) or [d, n], w2 [n, d]. Between forward and
     backward it keeps z = x w1 as an 8-bit checkpoint (ckpt8) or as bf16; f(z) is recomputed. With
-    x8 it keeps an 8-bit checkpoint of x too, and the backward needs no x."""
+    x8 it keeps an 8-bit checkpoint of x too, and the backward needs no x. out and dx are rounded to
+    bf16 with the routed part in them and once more with this expert's added; dw1 and dw2 are
+    written, not added to."""
 
     def __init__(self, T: int, d: int, n: int, act: int = MOE_ACT_SWIGLU, ckpt8: bool = True, x8: bool = False,
                  device="cuda"):
@@ -673,7 +675,9 @@ class Router:
 
     def backward(self, x, wg, dlogits, dx, grad=None):
         """dlogits += the losses' gradient (times grad, their upstream gradient); dwg; dx += the
-        gradient through the projection (both products take dlogits rounded to bf16)."""
+        gradient through the projection. Both products run on bf16 matrix cores and take the fp32
+        dlogits rounded to bf16, so dwg, though fp32, is off by up to 2^-8 of each term; dwg is
+        written, not added to."""
         moe_balance_loss_bwd(self.logits, self.counts, self.tokens, dlogits, self.k, self.balance_coef, self.z_coef,
                              valid=self.valid, seq_offsets=self.seq_offsets, grad=grad, accumulate=True,
                              dlogits_bf16=self.dlogits16)
