@@ -657,7 +657,7 @@ class Router:
         if self.wide is None:
             return wg
         _operand(wg, self.dwg.shape, _BF, "wg", self.logits.get_device())
-        self.wide[0][:, :wg.shape[1]].copy_(wg)
+        self.wide[0][:, :wg.shape[1]].copy_(wg.detach())
         return self.wide[0]
 
     def project(self, x, wg):

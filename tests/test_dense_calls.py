@@ -116,3 +116,14 @@ def test_sizes_past_32_bits_are_refused(lib, monkeypatch, name, call):
     with pytest.raises(ValueError, match="32 bits"):
         call(lambda *s, t=BF: torch.empty(*s, dtype=t, device="meta"))
     assert lib.reached == []
+
+
+def test_a_trained_weight_leaves_no_history_in_the_routers_copy(lib):
+    """12 experts: the padded copy must not join the weight's autograd graph, which would grow by a step a call."""
+    router = M.Router(6, 64, 12, 2, device="cpu")
+    wg = torch.nn.Parameter(torch.ones(64, 12, dtype=BF))
+    with pytest.raises(ValueError, match="GPU"):        # after the copy, on host tensors here
+        router.project(_z(6, 64), wg)
+    wide = router.wide[0]
+    assert (wide[:, :12] == 1).all() and (wide[:, 12:] == 0).all()
+    assert not wide.requires_grad and wide.grad_fn is None
