@@ -67,7 +67,7 @@ def draw(rng):
         kept = rng.randint(max(1, groups // 4), groups)
         score, k = rng.choice(["sigmoid", "softmax"]), rng.randint(1, min(8, kept * (E // groups)))
         return {"op": op, "T": _log(rng, 1, 131072), "E": E, "k": k, "score": score,
-                "bias": rng.random() < 0.6, "dead": rng.choice([0, 0, 1]), "groups": groups, "kept": kept, "top": rng.randint(1, 2),
+                "bias": rng.random() < 0.6, "dead": int(k < kept * (E // groups) and rng.random() < 0.3), "groups": groups, "kept": kept, "top": rng.randint(1, 2),
                 "renorm": k > 1 and rng.random() < 0.7, "scale": rng.choice([1.0, 2.5]), "bwd": rng.random() < 0.6}  # a lone weight of 1 has no gradient
     if op == "quant":
         if rng.random() < 0.5:
