@@ -552,6 +552,138 @@ int moe_balance_loss_bwd(const float* logits, const int32_t* counts, const int32
                          float z_coef, const float* grad, int accumulate, float* dlogits, uint16_t* dlogits_bf16,
                          moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Around a MoE block: the router with scores, a balance bias and groups; 4-bit
+ * blocks and the experts' products with them; the norms before and after.
+ * ------------------------------------------------------------------------- */
+
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_MAX_TOPK 64       /* largest k of moe_route_scores      */
+#define MOE_MAX_GROUPS 64     /* largest number of expert groups    */
+
+/* How tokens choose experts. */
+typedef struct moe_routing {
+    int score;        /* MOE_SCORE_*: s = softmax over all E, or sigmoid, of the logits           */
+    int groups;       /* the E experts as so many groups of neighbours (a divisor of E); 1: none */
+    int topk_groups;  /* groups that a token keeps                                              */
+    int group_top;    /* a group is worth its best choice value (1) or the sum of its two best (2) */
+    int renorm;       /* weights divided by their sum over the chosen k                        */
+    float scale;      /* factor of all weights                                                 */
+} moe_routing;
+
+/* Device workspace (bytes) of moe_route_scores. Host-only. */
+size_t moe_route_scores_workspace_bytes(int T, int k, int E);
+
+/*
+ * moe_route_scores -- moe_route_counts with a choice of scores: with s the
+ *   scores of a token's logits and b a bias that takes part in the choice alone,
+ *   c_e = s_e + b_e; the topk_groups groups of largest value are kept; slot j
+ *   holds the expert of j-th largest c in them, and
+ *   topk_w[t, j] = scale s_{e_j} (/ sum_i s_{e_i} with renorm).
+ *   The order is that of the exact values (formed in 64 bits where they lie
+ *   near), ties to the lower index; without a bias experts are ordered by their
+ *   logits. An expert whose logit or bias is not finite (a bias of -inf takes
+ *   one out of service) is chosen only when its kept groups hold too few others,
+ *   lowest index first, and then weighs 0; a non-finite logit sets
+ *   MOE_ERRBIT_NONFINITE_LOGIT, has no part in the softmax and none in a
+ *   group's value.
+ *   logits [T, E] fp32, bias [E] fp32 or NULL (in); the outputs, err_word and
+ *   M_cap as of moe_route_counts.
+ *   workspace: moe_route_scores_workspace_bytes(T, k, E) bytes, 16-byte aligned.
+ * Requires 1 <= k <= E <= MOE_MAX_EXPERTS, k <= MOE_MAX_TOPK, at most the experts
+ * of topk_groups groups, groups <= MOE_MAX_GROUPS.
+ */
+int moe_route_scores(const float* logits, const float* bias, const moe_routing* how, int T, int E, int k,
+                     int32_t* topk_idx, float* topk_w, int32_t* counts, int32_t* offsets, int32_t* row_of,
+                     int32_t* src_of, int64_t M_cap, int32_t* err_word, void* workspace, size_t workspace_bytes,
+                     moe_stream_t stream);
+
+/*
+ * moe_route_scores_bwd -- gradient w.r.t. the logits given ds = dL/dtopk_w, for
+ *   the experts chosen (topk_idx as moe_route_scores wrote it; the choice itself
+ *   and the bias have none). An expert that weighs 0 for want of a finite logit
+ *   or bias has none either. dlogits [T, E] fp32 (out, every element).
+ */
+int moe_route_scores_bwd(const float* logits, const float* bias, const moe_routing* how, const int32_t* topk_idx,
+                         const float* ds, int T, int E, int k, float* dlogits, moe_stream_t stream);
+
+/*
+ * moe_quant_mxfp4 -- MXFP4 quantization of `batch` bf16 matrices src [batch, R, C]:
+ *   blocks of 32 values share the smallest E8M0 scale 2^e with amax <= 6 * 2^e, so
+ *   that none is clipped, and are E2M1 codes, rounded to nearest-even, two a byte
+ *   (the first in the low half). A value moves by at most a quarter of itself
+ *   while it lies in its block's normal range, by at most 2^(e-2) below it. A
+ *   block with a NaN or an infinity takes scale 255 and is NaN as a whole.
+ *   MOE_QUANT_ROWWISE: blocks along the columns; q_row [batch, R, C / 2], s_row
+ *     [batch, R, C / 32]. Needs C % 32 == 0.
+ *   MOE_QUANT_COLWISE: blocks along the rows, stored transposed; q_col
+ *     [batch, C, R / 2], s_col [batch, C, R / 32]: weights [E, K, N] as
+ *     moe_grouped_linear_mxfp4 reads them. Needs R % 32 == 0, C % 8 == 0.
+ *   src and the codes 16-byte aligned.
+ */
+int moe_quant_mxfp4(const uint16_t* src, int batch, int64_t R, int C, int mode, uint8_t* q_row, uint8_t* s_row,
+                    uint8_t* q_col, uint8_t* s_col, moe_stream_t stream);
+
+/* moe_dequant_mxfp4 -- bf16 values [R, C] of row-wise codes q [R, C / 2] and scales
+ *   s [R, C / 32]; exact wherever code * scale is a bf16 number. Requires C % 32 == 0. */
+int moe_dequant_mxfp4(const uint8_t* q, const uint8_t* s, int64_t R, int C, uint16_t* out, moe_stream_t stream);
+
+#define MOE_MAX_NORM_WIDTH 16384 /* largest d of the norms */
+#define MOE_GATE_LINEAR 0        /* the gate's values as they are */
+#define MOE_GATE_SIGMOID 1       /* their logistic sigmoid        */
+
+/* Device workspace (bytes) of moe_norm_bwd and moe_post_norm_bwd where dw is asked
+ * for. Host-only. */
+size_t moe_norm_workspace_bytes(int T, int d);
+
+/*
+ * moe_norm_fwd -- the norm before a block, with the residual sum: total = x +
+ *   residual, rounded to bf16 (both NULL: x itself is normalised), rstd = 1 /
+ *   sqrt(mean(total^2) + eps), y = total rstd w.
+ *   x, residual, total, y [T, d], w [d] bf16; rstd [T] fp32, or NULL. total may be
+ *   x or residual, and y may be x where there is no residual.
+ *   Sums are fp32, y is rounded once; the squares' mean must lie within fp32.
+ * Requires d % 8 == 0, d <= MOE_MAX_NORM_WIDTH, eps > 0, 16-byte aligned bf16
+ * tensors, as the three entry points below.
+ */
+int moe_norm_fwd(const uint16_t* x, const uint16_t* residual, const uint16_t* w, int T, int d, float eps,
+                 uint16_t* total, uint16_t* y, float* rstd, moe_stream_t stream);
+
+/*
+ * moe_norm_bwd -- dx = rstd (g - h mean(g h)) + dres with h = x rstd, g = dy w; dw =
+ *   sum over t of dy h. x is what was normalised (total, where there was one), so
+ *   dx is the gradient of x and of the residual alike; dres [T, d] or NULL is the
+ *   gradient that reaches it by the residual stream. dx bf16 (may be dy or dres),
+ *   dw [d] fp32 or NULL, summed in a fixed order.
+ */
+int moe_norm_bwd(const uint16_t* dy, const uint16_t* x, const uint16_t* w, const float* rstd, const uint16_t* dres,
+                 int T, int d, uint16_t* dx, float* dw, void* workspace, size_t workspace_bytes,
+                 moe_stream_t stream);
+
+/*
+ * moe_post_norm_fwd -- after a block: out = x + scale f(gate) (y rstd w).
+ *   With row_of != NULL y holds the experts' rows and the block's output is their
+ *   weighted sum, rounded to bf16 as moe_combine gives it (topk_w NULL: unit
+ *   weights); it is stored in total [T, d] when that is not NULL. Else y is [T, d].
+ *   gate: NULL (gate_cols 0), one a token [T] (1), or one a channel [T, d] (d); f
+ *   is the identity or the sigmoid (gate_act). x [T, d]: the residual stream; out
+ *   may be x. rstd [T] fp32 or NULL.
+ */
+int moe_post_norm_fwd(const uint16_t* y, const int32_t* row_of, const float* topk_w, int k, const uint16_t* x,
+                      const uint16_t* w, const uint16_t* gate, int gate_cols, int gate_act, float scale, float eps,
+                      int T, int d, uint16_t* total, uint16_t* out, float* rstd, moe_stream_t stream);
+
+/*
+ * moe_post_norm_bwd -- gradients of y [T, d] (the block's output: total, where the
+ *   rows were combined; moe_grouped_mlp_bwd takes dy from there), of the gate
+ *   (bf16 [T, d], or fp32 [T] for one a token; NULL: not wanted) and of w (fp32,
+ *   or NULL). The gradient of x is dout itself. dy may be dout.
+ */
+int moe_post_norm_bwd(const uint16_t* dout, const uint16_t* y, const uint16_t* w, const float* rstd,
+                      const uint16_t* gate, int gate_cols, int gate_act, float scale, int T, int d, uint16_t* dy,
+                      void* dgate, float* dw, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,6 +20,7 @@
 //   per (token, expert) pair, regions padded to the alignment unit.]
 #include <mutex>
 
+#include "block_launch.hpp"
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -675,13 +676,17 @@ struct RoutePlan {
 constexpr int64_t kFusedHist = 65536, kFusedHistReads = (int64_t)8 << 20;
 constexpr int kFusedPasses = 2;
 
+bool layout_fused_fits(int64_t nchunks, int E) {
+    return nchunks * E <= kFusedHist && nchunks * nchunks * E <= kFusedHistReads;
+}
+
 static RoutePlan route_plan(int T, int k, int E) {
     RoutePlan pl{};
     pl.G = E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64;
     for (int passes = 1; passes <= kFusedPasses; passes *= 2) {
         const int64_t ct = (int64_t)(kRouteBlock / pl.G) * passes;
         const int64_t nc = ((int64_t)T + ct - 1) / ct;
-        if (nc * E <= kFusedHist && nc * nc * E <= kFusedHistReads) {
+        if (layout_fused_fits(nc, E)) {
             pl.fused = true;
             pl.nchunks = (int)nc;
             pl.CT = (int)ct;
@@ -693,14 +698,35 @@ static RoutePlan route_plan(int T, int k, int E) {
     return pl;
 }
 
+static int expert_bits(int E) {
+    int nbits = 0;
+    while ((1 << nbits) < E) ++nbits;
+    return nbits;
+}
+
+void launch_layout_fused(const int32_t* topk_idx, int T, int k, int E, int CT, int nchunks, const int32_t* hist,
+                         int32_t* counts, int32_t* offsets, int32_t* row_of, int32_t* src_of, hipStream_t s) {
+    layout_chunk_kernel<<<nchunks, 256, 0, s>>>(topk_idx, T, k, E, expert_bits(E), CT, nchunks, hist, counts, offsets,
+                                                row_of, src_of);
+}
+
+void launch_layout(const int32_t* topk_idx, int T, int k, int E, int nchunks, int32_t* hist, int32_t* counts,
+                   int32_t* offsets, int32_t* row_of, int32_t* src_of, int64_t M_cap, hipStream_t s) {
+    const int64_t P = (int64_t)T * k;
+    int32_t* base = hist + (int64_t)nchunks * E;
+    const int nblk = (nchunks + 3) / 4;
+    const size_t lds = 4 * (size_t)E * sizeof(int32_t);
+    layout_hist_kernel<<<nblk, 256, lds, s>>>(topk_idx, P, E, nchunks, hist, src_of, M_cap);
+    layout_scan_kernel<<<E, 256, 0, s>>>(hist, nchunks, E, base, counts);
+    layout_scatter_kernel<<<nblk, 256, lds, s>>>(topk_idx, P, E, expert_bits(E), nchunks, base, counts, offsets,
+                                                 row_of, src_of);
+}
+
 int launch_route(const float* logits, int T, int E, int k, int renorm, int32_t* topk_idx,
                  float* topk_w, int32_t* counts, int32_t* offsets, int32_t* row_of,
                  int32_t* src_of, int64_t M_cap, int32_t* err_word, void* ws, hipStream_t s) {
     const RoutePlan pl = route_plan(T, k, E);
-    const int64_t P = (int64_t)T * k;
     int32_t* hist = (int32_t*)ws;
-    int nbits = 0;
-    while ((1 << nbits) < E) ++nbits;
     if (pl.fused) {
         auto first = [&](auto kern) {
             kern<<<pl.nchunks, kRouteBlock, 0, s>>>(logits, T, E, k, renorm, pl.CT, topk_idx, topk_w, err_word,
@@ -720,11 +746,9 @@ int launch_route(const float* logits, int T, int E, int k, int renorm, int32_t* 
             first(route_chunk_kernel<64, 8>);
         else
             first(route_chunk_kernel<64, MOE_MAX_E / 64>);
-        layout_chunk_kernel<<<pl.nchunks, 256, 0, s>>>(topk_idx, T, k, E, nbits, pl.CT, pl.nchunks, hist,
-                                                       counts, offsets, row_of, src_of);
+        launch_layout_fused(topk_idx, T, k, E, pl.CT, pl.nchunks, hist, counts, offsets, row_of, src_of, s);
         return hipGetLastError() == hipSuccess ? 0 : -4;
     }
-    int32_t* base = hist + (int64_t)pl.nchunks * E;
     auto topk = [&](auto kern) {
         const int64_t blocks = ((int64_t)T * pl.G + 255) / 256;
         kern<<<(unsigned)blocks, 256, 0, s>>>(logits, T, E, k, renorm, topk_idx, topk_w, err_word);
@@ -743,12 +767,7 @@ int launch_route(const float* logits, int T, int E, int k, int renorm, int32_t* 
         topk(route_topk_kernel<64, 8>);
     else
         topk(route_topk_kernel<64, MOE_MAX_E / 64>);
-    const int nblk = (pl.nchunks + 3) / 4;
-    const size_t lds = 4 * (size_t)E * sizeof(int32_t);
-    layout_hist_kernel<<<nblk, 256, lds, s>>>(topk_idx, P, E, pl.nchunks, hist, src_of, M_cap);
-    layout_scan_kernel<<<E, 256, 0, s>>>(hist, pl.nchunks, E, base, counts);
-    layout_scatter_kernel<<<nblk, 256, lds, s>>>(topk_idx, P, E, nbits, pl.nchunks, base, counts, offsets,
-                                                 row_of, src_of);
+    launch_layout(topk_idx, T, k, E, pl.nchunks, hist, counts, offsets, row_of, src_of, M_cap, s);
     return hipGetLastError() == hipSuccess ? 0 : -4;
 }
 

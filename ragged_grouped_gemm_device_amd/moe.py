@@ -46,6 +46,13 @@ MOE_ERRBIT_NONFINITE_LOGIT = 0x1
 MOE_QUANT_ROWWISE = 0x1
 MOE_QUANT_COLWISE = 0x2
 MOE_ROUTE_STATIC_SCRATCH_BYTES = 8 << 20
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_MAX_TOPK = 64
+MOE_MAX_GROUPS = 64
+MOE_MAX_NORM_WIDTH = 16384
+MOE_GATE_LINEAR = 0
+MOE_GATE_SIGMOID = 1
 
 # (name, restype, argtypes) of every exported symbol
 _P = C.c_void_p
@@ -77,6 +84,16 @@ SIGNATURES = {
     "moe_balance_workspace_bytes": (_SZ, [_I, _I, _I]),
     "moe_balance_loss": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, C.c_float, C.c_float, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_balance_loss_bwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, C.c_float, C.c_float, _P, _I, _P, _P, _P]),
+    "moe_route_scores_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_route_scores": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "moe_route_scores_bwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P]),
+    "moe_quant_mxfp4": (_I, [_P, _I, _I64, _I, _I, _P, _P, _P, _P, _P]),
+    "moe_dequant_mxfp4": (_I, [_P, _P, _I64, _I, _P, _P]),
+    "moe_norm_workspace_bytes": (_SZ, [_I, _I]),
+    "moe_norm_fwd": (_I, [_P, _P, _P, _I, _I, C.c_float, _P, _P, _P, _P]),
+    "moe_norm_bwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _SZ, _P]),
+    "moe_post_norm_fwd": (_I, [_P, _P, _P, _I, _P, _P, _P, _I, _I, C.c_float, C.c_float, _I, _I, _P, _P, _P, _P]),
+    "moe_post_norm_bwd": (_I, [_P, _P, _P, _P, _P, _I, _I, C.c_float, _I, _I, _P, _P, _P, _P, _SZ, _P]),
 }
 
 
@@ -99,6 +116,10 @@ class moe_mx_fwd(C.Structure):
 
 class moe_mx_bwd(C.Structure):
     _fields_ = [(name, _P) for name in MX_BWD_FIELDS]
+
+
+class moe_routing(C.Structure):
+    _fields_ = [("score", _I), ("groups", _I), ("topk_groups", _I), ("group_top", _I), ("renorm", _I), ("scale", C.c_float)]
 
 
 _LIB = None
@@ -472,6 +493,179 @@ def moe_balance_loss_bwd(logits, counts, tokens, dlogits, k, balance_coef, z_coe
                                      k, S, balance_coef, z_coef, _ptr(grad), int(bool(accumulate)), _ptr(dlogits),
                                      _ptr(dlogits_bf16), _stream(dev))
     _check("moe_balance_loss_bwd", rc)
+
+
+# ------------------------------------------------------------------ around the block
+class Routing:
+    """How tokens choose experts (moe_route_scores): scores (MOE_SCORE_*), a bias [E] fp32 that takes
+    part in the choice alone (kept by reference; -inf takes an expert out of service), groups of
+    neighbouring experts of which a token keeps topk_groups (a group is worth its best choice value, or
+    with group_top = 2 the sum of its two best), and weights, renormalised over the chosen and scaled."""
+
+    def __init__(self, score=MOE_SCORE_SIGMOID, bias=None, groups=1, topk_groups=1, group_top=2, renorm=True,
+                 scale=1.0):
+        self.bias = bias
+        self.how = moe_routing(score, groups, topk_groups, group_top, int(bool(renorm)), scale)
+        self.ref = C.byref(self.how)
+
+
+def moe_route_scores_workspace_bytes(T: int, k: int, E: int) -> int:
+    return int(_lib().moe_route_scores_workspace_bytes(T, k, E))
+
+
+def moe_route_scores(logits, k, topk_idx, topk_w, counts, offsets, row_of, src_of, err_word, workspace, routing):
+    """moe_route_counts with the scores, bias, groups and weights of a Routing."""
+    dev = _device(logits)
+    T, E = logits.shape
+    _sizes(T, E, k)
+    _operand(logits, (T, E), _F32, "logits", dev)
+    _operand(routing.bias, (E,), _F32, "bias", dev)
+    _operand(topk_idx, (T, k), _I32, "topk_idx", dev)
+    _operand(topk_w, (T, k), _F32, "topk_w", dev)
+    _operand(counts, (E,), _I32, "counts", dev)
+    _operand(offsets, (E + 1,), _I32, "offsets", dev)
+    _operand(row_of, (T * k,), _I32, "row_of", dev)
+    _operand(src_of, (src_of.numel(),), _I32, "src_of", dev)
+    _operand(err_word, (1,), _I32, "err_word", dev)
+    ws, nws = _space(workspace, dev)
+    _check("moe_route_scores", _lib().moe_route_scores(
+        _ptr(logits), _ptr(routing.bias), routing.ref, T, E, k, _ptr(topk_idx), _ptr(topk_w), _ptr(counts),
+        _ptr(offsets), _ptr(row_of), _ptr(src_of), src_of.numel(), _ptr(err_word), ws, nws, _stream(dev)))
+
+
+def moe_route_scores_bwd(logits, topk_idx, ds, dlogits, routing):
+    """dlogits [T, E] from ds = dL/dtopk_w, for the experts that moe_route_scores chose."""
+    dev = _device(logits)
+    (T, E), k = logits.shape, topk_idx.shape[1]
+    _sizes(T, E, k)
+    _operand(logits, (T, E), _F32, "logits", dev)
+    _operand(routing.bias, (E,), _F32, "bias", dev)
+    _operand(topk_idx, (T, k), _I32, "topk_idx", dev)
+    _operand(ds, (T, k), _F32, "ds", dev)
+    _operand(dlogits, (T, E), _F32, "dlogits", dev)
+    _check("moe_route_scores_bwd", _lib().moe_route_scores_bwd(
+        _ptr(logits), _ptr(routing.bias), routing.ref, _ptr(topk_idx), _ptr(ds), T, E, k, _ptr(dlogits), _stream(dev)))
+
+
+def moe_quant_mxfp4(src, mode, q_row=None, s_row=None, q_col=None, s_col=None):
+    """MXFP4 codes (two a byte) and scales of src [R, C] or [batch, R, C]: row-wise [.., R, C / 2] and
+    [.., R, C / 32], column-wise and transposed [.., C, R / 2] and [.., C, R / 32]."""
+    dev = _device(src)
+    lead, (R, Cc) = tuple(src.shape[:-2]), src.shape[-2:]
+    batch = lead[0] if lead else 1
+    _sizes(0, Cc, batch)
+    if src.dim() not in (2, 3):
+        raise ValueError(f"src: {src.dim()} dimensions; 2 or 3 expected")
+    _operand(src, src.shape, _BF, "src", dev)
+    _operand(q_row, lead + (R, Cc // 2), _U8, "q_row", dev)
+    _operand(s_row, lead + (R, Cc // MOE_MX_BLOCK), _U8, "s_row", dev)
+    _operand(q_col, lead + (Cc, R // 2), _U8, "q_col", dev)
+    _operand(s_col, lead + (Cc, R // MOE_MX_BLOCK), _U8, "s_col", dev)
+    _check("moe_quant_mxfp4", _lib().moe_quant_mxfp4(_ptr(src), batch, R, Cc, mode, _ptr(q_row), _ptr(s_row),
+                                                     _ptr(q_col), _ptr(s_col), _stream(dev)))
+
+
+def moe_dequant_mxfp4(q, s, out):
+    """bf16 values [R, C] of row-wise MXFP4 codes [R, C / 2] and scales [R, C / 32]."""
+    dev = _device(out)
+    R, Cc = out.shape
+    _sizes(0, Cc)
+    _operand(q, (R, Cc // 2), _U8, "q", dev)
+    _operand(s, (R, Cc // MOE_MX_BLOCK), _U8, "s", dev)
+    _operand(out, (R, Cc), _BF, "out", dev)
+    _check("moe_dequant_mxfp4", _lib().moe_dequant_mxfp4(_ptr(q), _ptr(s), R, Cc, _ptr(out), _stream(dev)))
+
+
+def moe_norm_workspace_bytes(T: int, d: int) -> int:
+    return int(_lib().moe_norm_workspace_bytes(T, d))
+
+
+def moe_norm_fwd(x, w, y, rstd=None, eps=1e-6, residual=None, total=None):
+    """total = x + residual (bf16), y = total rstd w; without a residual, x itself is normalised."""
+    dev = _device(x)
+    T, d = x.shape
+    _sizes(T, d)
+    _operand(x, (T, d), _BF, "x", dev)
+    _operand(residual, (T, d), _BF, "residual", dev)
+    _operand(w, (d,), _BF, "w", dev)
+    _operand(total, (T, d), _BF, "total", dev)
+    _operand(y, (T, d), _BF, "y", dev)
+    _operand(rstd, (T,), _F32, "rstd", dev)
+    _check("moe_norm_fwd", _lib().moe_norm_fwd(_ptr(x), _ptr(residual), _ptr(w), T, d, eps, _ptr(total), _ptr(y),
+                                               _ptr(rstd), _stream(dev)))
+
+
+def moe_norm_bwd(dy, x, w, rstd, dx, dw=None, workspace=None, dres=None):
+    """dx (+ dres, the residual stream's gradient) and dw of a norm of x."""
+    dev = _device(dy)
+    T, d = dy.shape
+    _sizes(T, d)
+    for t, name in ((dy, "dy"), (x, "x"), (dres, "dres"), (dx, "dx")):
+        _operand(t, (T, d), _BF, name, dev)
+    _operand(w, (d,), _BF, "w", dev)
+    _operand(rstd, (T,), _F32, "rstd", dev)
+    _operand(dw, (d,), _F32, "dw", dev)
+    ws, nws = _space(workspace, dev)
+    _check("moe_norm_bwd", _lib().moe_norm_bwd(_ptr(dy), _ptr(x), _ptr(w), _ptr(rstd), _ptr(dres), T, d, _ptr(dx),
+                                               _ptr(dw), ws, nws, _stream(dev)))
+
+
+def _gate(gate, T, d, dev):
+    """Columns of a post norm's gate: 0 (none), 1 (one a token) or d."""
+    if gate is None:
+        return 0
+    cols = gate.shape[1] if gate.dim() == 2 else -1
+    if cols not in (1, d):
+        raise ValueError(f"gate: {tuple(gate.shape)}; expected {(T, 1)} or {(T, d)}")
+    _operand(gate, (T, cols), _BF, "gate", dev)
+    return cols
+
+
+def moe_post_norm_fwd(y, x, w, out, rstd=None, eps=1e-6, gate=None, gate_act=MOE_GATE_LINEAR, scale=1.0, row_of=None,
+                      topk_w=None, total=None):
+    """out = x + scale f(gate) (norm(y) w). With row_of [T * k], y holds the experts' rows and their sum
+    weighted by topk_w [T, k] is normalised (and stored in total)."""
+    dev = _device(x)
+    T, d = x.shape
+    _sizes(T, d)
+    k = 0
+    if row_of is None:
+        _operand(y, (T, d), _BF, "y", dev)
+    else:
+        k = row_of.numel() // max(T, 1)
+        _operand(row_of, (T * k,), _I32, "row_of", dev)
+        _operand(y, (y.shape[0], d), _BF, "y", dev)
+        _operand(topk_w, (T, k), _F32, "topk_w", dev)
+    for t, name in ((x, "x"), (total, "total"), (out, "out")):
+        _operand(t, (T, d), _BF, name, dev)
+    _operand(w, (d,), _BF, "w", dev)
+    _operand(rstd, (T,), _F32, "rstd", dev)
+    cols = _gate(gate, T, d, dev)
+    _check("moe_post_norm_fwd", _lib().moe_post_norm_fwd(
+        _ptr(y), _ptr(row_of), _ptr(topk_w), k, _ptr(x), _ptr(w), _ptr(gate), cols, gate_act, scale, eps, T, d,
+        _ptr(total), _ptr(out), _ptr(rstd), _stream(dev)))
+
+
+def moe_post_norm_bwd(dout, y, w, rstd, dy, dw=None, workspace=None, gate=None, dgate=None, gate_act=MOE_GATE_LINEAR,
+                      scale=1.0):
+    """Gradients of the block's output y, the gate (bf16 [T, d], fp32 [T, 1]) and w; x's is dout."""
+    dev = _device(dout)
+    T, d = dout.shape
+    _sizes(T, d)
+    for t, name in ((dout, "dout"), (y, "y"), (dy, "dy")):
+        _operand(t, (T, d), _BF, name, dev)
+    _operand(w, (d,), _BF, "w", dev)
+    _operand(rstd, (T,), _F32, "rstd", dev)
+    _operand(dw, (d,), _F32, "dw", dev)
+    cols = _gate(gate, T, d, dev)
+    if dgate is not None:
+        if gate is None:
+            raise ValueError("dgate: there is no gate")
+        _operand(dgate, (T, cols), _F32 if cols == 1 else _BF, "dgate", dev)
+    ws, nws = _space(workspace, dev)
+    _check("moe_post_norm_bwd", _lib().moe_post_norm_bwd(
+        _ptr(dout), _ptr(y), _ptr(w), _ptr(rstd), _ptr(gate), cols, gate_act, scale, T, d, _ptr(dy), _ptr(dgate),
+        _ptr(dw), ws, nws, _stream(dev)))
 
 
 # ------------------------------------------------------------------ buffers
