@@ -629,6 +629,36 @@ int moe_quant_mxfp4(const uint16_t* src, int batch, int64_t R, int C, int mode, 
  *   s [R, C / 32]; exact wherever code * scale is a bf16 number. Requires C % 32 == 0. */
 int moe_dequant_mxfp4(const uint8_t* q, const uint8_t* s, int64_t R, int C, uint16_t* out, moe_stream_t stream);
 
+/* forms of the rows that the 4-bit product reads */
+#define MOE_X_BF16 0
+#define MOE_X_MXFP8 1   /* codes [rows, K], scales [rows, K / 32], as moe_quant_mxfp8 writes row-wise */
+#define MOE_X_MXFP4 2   /* codes [rows, K / 2], scales [rows, K / 32], as moe_quant_mxfp4 does      */
+
+/* Device workspace (bytes) of moe_grouped_linear_mxfp4. Host-only. */
+size_t moe_grouped_linear_mxfp4_workspace_bytes(int T, int k, int E, int K, int N);
+
+/*
+ * moe_grouped_linear_mxfp4 -- one product of all experts with 4-bit weights:
+ *   y[r] = f(x_r W_e) for the counts[e] rows r from offsets[e] of every expert e,
+ *   with W_e [K, N] given transposed as MXFP4: w_q [E, N, K / 2], w_s [E, N, K / 32]
+ *   (moe_quant_mxfp4 of w [E, K, N], column-wise). x_r is row r of x [M_cap, K]
+ *   (the experts' buffer), or with src_of != NULL row src_of[r] / k of x [T, K]:
+ *   tokens are read, and quantized, once, and not copied k times.
+ *   act: any MOE_ACT_*; the gated ones take N as 32 gate and 32 up columns in turn
+ *   and give y [M_cap, N / 2], the others y [M_cap, N] (bf16). Sums and f are fp32,
+ *   y is rounded once. Rows past an expert's counts[e] are neither read nor
+ *   written, of x and y alike.
+ *   T, k: the routing's sizes (the host does not know the counts).
+ *   workspace: moe_grouped_linear_mxfp4_workspace_bytes(T, k, E, K, N) bytes.
+ * Requires K % 32 == 0, N % 8 == 0 (64 when gated), both at most MOE_MAX_WIDTH,
+ * M_cap >= moe_capacity_rows(T, k, E), 16-byte aligned x, w_q and y; gathered
+ * rows within 2^31 bytes.
+ */
+int moe_grouped_linear_mxfp4(const void* x, const uint8_t* x_s, int x_fmt, const int32_t* src_of, int T, int k,
+                             const uint8_t* w_q, const uint8_t* w_s, const int32_t* offsets, const int32_t* counts,
+                             int E, int K, int N, int64_t M_cap, int act, uint16_t* y, void* workspace,
+                             size_t workspace_bytes, moe_stream_t stream);
+
 #define MOE_MAX_NORM_WIDTH 16384 /* largest d of the norms */
 #define MOE_GATE_LINEAR 0        /* the gate's values as they are */
 #define MOE_GATE_SIGMOID 1       /* their logistic sigmoid        */

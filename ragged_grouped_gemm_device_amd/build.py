@@ -14,7 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["api.cpp", "api_dense.cpp", "route.hip", "permute.hip", "gemm.hip", "mx.hip", "dense.hip", "act.hip",
-           "balance.hip", "api_block.cpp", "router.hip", "mxfp4.hip", "norm.hip"]
+           "balance.hip", "api_block.cpp", "router.hip", "mxfp4.hip", "experts4.hip", "norm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

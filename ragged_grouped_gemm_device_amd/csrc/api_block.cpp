@@ -109,6 +109,33 @@ int moe_dequant_mxfp4(const uint8_t* q, const uint8_t* s, int64_t R, int C, uint
     return status(moe::launch_dequant_mxfp4(q, s, R, C, out, S(stream)));
 }
 
+size_t moe_grouped_linear_mxfp4_workspace_bytes(int T, int k, int E, int K, int N) {
+    return 0;
+}
+
+int moe_grouped_linear_mxfp4(const void* x, const uint8_t* x_s, int x_fmt, const int32_t* src_of, int T, int k,
+                             const uint8_t* w_q, const uint8_t* w_s, const int32_t* offsets, const int32_t* counts,
+                             int E, int K, int N, int64_t M_cap, int act, uint16_t* y, void* workspace,
+                             size_t workspace_bytes, moe_stream_t stream) {
+    const int64_t cap = moe_capacity_rows(T, k, E);
+    if (cap < 0 || K <= 0 || N <= 0) return MOE_ERR_INVALID_ARG;
+    if (!x || !w_q || !w_s || !offsets || !counts || !y || !aligned({x, w_q, y})) return MOE_ERR_INVALID_ARG;
+    if (x_fmt != MOE_X_BF16 && x_fmt != MOE_X_MXFP8 && x_fmt != MOE_X_MXFP4) return MOE_ERR_UNSUPPORTED;
+    if (!x_s != (x_fmt == MOE_X_BF16)) return MOE_ERR_INVALID_ARG;
+    if (act < MOE_ACT_SWIGLU || act > MOE_ACT_GELU) return MOE_ERR_UNSUPPORTED;
+    const bool gated = act == MOE_ACT_SWIGLU || act == MOE_ACT_GEGLU;
+    if (K % MOE_MX_BLOCK || N % (gated ? 2 * MOE_GLU_INTERLEAVE : 8)) return MOE_ERR_UNSUPPORTED;
+    if (K > MOE_MAX_WIDTH || N > MOE_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
+    if (M_cap < cap || M_cap > INT32_MAX) return MOE_ERR_WORKSPACE;
+    // gathered rows are addressed from x with 32-bit byte offsets
+    const int64_t row = x_fmt == MOE_X_BF16 ? 2 * (int64_t)K : x_fmt == MOE_X_MXFP8 ? K : K / 2;
+    if (src_of && T * row > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    // tiles are counted in 32 bits
+    if ((cap / 64 + E) * ((N + 63) / 64) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    return status(moe::launch_experts4({x, x_s, x_fmt, src_of, T, k, w_q, w_s, offsets, counts, E, N, K, M_cap, act, y},
+                                       S(stream)));
+}
+
 size_t moe_norm_workspace_bytes(int T, int d) {
     return check_norm(T, d) == MOE_OK ? moe::norm_workspace_bytes(T, d) : 0;
 }

@@ -41,6 +41,22 @@ int launch_quant_mxfp4(const uint16_t* src, int batch, int64_t R, int C, int mod
                        uint8_t* q_col, uint8_t* s_col, hipStream_t s);
 int launch_dequant_mxfp4(const uint8_t* q, const uint8_t* sc, int64_t R, int C, uint16_t* out, hipStream_t s);
 
+// ---- the experts' product with 4-bit weights
+struct Experts4Call {
+    const void* x;
+    const uint8_t* x_s;
+    int fmt;                // of x: 0 bf16, 1 MXFP8, 2 MXFP4
+    const int32_t* src_of;  // nullable
+    int T, k;
+    const uint8_t *w_q, *w_s;
+    const int32_t *offsets, *counts;
+    int E, N, K;
+    int64_t M_cap;
+    int act;
+    uint16_t* y;
+};
+int launch_experts4(const Experts4Call& c, hipStream_t s);
+
 // ---- norms
 constexpr int kNormMaxWidth = 16384;
 

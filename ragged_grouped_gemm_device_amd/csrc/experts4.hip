@@ -1,0 +1,541 @@
+// The experts' product with 4-bit weights (gfx950): y[R_e] = f(X[R_e] W_e), W_e given as MXFP4 rows
+// [N, K] (blocks along K), X as bf16, MXFP8 or MXFP4, sums in fp32.
+//
+// Two kernels. experts4_tile_kernel: tiles of BM rows x 256 columns over LDS slabs, for experts with many
+// rows, bound by the matrix cores. experts4_rows_kernel: weights straight from HBM into the matrix
+// instruction's operands, for few rows (single tokens, decode batches), bound by the read of W.
+//
+// 8- and 4-bit operands go into v_mfma_scale as they are, with their block scales. bf16 rows need bf16
+// weights: a code times its scale is one, exactly, and gfx950 converts two in one instruction; 8
+// conversions feed 8 MFMAs of a wavefront.
+#include <algorithm>
+
+#include "block_common.hpp"
+#include "dense_common.hpp"
+
+namespace moe {
+
+constexpr int kBf16 = 0, kMx8 = 1, kMx4 = 2;  // formats of X
+
+struct Experts4Args {
+    const uint8_t* x;       // rows of K bf16, K bytes or K / 2 bytes
+    const uint8_t* xs;      // block scales [rows, K / 32]; formats 1, 2
+    const int32_t* src_of;  // nullable: rows are those of the experts' buffer
+    int k;
+    int64_t rows;           // rows of x
+    const uint8_t *wq, *ws;
+    const int32_t *offsets, *counts;
+    int E, N, K, act;
+    uint16_t* y;
+};
+
+__device__ __forceinline__ int64_t x_row_bytes(int fmt, int K) { return fmt == kBf16 ? 2 * (int64_t)K : fmt == kMx8 ? K : K / 2; }
+
+// f of one output, or of a gate and its up value
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+    switch (act) {
+        case 0: f(std::integral_constant<int, 0>{}); break;
+        case 1: f(std::integral_constant<int, 1>{}); break;
+        case 2: f(std::integral_constant<int, 2>{}); break;
+        case 3: f(std::integral_constant<int, 3>{}); break;
+        case 4: f(std::integral_constant<int, 4>{}); break;
+        default: f(std::integral_constant<int, 5>{}); break;
+    }
+}
+
+// 8 bf16 weights from 8 codes (a word) and their block's scale
+__device__ __forceinline__ bf16x8_t weights8(uint32_t w, float s) {
+    const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
+    const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
+    return bf16x8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+__device__ __forceinline__ i32x8_t operand4(uint4 v) { return i32x8_t{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0}; }
+__device__ __forceinline__ i32x8_t operand8(uint4 a, uint4 b) {
+    return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+// ------------------------------------------------------------------ few rows
+// A workgroup takes 64 columns of one expert and 16 RT of its rows; its NW wavefronts split K in blocks
+// of 128 and join in LDS. In a 16 x 16 x 128 product lane l supplies row l & 15 of W and of X, W's 16-byte
+// piece l / 16 (one scale block); with bf16 the piece is used in four 16 x 16 x 32 products, whose K then
+// runs in the order (piece, word), X's the same. DEP blocks are in flight a wavefront.
+template <int F, int RT, int NW, int DEP>
+__global__ void __launch_bounds__(NW * 64) experts4_rows_kernel(Experts4Args p) {
+    constexpr int kLd = 68;  // floats a row of the join: 64 and a pad against bank conflicts
+    constexpr int kX = F == kBf16 ? 4 : F == kMx8 ? 2 : 1;  // 16-byte pieces of X a lane, row tile and block
+    __shared__ __align__(16) float s_red[NW][RT * 16][kLd];
+    const int lane = lane_id(), wave = threadIdx.x >> 6;
+    const int r = lane & 15, g = lane >> 4;
+    // the blockIdx.y-th expert that has rows
+    int e = -1, m = 0;
+    for (int base = 0, left = blockIdx.y; base < p.E; base += 64) {
+        const int c = base + lane < p.E ? p.counts[base + lane] : 0;
+        uint64_t some = __ballot(c > 0);
+        const int n = __popcll(some);
+        if (left < n) {
+            while (left--) some &= some - 1;
+            const int at = __ffsll((unsigned long long)some) - 1;
+            e = base + at;
+            m = __shfl(c, at, 64);
+            break;
+        }
+        left -= n;
+    }
+    e = __builtin_amdgcn_readfirstlane(e);
+    m = __builtin_amdgcn_readfirstlane(m);
+    if (e < 0) return;
+    const int n0 = blockIdx.x * 64;
+    const int K = p.K, KB = K / 32;
+    const uint8_t* w[4];
+    const uint8_t* ws[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t n = (int64_t)e * p.N + min(n0 + 16 * j + r, p.N - 1);
+        w[j] = p.wq + n * (K / 2) + 16 * g;
+        ws[j] = p.ws + n * KB + g;
+    }
+    const int64_t xb = x_row_bytes(F, K);
+    for (int first = blockIdx.z * 16 * RT; first < m; first += gridDim.z * 16 * RT) {
+    const int row0 = p.offsets[e] + first, rows = min(m - first, 16 * RT);
+    const uint8_t* x[RT];
+    const uint8_t* xs[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        int64_t row = row0 + min(16 * i + r, rows - 1);
+        if (p.src_of) row = p.src_of[row] / p.k;
+        x[i] = p.x + row * xb + (F == kBf16 ? 64 * g : 16 * g);
+        xs[i] = F == kBf16 ? nullptr : p.xs + row * KB + g;
+    }
+    struct Block {
+        uint4 w[4], x[RT][kX];
+        uint32_t ws[4], xs[RT];
+    };
+    const int nb = (K + 127) / 128;
+    const int b0 = nb * wave / NW, b1 = nb * (wave + 1) / NW;
+    auto load = [&](Block& b, int at) {
+        const bool ok = 128 * at + 32 * g < K;  // the last block may hold fewer than four scale blocks
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            b.w[j] = ok ? *(const uint4*)(w[j] + 64 * (int64_t)at) : zero;
+            b.ws[j] = ok ? ws[j][4 * at] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            if constexpr (F == kBf16) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) b.x[i][q] = ok ? *(const uint4*)(x[i] + 256 * (int64_t)at + 16 * q) : zero;
+            } else if constexpr (F == kMx8) {
+                b.x[i][0] = 128 * at + 16 * g < K ? *(const uint4*)(x[i] + 128 * (int64_t)at) : zero;
+                b.x[i][1] = 128 * at + 64 + 16 * g < K ? *(const uint4*)(x[i] + 128 * (int64_t)at + 64) : zero;
+            } else {
+                b.x[i][0] = ok ? *(const uint4*)(x[i] + 64 * (int64_t)at) : zero;
+            }
+            b.xs[i] = F != kBf16 && ok ? xs[i][4 * at] : 0;
+        }
+    };
+    f32x4_t acc[4][RT];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[j][i] = (f32x4_t){};
+    auto multiply = [&](const Block& b) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (F == kBf16) {
+                const float s = e8m0_value(b.ws[j]);
+                const uint32_t words[4] = {b.w[j].x, b.w[j].y, b.w[j].z, b.w[j].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const bf16x8_t v = weights8(words[q], s);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+                        acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8_t, b.x[i][q]), acc[j][i], 0, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    if constexpr (F == kMx8)
+                        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            operand4(b.w[j]), operand8(b.x[i][0], b.x[i][1]), acc[j][i], 4, 0, 0, (int)b.ws[j], 0, (int)b.xs[i]);
+                    else
+                        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            operand4(b.w[j]), operand4(b.x[i][0]), acc[j][i], 4, 4, 0, (int)b.ws[j], 0, (int)b.xs[i]);
+                }
+            }
+        }
+    };
+    Block blk[DEP];
+#pragma unroll
+    for (int i = 0; i < DEP; ++i)
+        if (b0 + i < b1) load(blk[i], b0 + i);
+    for (int b = b0; b < b1; b += DEP) {
+#pragma unroll
+        for (int i = 0; i < DEP; ++i) {
+            if (b + i < b1) {
+                multiply(blk[i]);
+                if (b + i + DEP < b1) load(blk[i], b + i + DEP);
+            }
+        }
+    }
+    // lane: row l & 15 of X, columns 16 j + 4 (l / 16) + [0, 4)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) *(f32x4_t*)&s_red[wave][16 * i + r][16 * j + 4 * g] = acc[j][i];
+    __syncthreads();
+    with_act(p.act, [&](auto A) {
+        constexpr int ACT = decltype(A)::value;
+        constexpr bool G = ACT < 2;
+        constexpr int Q = G ? 8 : 16;  // quads of outputs a row
+        const int NO = G ? p.N / 2 : p.N;
+        for (int i = threadIdx.x; i < RT * 16 * Q; i += NW * 64) {
+            const int row = i / Q, c = 4 * (i % Q);
+            if (row >= rows || n0 / (G ? 2 : 1) + c >= NO) continue;
+            f32x4_t a = {}, u = {};
+            for (int v = 0; v < NW; ++v) {
+                a += *(const f32x4_t*)&s_red[v][row][c];
+                if constexpr (G) u += *(const f32x4_t*)&s_red[v][row][c + 32];
+            }
+            float o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] = G ? dense_act<ACT>(a[q]) * u[q] : dense_act<ACT>(a[q]);
+            *(uint2*)(p.y + (int64_t)(row0 + row) * NO + n0 / (G ? 2 : 1) + c) =
+                make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+        }
+    });
+    __syncthreads();  // read out before the next rows' sums
+    }
+}
+
+// ------------------------------------------------------------------ tiles
+// What a format's slab holds: KS elements of K, 128 bytes a row of X and WROW a row of W.
+template <int F>
+struct Slab {
+    static constexpr int KS = F == kBf16 ? 64 : F == kMx8 ? 128 : 256;
+    static constexpr int WROW = KS / 2;
+    static constexpr int WCH = WROW / 16;        // 16-byte pieces a row of W: 2, 4, 8
+    static constexpr int SPG = 512 / KS;         // slabs that a row's 16 scale bytes serve
+};
+
+// byte offset of 16-byte piece c of row r, rows of CH pieces: pieces are XOR-swizzled so that the rows of
+// one 256-byte bank window and the next differ (128-byte rows: as the grouped GEMMs' slabs)
+template <int CH>
+__device__ __forceinline__ int slab_swz(int r) {
+    return CH == 8 ? (r >> 1) & 7 : CH == 4 ? (r >> 2) & 3 : (r >> 3) & 1;
+}
+template <int CH>
+__device__ __forceinline__ int slab_byte(int r, int c) {
+    return r * CH * 16 + ((c ^ slab_swz<CH>(r)) << 4);
+}
+
+template <int F, int BMX, bool GLU>
+__global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
+    using SL = Slab<F>;
+    constexpr int TM = BMX / 64;        // 32-row tiles a wavefront (2 x 4 wavefronts)
+    constexpr int XB = BMX * 128, WB = 256 * SL::WROW;
+    constexpr int XL = XB / 8192, WL = WB / 8192;  // copies of 16 bytes a thread
+    // a slab, or the epilogue's 4 KiB of each of the 8 wavefronts
+    __shared__ __attribute__((aligned(1024))) uint8_t s_ab[2][XB + WB > 32768 ? XB + WB : 32768];
+    __shared__ __attribute__((aligned(1024))) uint8_t s_sc[2][(BMX + 256) * 16];
+    __shared__ int s_tiles[MOE_MAX_E + 1];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 2, wn = wave & 3, h = lane >> 5, lr = lane & 31;
+    const int K = p.K, KB = K / 32, ntn = (p.N + 255) / 256;
+    const int64_t xb = x_row_bytes(F, K);
+    const int wb = K / 2;
+    // first M tile of every expert
+    for (int i = tid; i < p.E; i += 512) s_tiles[i + 1] = (p.counts[i] + BMX - 1) / BMX;
+    if (tid == 0) s_tiles[0] = 0;
+    __syncthreads();
+    if (tid < 64) {
+        int carry = 0;
+        for (int base = 0; base < p.E; base += 64) {
+            int v = base + lane < p.E ? s_tiles[base + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int u = __shfl_up(v, o, 64);
+                if (lane >= o) v += u;
+            }
+            if (base + lane < p.E) s_tiles[base + lane + 1] = v + carry;
+            carry += __shfl(v, 63, 64);
+        }
+    }
+    __syncthreads();
+    const int mtiles = s_tiles[p.E], total = mtiles * ntn;
+    const int nbl = gridDim.x;  // a multiple of 8
+    auto logical = [&](int round) { return round * nbl + (blockIdx.x & 7) * (nbl >> 3) + (blockIdx.x >> 3); };
+    struct Tile {
+        int e, row0, rows, n0;
+    };
+    auto get_tile = [&](int tt) -> Tile {
+        constexpr int G = 8;  // bands of 8 M tiles: an XCD's neighbouring tiles share operand panels in its L2
+        const int band = tt / (G * ntn), within = tt - band * G * ntn, bm = min(G, mtiles - band * G);
+        const int mt = band * G + within % bm;
+        int lo = 0, hi = p.E;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_tiles[mid] <= mt) lo = mid; else hi = mid;
+        }
+        Tile t;
+        t.e = __builtin_amdgcn_readfirstlane(lo);
+        const int skip = __builtin_amdgcn_readfirstlane((mt - s_tiles[lo]) * BMX);
+        t.row0 = __builtin_amdgcn_readfirstlane(p.offsets[lo]) + skip;
+        t.rows = min(__builtin_amdgcn_readfirstlane(p.counts[lo]) - skip, BMX);
+        t.n0 = __builtin_amdgcn_readfirstlane(within / bm * 256);
+        return t;
+    };
+    // What a thread copies of a tile: its rows of X (offsets from the tile's or, gathered, x's base; rows past
+    // the expert's last are its last again, and not stored) and of W, and one row's scales.
+    const int xc = (tid & 7) ^ slab_swz<8>(tid >> 3);  // the piece of a 128-byte row, the same in every copy
+    const int wc = (tid & (SL::WCH - 1)) ^ slab_swz<SL::WCH>(tid / SL::WCH);
+    struct Src {
+        i32x4_t rx, rw;
+        uint32_t xo[XL], wo[WL];
+        const uint8_t* sc;  // this thread's row of scales
+    };
+    auto source_row = [&](const Tile& t, int r) -> int64_t {
+        const int row = t.row0 + min(r, t.rows - 1);
+        return p.src_of ? p.src_of[row] / p.k : row;
+    };
+    auto make_src = [&](const Tile& t) -> Src {
+        Src s;
+        const int64_t base = p.src_of ? 0 : t.row0;
+        s.rx = rsrc_from(p.x, p.rows * xb, base * xb);
+        const int64_t n0 = (int64_t)t.e * p.N + t.n0;
+        s.rw = rsrc_words(p.wq + n0 * wb, clamp_records((int64_t)min(p.N - t.n0, 256) * wb));
+#pragma unroll
+        for (int i = 0; i < XL; ++i) s.xo[i] = (uint32_t)((source_row(t, (tid >> 3) + 64 * i) - base) * xb) + xc * 16;
+#pragma unroll
+        for (int i = 0; i < WL; ++i)
+            s.wo[i] = (uint32_t)(min(tid / SL::WCH + i * (512 / SL::WCH), p.N - t.n0 - 1) * wb) + wc * 16;
+        // threads [0, 256) the rows of W, [256, 256 + BMX) those of X
+        if (tid < 256) s.sc = p.ws + (n0 + min(tid, p.N - t.n0 - 1)) * KB;
+        else if (F != kBf16 && tid < 256 + BMX) s.sc = p.xs + source_row(t, tid - 256) * KB;
+        else s.sc = nullptr;
+        return s;
+    };
+    auto issue = [&](const Src& s, int kt, int buf) {
+        const uint32_t l0 = (uint32_t)(uintptr_t)(LDS_AS char*)(&s_ab[buf][0]) + wave * 1024;
+        const uint32_t xk = (uint32_t)kt * 128, wk = (uint32_t)kt * SL::WROW;
+        const bool xin = (int64_t)xk + xc * 16 < xb, win = (int)wk + wc * 16 < wb;  // past K: zeros
+#pragma unroll
+        for (int i = 0; i < XL; ++i) lds_copy16(s.rx, l0 + i * 8192, xin ? s.xo[i] + xk : kMasked);
+#pragma unroll
+        for (int i = 0; i < WL; ++i) lds_copy16(s.rw, l0 + XB + i * 8192, win ? s.wo[i] + wk : kMasked);
+    };
+    // 16 scale bytes of this thread's row (512 of K): zeros past its end
+    auto load_scales = [&](const Src& s, int grp) -> uint4 {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (s.sc) {
+            const int at = grp * 16, n = min(16, KB - at);
+            if (n == 16) {
+                __builtin_memcpy(&v, s.sc + at, 16);
+            } else {
+                uint32_t b[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i < n) b[i >> 2] |= (uint32_t)s.sc[at + i] << (8 * (i & 3));
+                v = make_uint4(b[0], b[1], b[2], b[3]);
+            }
+        }
+        return v;
+    };
+    auto store_scales = [&](uint4 v, int sbuf) {
+        if (tid < 256 + (F == kBf16 ? 0 : BMX)) *(uint4*)(s_sc[sbuf] + tid * 16) = v;
+    };
+    int round = 0;
+    int t = logical(0);
+    if (t >= total) return;
+    Tile tl = get_tile(t);
+    Src src = make_src(tl);
+    const int nk = (K + SL::KS - 1) / SL::KS, ng = (nk + SL::SPG - 1) / SL::SPG;
+    issue(src, 0, 0);
+    uint4 held = load_scales(src, 0);
+    store_scales(held, 0);
+    int buf0 = 0, sg0 = 0;
+    f32x16_t acc[TM][2];
+    for (;;) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[i][j] = (f32x16_t){};
+        const int tn = logical(round + 1);
+        const bool have_next = tn < total;
+        Tile tl_next = tl;
+        Src src_next = src;
+        if (have_next) {
+            tl_next = get_tile(tn);
+            src_next = make_src(tl_next);
+        }
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        for (int kt = 0; kt < nk; ++kt) {
+            const int cur = (buf0 + kt) & 1, grp = kt / SL::SPG, sub = kt % SL::SPG;
+            const bool last = kt + 1 == nk;
+            if (!last) issue(src, kt + 1, cur ^ 1);
+            else if (have_next) issue(src_next, 0, cur ^ 1);
+            // the next group of scales, or the next tile's first, on the way through registers
+            const bool fetch = last ? have_next : sub == SL::SPG - 1;
+            if (fetch) held = last ? load_scales(src_next, 0) : load_scales(src, grp + 1);
+            const uint8_t* sX = s_ab[cur];
+            const uint8_t* sW = s_ab[cur] + XB;
+            const uint8_t* sc = s_sc[(sg0 + grp) & 1] + sub * (SL::KS / 32);
+            const int wrow = wn * 64 + lr, xrow = wm * (BMX / 2) + lr;
+            if constexpr (F == kBf16) {
+                // W's piece h of a row (K 32 h ..) is one scale block: step q takes its word q, X's piece 4 h + q
+                uint4 fw[2];
+                float fs[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    fw[j] = *(const uint4*)(sW + slab_byte<2>(wrow + 32 * j, h));
+                    fs[j] = e8m0_value(sc[(wrow + 32 * j) * 16 + h]);
+                }
+                static_for<4>([&](auto Q) {
+                    bf16x8_t fx[TM];
+#pragma unroll
+                    for (int i = 0; i < TM; ++i) fx[i] = *(const bf16x8_t*)(sX + slab_byte<8>(xrow + 32 * i, 4 * h + Q));
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t word = Q == 0 ? fw[j].x : Q == 1 ? fw[j].y : Q == 2 ? fw[j].z : fw[j].w;
+                        const bf16x8_t v = weights8(word, fs[j]);
+#pragma unroll
+                        for (int i = 0; i < TM; ++i)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, fx[i], acc[i][j], 0, 0, 0);
+                    }
+                });
+            } else {
+                constexpr int NS = SL::KS / 64;  // steps of 64
+                // scale words of 128 of K, shifted by the lane half's block: byte 0 serves the word's first
+                // step, byte 2 its second
+                uint32_t ss[2][NS / 2], sx[TM][NS / 2];
+#pragma unroll
+                for (int u = 0; u < NS / 2; ++u) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) ss[j][u] = *(const uint32_t*)(sc + (wrow + 32 * j) * 16 + 4 * u) >> (8 * h);
+#pragma unroll
+                    for (int i = 0; i < TM; ++i) sx[i][u] = *(const uint32_t*)(sc + (256 + xrow + 32 * i) * 16 + 4 * u) >> (8 * h);
+                }
+                auto frag_w = [&](int j, int s) { return operand4(*(const uint4*)(sW + slab_byte<SL::WCH>(wrow + 32 * j, 2 * s + h))); };
+                auto frag_x = [&](int i, int s) {
+                    if constexpr (F == kMx4) return operand4(*(const uint4*)(sX + slab_byte<8>(xrow + 32 * i, 2 * s + h)));
+                    else return operand8(*(const uint4*)(sX + slab_byte<8>(xrow + 32 * i, 4 * s + h)),
+                                         *(const uint4*)(sX + slab_byte<8>(xrow + 32 * i, 4 * s + 2 + h)));
+                };
+                i32x8_t fw[2], fx[TM];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) fw[j] = frag_w(j, 0);
+#pragma unroll
+                for (int i = 0; i < TM; ++i) fx[i] = frag_x(i, 0);
+                static_for<NS>([&](auto S) {
+                    constexpr bool more = S + 1 < NS;
+                    static_for<2>([&](auto J) {
+                        static_for<TM>([&](auto I) {
+                            acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                fw[J], fx[I], acc[I][J], 4, F == kMx4 ? 4 : 0, 2 * (S & 1), (int)ss[J][S / 2], 2 * (S & 1),
+                                (int)sx[I][S / 2]);
+                            if constexpr (more && J == 1) fx[I] = frag_x(I, S + 1);
+                        });
+                        if constexpr (more) fw[J] = frag_w(J, S + 1);
+                    });
+                });
+            }
+            // pinned before the wait below (the compiler would sink them past it)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(acc[i][j]));
+            if (!last) {
+                __builtin_amdgcn_s_waitcnt(0);
+                if (fetch) store_scales(held, (sg0 + grp + 1) & 1);
+                __syncthreads();
+            }
+        }
+        // Epilogue: lane = row, columns 8 q + 4 h + s of each 32-wide tile; 32 rows at a time through this
+        // wavefront's 4 KiB of the slab no longer read, so that stores cover whole rows.
+        const int next_buf0 = (buf0 + nk) & 1;
+        __syncthreads();  // the last slab is read out
+        uint8_t* stg = &s_ab[next_buf0 ^ 1][0] + wave * 4096;
+        with_act(p.act, [&](auto A) {
+            constexpr int ACT = decltype(A)::value;
+            if constexpr ((ACT < 2) == GLU) {
+                const int NO = GLU ? p.N / 2 : p.N;
+                constexpr int PC = GLU ? 4 : 8;  // 16-byte pieces a row
+                const int col0 = (tl.n0 + wn * 64) / (GLU ? 2 : 1);
+                static_for<TM>([&](auto I) {
+                    static_for<GLU ? 1 : 2>([&](auto J) {
+                        static_for<4>([&](auto Q) {
+                            float o[4];
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) {
+                                o[s] = dense_act<ACT>(acc[I][J][4 * Q + s]);
+                                if constexpr (GLU) o[s] *= acc[I][1][4 * Q + s];
+                            }
+                            *(uint2*)(stg + slab_byte<PC>(lr, 4 * J + Q) + 8 * h) =
+                                make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+                        });
+                    });
+                    wave_lds_sync();
+                    static_for<PC / 2>([&](auto It) {
+                        const int R = It * (64 / PC) + lane / PC, c = lane % PC;
+                        const uint4 v = *(const uint4*)(stg + slab_byte<PC>(R, c));
+                        const int m = wm * (BMX / 2) + 32 * I + R, col = col0 + 8 * c;
+                        if (m < tl.rows && col < NO) st_nt16(p.y + (int64_t)(tl.row0 + m) * NO + col, v);
+                    });
+                    wave_lds_sync();
+                });
+            }
+        });
+        if (!have_next) break;
+        store_scales(held, (sg0 + ng) & 1);
+        ++round;
+        buf0 = next_buf0;
+        sg0 = (sg0 + ng) & 1;
+        tl = tl_next;
+        src = src_next;
+    }
+}
+
+// ------------------------------------------------------------------ launch
+template <int F>
+static void experts4_any(const Experts4Args& a, int T, int k, hipStream_t s) {
+    const int64_t pairs = (int64_t)T * k;
+    const int active = (int)std::min<int64_t>(a.E, pairs);
+    const double mean = (double)pairs / active;  // rows an expert
+    if (mean <= 48) {
+        auto go = [&](auto R, auto W) {
+            constexpr int RT = decltype(R)::value, NW = decltype(W)::value;
+            const dim3 grid((a.N + 63) / 64, active, (unsigned)((std::min(T, (int)(2 * mean + 1)) + 16 * RT - 1) / (16 * RT)));
+            experts4_rows_kernel<F, RT, NW, RT == 1 ? 3 : 2><<<grid, NW * 64, 0, s>>>(a);
+        };
+        if (mean <= 8 || T <= 16) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
+        else go(std::integral_constant<int, 2>{}, std::integral_constant<int, 8>{});
+        return;
+    }
+    auto go = [&](auto B) {
+        constexpr int BMX = decltype(B)::value;
+        const int64_t bound = (pairs / BMX + active) * ((a.N + 255) / 256);
+        const int grid = persistent_grid(bound);
+        if (a.act < 2) experts4_tile_kernel<F, BMX, true><<<grid, 512, 0, s>>>(a);
+        else experts4_tile_kernel<F, BMX, false><<<grid, 512, 0, s>>>(a);
+    };
+    if (mean <= 96) go(std::integral_constant<int, 64>{});
+    else if (mean <= 192) go(std::integral_constant<int, 128>{});
+    else go(std::integral_constant<int, 256>{});
+}
+
+int launch_experts4(const Experts4Call& c, hipStream_t s) {
+    Experts4Args a{};
+    a.x = (const uint8_t*)c.x, a.xs = c.x_s, a.src_of = c.src_of, a.k = c.k, a.rows = c.src_of ? c.T : c.M_cap;
+    a.wq = c.w_q, a.ws = c.w_s, a.offsets = c.offsets, a.counts = c.counts;
+    a.E = c.E, a.N = c.N, a.K = c.K, a.act = c.act, a.y = c.y;
+    if (c.fmt == kBf16) experts4_any<kBf16>(a, c.T, c.k, s);
+    else if (c.fmt == kMx8) experts4_any<kMx8>(a, c.T, c.k, s);
+    else experts4_any<kMx4>(a, c.T, c.k, s);
+    return hipGetLastError() == hipSuccess ? 0 : -4;
+}
+
+}  // namespace moe

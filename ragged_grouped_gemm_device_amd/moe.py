@@ -50,6 +50,9 @@ MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
 MOE_MAX_TOPK = 64
 MOE_MAX_GROUPS = 64
+MOE_X_BF16 = 0
+MOE_X_MXFP8 = 1
+MOE_X_MXFP4 = 2
 MOE_MAX_NORM_WIDTH = 16384
 MOE_GATE_LINEAR = 0
 MOE_GATE_SIGMOID = 1
@@ -89,6 +92,8 @@ SIGNATURES = {
     "moe_route_scores_bwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P]),
     "moe_quant_mxfp4": (_I, [_P, _I, _I64, _I, _I, _P, _P, _P, _P, _P]),
     "moe_dequant_mxfp4": (_I, [_P, _P, _I64, _I, _P, _P]),
+    "moe_grouped_linear_mxfp4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_grouped_linear_mxfp4": (_I, [_P, _P, _I, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I64, _I, _P, _P, _SZ, _P]),
     "moe_norm_workspace_bytes": (_SZ, [_I, _I]),
     "moe_norm_fwd": (_I, [_P, _P, _P, _I, _I, C.c_float, _P, _P, _P, _P]),
     "moe_norm_bwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _SZ, _P]),
@@ -574,6 +579,36 @@ def moe_dequant_mxfp4(q, s, out):
     _operand(s, (R, Cc // MOE_MX_BLOCK), _U8, "s", dev)
     _operand(out, (R, Cc), _BF, "out", dev)
     _check("moe_dequant_mxfp4", _lib().moe_dequant_mxfp4(_ptr(q), _ptr(s), R, Cc, _ptr(out), _stream(dev)))
+
+
+def moe_grouped_linear_mxfp4_workspace_bytes(T: int, k: int, E: int, K: int, N: int) -> int:
+    return int(_lib().moe_grouped_linear_mxfp4_workspace_bytes(T, k, E, K, N))
+
+
+def moe_grouped_linear_mxfp4(x, w_q, w_s, offsets, counts, y, T, k, act=MOE_ACT_NONE, x_s=None, src_of=None,
+                             workspace=None):
+    """y = f(x W_e) for every expert's rows, W_e as MXFP4 [E, N, K / 2] with scales [E, N, K / 32]. x: the
+    experts' rows [M_cap, ..], or with src_of the tokens [T, ..]; bf16, or codes with their scales x_s
+    (MXFP8 [.., K], MXFP4 [.., K / 2]). y [M_cap, N], or [M_cap, N / 2] for a gated activation; rows past an
+    expert's count are left as they are."""
+    dev = _device(x)
+    E, N, K = w_q.shape[0], w_q.shape[1], 2 * w_q.shape[2]
+    _sizes(T, E, K, N, k)
+    M_cap = y.shape[0]
+    rows = M_cap if src_of is None else T
+    fmt = MOE_X_BF16 if x_s is None else MOE_X_MXFP8 if x.shape[-1] == K else MOE_X_MXFP4
+    _operand(x, (rows, K // 2 if fmt == MOE_X_MXFP4 else K), _BF if fmt == MOE_X_BF16 else _U8, "x", dev)
+    _operand(x_s, (rows, K // MOE_MX_BLOCK), _U8, "x_s", dev)
+    _operand(w_q, (E, N, K // 2), _U8, "w_q", dev)
+    _operand(w_s, (E, N, K // MOE_MX_BLOCK), _U8, "w_s", dev)
+    _operand(offsets, (E + 1,), _I32, "offsets", dev)
+    _operand(counts, (E,), _I32, "counts", dev)
+    _operand(src_of, (M_cap,), _I32, "src_of", dev)
+    _operand(y, (M_cap, N // 2 if act in _GATED else N), _BF, "y", dev)
+    ws, nws = _space(workspace, dev)
+    _check("moe_grouped_linear_mxfp4", _lib().moe_grouped_linear_mxfp4(
+        _ptr(x), _ptr(x_s), fmt, _ptr(src_of), T, k, _ptr(w_q), _ptr(w_s), _ptr(offsets), _ptr(counts), E, K, N, M_cap,
+        act, _ptr(y), ws, nws, _stream(dev)))
 
 
 def moe_norm_workspace_bytes(T: int, d: int) -> int:
