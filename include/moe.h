@@ -626,7 +626,8 @@ int moe_quant_mxfp4(const uint16_t* src, int batch, int64_t R, int C, int mode, 
                     uint8_t* q_col, uint8_t* s_col, moe_stream_t stream);
 
 /* moe_dequant_mxfp4 -- bf16 values [R, C] of row-wise codes q [R, C / 2] and scales
- *   s [R, C / 32]; exact wherever code * scale is a bf16 number. Requires C % 32 == 0. */
+ *   s [R, C / 32]; exact wherever code * scale is a bf16 number (all but a magnitude of 2^128, to
+ *   which bf16's very largest round: an infinity). Requires C % 32 == 0. */
 int moe_dequant_mxfp4(const uint8_t* q, const uint8_t* s, int64_t R, int C, uint16_t* out, moe_stream_t stream);
 
 /* forms of the rows that the 4-bit product reads */

@@ -59,6 +59,25 @@ struct RouteLds {
 
 __device__ __forceinline__ float logistic(float x) { return 1.f / (1.f + __expf(-x)); }
 
+// exp(a - b) with the rounding of the difference made good: it would be an error of up to 2^-24 |a - b| of
+// the result.
+__device__ __forceinline__ float exp_of_difference(float a, float b) {
+    const float d = a - b, bb = d - a;
+    const float e = (a - (d - bb)) - (b + bb);
+    return expf(d) * (1.f + e);
+}
+
+// A chosen expert's score from its logit. Renormalised weights take it over exp(shift), shift the best chosen
+// logit (the sigmoid's: where that is negative), so that they keep their precision where all scores underflow.
+struct SlotScore {
+    bool sigmoid, renorm;
+    float shift, mx, inv;  // mx, inv: a softmax's maximum and 1 / sum over all experts
+    __device__ __forceinline__ float operator()(float v) const {
+        if (renorm) return sigmoid ? exp_of_difference(fminf(v, 0.f), shift) / (1.f + expf(-fabsf(v))) : exp_of_difference(v, shift);
+        return sigmoid ? 1.f / (1.f + expf(-v)) : exp_of_difference(v, mx) * inv;
+    }
+};
+
 // Are the scores of two experts with equal fp32 values certainly equal, or only near?
 __device__ __forceinline__ bool same_inputs(const RouteArgs& p, const float* row, int a, int b) {
     return row[a] == row[b] && (!p.bias || p.bias[a] == p.bias[b]);
@@ -312,21 +331,15 @@ __global__ void __launch_bounds__(kScoresThreads) route_scores_kernel(RouteArgs 
             todo &= L == 64 ? 0ull : ~(((1ull << (L & 63)) - 1) << (w * L));
         }
         wave_lds_sync();
-        // weights, slot by slot; shifted by the best chosen score's exponent, so that renormalised ones
-        // keep their precision where all scores underflow
+        // weights, slot by slot
         float xs = -INFINITY;
         for (int j = gl; j < k; j += L) {
             const int e = lds.sel[tw][j];
             if (live && available(p, row, e)) xs = fmaxf(xs, row[e]);
         }
         xs = lanes_max<L>(xs);
-        const float shift = p.sigmoid ? fminf(xs, 0.f) : xs;
-        auto weight = [&](int e) -> float {
-            if (!available(p, row, e)) return 0.f;
-            const float v = row[e];
-            if (!p.renorm) return score(v);
-            return p.sigmoid ? __expf(fminf(v, 0.f) - shift) / (1.f + __expf(-fabsf(v))) : __expf(v - shift);
-        };
+        const SlotScore slot{p.sigmoid != 0, p.renorm != 0, p.sigmoid ? fminf(xs, 0.f) : xs, mx, inv};
+        auto weight = [&](int e) { return available(p, row, e) ? slot(row[e]) : 0.f; };
         float total = 0.f;
         if (p.renorm) {
             for (int j = gl; j < k; j += L) total += live ? weight(lds.sel[tw][j]) : 0.f;
@@ -414,32 +427,29 @@ __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs p) {
         if ((uint32_t)e >= (uint32_t)E) return -1;
         return isfinite(row[e]) && (!p.bias || isfinite(p.bias[e])) ? e : -1;
     };
-    float shift = 0.f;
+    float xs = -INFINITY;
     if (p.renorm) {
-        float xs = -INFINITY;
         for (int j = gl; j < k; j += L) {
             const int e = slot(j);
             if (e >= 0) xs = fmaxf(xs, row[e]);
         }
         xs = lanes_max<L>(xs);
-        shift = p.sigmoid ? fminf(xs, 0.f) : xs;
     }
-    auto weight = [&](float v) -> float {
-        if (p.renorm) return p.sigmoid ? __expf(fminf(v, 0.f) - shift) / (1.f + __expf(-fabsf(v))) : __expf(v - shift);
-        return p.sigmoid ? logistic(v) : __expf(v - mx) * inv;
-    };
-    float total = 0.f, dot = 0.f;
-    for (int j = gl; j < k; j += L) {
-        const int e = slot(j);
-        if (e >= 0) {
-            const float w = weight(row[e]);
-            total += w;
-            dot = fmaf(w, p.ds[t * k + j], dot);
+    const SlotScore weight{p.sigmoid != 0, p.renorm != 0, p.sigmoid ? fminf(xs, 0.f) : xs, mx, inv};
+    float total = 1.f, dot = 0.f;
+    if (p.renorm) {
+        total = 0.f;
+        for (int j = gl; j < k; j += L) {
+            const int e = slot(j);
+            if (e >= 0) total += weight(row[e]);
         }
+        total = lanes_sum<L>(total);
     }
-    total = lanes_sum<L>(total);
+    for (int j = gl; j < k; j += L) {
+        const int e = slot(j);  // divided, not times a reciprocal: a lone weight is 1 and has no gradient
+        if (e >= 0) dot = fmaf(weight(row[e]) / total, p.ds[t * k + j], dot);
+    }
     dot = lanes_sum<L>(dot);
-    const float rt = p.renorm ? (total > 0.f ? 1.f / total : 0.f) : 1.f;
     wave_lds_sync();
     for (int j = gl; j < k; j += L) {
         const int e = slot(j);
@@ -448,8 +458,8 @@ __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs p) {
         if (dense) {
             g[e] = d;
         } else {
-            const float w = weight(v) * rt;
-            g[e] = p.scale * w * (p.sigmoid ? logistic(-v) : 1.f) * (p.renorm ? d - dot * rt : d);
+            const float w = weight(v) / total;
+            g[e] = p.scale * w * (p.sigmoid ? 1.f / (1.f + expf(v)) : 1.f) * (p.renorm ? d - dot : d);
         }
     }
     wave_lds_sync();

@@ -723,7 +723,8 @@ class Buffers:
         self.row_of = torch.empty(T * k, dtype=i32, device=dev)
         self.src_of = torch.empty(M, dtype=i32, device=dev)
         self.err = torch.zeros(1, dtype=i32, device=dev)
-        self.route_ws = torch.empty(max(16, moe_route_workspace_bytes(T, k, E)), dtype=u8, device=dev)
+        self.route_ws = torch.empty(max(16, moe_route_workspace_bytes(T, k, E), moe_route_scores_workspace_bytes(T, k, E)),
+                                    dtype=u8, device=dev)
         self.x_perm = torch.empty(M, d, dtype=bf, device=dev)
         n1 = 2 * n if gated else n   # FC1 width (non-gated sReLU: n)
         if h is not None and not (h.shape == (M, n1) and h.dtype is bf and h.is_contiguous()
@@ -786,6 +787,7 @@ class Buffers:
             self.dxt_q = torch.empty(d, M, dtype=u8, device=dev)
             self.dxt_s = torch.empty(d, M // 32, dtype=u8, device=dev)
         self.xt_from_forward = False
+        self.served = False   # the last forward kept nothing for a backward pass
 
     def quantize_weights(self, w1, w2):
         """MXFP8 weight copies: W1_e along 2n [E, d, 2n] (FC1 dgrad) and along d, transposed
@@ -920,23 +922,110 @@ class Router:
             self.dwg.copy_(dwg[:, :E])
 
 
+class Experts4:
+    """The routed experts' weights as MXFP4, for serving: w1 [E, d, 2n] (gated; n wide otherwise) and w2
+    [E, n, d] in 17 instead of 64 bytes for 32 values. x_form: how the products take their rows, as bf16, or
+    quantized to MXFP8 or MXFP4 on the way (the tokens once, before they are gathered)."""
+
+    def __init__(self, T: int, k: int, E: int, d: int, n: int, act: int = MOE_ACT_SWIGLU, x_form: int = MOE_X_BF16,
+                 device="cuda"):
+        self.T, self.k, self.act, self.x_form = T, k, act, x_form
+        n1 = 2 * n if act in _GATED else n
+        new = lambda *shape: torch.empty(*shape, dtype=_U8, device=device)  # noqa: E731
+        self.w1_q, self.w1_s = new(E, n1, d // 2), new(E, n1, d // MOE_MX_BLOCK)
+        self.w2_q, self.w2_s = new(E, d, n // 2), new(E, d, n // MOE_MX_BLOCK)
+        M = moe_capacity_rows(T, k, E)
+        self.x_q = self.x_s = self.a_q = self.a_s = None
+        if x_form != MOE_X_BF16:
+            per = 1 if x_form == MOE_X_MXFP8 else 2
+            self.x_q, self.x_s = new(T, d // per), new(T, d // MOE_MX_BLOCK)
+            self.a_q, self.a_s = new(M, n // per), new(M, n // MOE_MX_BLOCK)
+        self.ws = new(max(16, moe_grouped_linear_mxfp4_workspace_bytes(T, k, E, d, n1),
+                          moe_grouped_linear_mxfp4_workspace_bytes(T, k, E, n, d)))
+
+    def load(self, w1, w2):
+        """Quantizes bf16 weights, once."""
+        moe_quant_mxfp4(w1, MOE_QUANT_COLWISE, q_col=self.w1_q, s_col=self.w1_s)
+        moe_quant_mxfp4(w2, MOE_QUANT_COLWISE, q_col=self.w2_q, s_col=self.w2_s)
+
+    def _rows(self, x, q, s):
+        if self.x_form == MOE_X_BF16:
+            return x, None
+        (moe_quant_mxfp8 if self.x_form == MOE_X_MXFP8 else moe_quant_mxfp4)(x, MOE_QUANT_ROWWISE, q, s)
+        return q, s
+
+    def forward(self, x, offsets, counts, src_of, a, y):
+        """a = f(x w1), y = a w2 over the rows that the routing made."""
+        q, s = self._rows(x, self.x_q, self.x_s)
+        moe_grouped_linear_mxfp4(q, self.w1_q, self.w1_s, offsets, counts, a, self.T, self.k, act=self.act, x_s=s,
+                                 src_of=src_of, workspace=self.ws)
+        q, s = self._rows(a, self.a_q, self.a_s)
+        moe_grouped_linear_mxfp4(q, self.w2_q, self.w2_s, offsets, counts, y, self.T, self.k, x_s=s, workspace=self.ws)
+
+
+class BlockNorms:
+    """The norms of the residual block around the layer: out = x + scale f(gate) (norm(layer(norm(x) w_pre)) w_post).
+    After a forward: out, and y, the layer's input; after a backward: dx, dw_pre, dw_post, and dgate (bf16 [T, d],
+    or fp32 [T, 1] for one gate a token). gate_cols: 0 (no gate), 1 or d."""
+
+    def __init__(self, T: int, d: int, gate_cols: int = 0, gate_act: int = MOE_GATE_LINEAR, scale: float = 1.0,
+                 eps: float = 1e-6, device="cuda"):
+        new = lambda *shape, t=_BF: torch.empty(*shape, dtype=t, device=device)  # noqa: E731
+        self.gate_act, self.scale, self.eps = gate_act, scale, eps
+        self.y, self.out, self.dy, self.dx = new(T, d), new(T, d), new(T, d), new(T, d)
+        self.rstd_pre, self.rstd_post = new(T, t=_F32), new(T, t=_F32)
+        self.dw_pre, self.dw_post = new(d, t=_F32), new(d, t=_F32)
+        self.dgate = new(T, gate_cols, t=_F32 if gate_cols == 1 else _BF) if gate_cols else None
+        self.ws = new(max(16, moe_norm_workspace_bytes(T, d)), t=_U8)
+
+    def before(self, x, w):
+        moe_norm_fwd(x, w, self.y, self.rstd_pre, self.eps)
+        return self.y
+
+    def after(self, x, w, gate, y, **rows):
+        moe_post_norm_fwd(y, x, w, self.out, self.rstd_post, self.eps, gate=gate, gate_act=self.gate_act,
+                          scale=self.scale, **rows)
+
+    def back_after(self, dout, w, gate, y):
+        moe_post_norm_bwd(dout, y, w, self.rstd_post, self.dy, self.dw_post, self.ws, gate=gate, dgate=self.dgate,
+                          gate_act=self.gate_act, scale=self.scale)
+        return self.dy
+
+    def back_before(self, dy, dout, x, w):
+        moe_norm_bwd(dy, x, w, self.rstd_pre, self.dx, self.dw_pre, self.ws, dres=dout)
+
+
 def forward(buf: Buffers, x, logits, w1, w2, renorm=False, fwd_stages=MOE_STAGES_FWD, store_h=True,
-            act=MOE_ACT_SWIGLU, gather=False, mx=False, router=None, shared=None):
+            act=MOE_ACT_SWIGLU, gather=False, mx=False, router=None, shared=None, routing=None, experts4=None,
+            norms=None):
     """route -> permute -> FC1+GLU -> FC2 -> combine (all enqueued, no sync). With gather, FC1
     reads the rows of x through src_of and no permuted copy is made. With mx (buffers made with
     mx=True, quantize_weights done), X_perm is quantized row-wise (FC1 operand) and column-wise
     (FC1 wgrad operand) in one pass and both GEMMs run on MXFP8. With buffers made with ckpt8, H
     is kept as an 8-bit checkpoint. router = (Router, wg): the logits are x wg (logits is None),
     and the router losses follow the routing. shared = (SharedExpert, w1, w2): the shared expert's
-    output is added to out."""
+    output is added to out. routing = a Routing: its scores, bias, groups and weights (renorm is then its
+    own). experts4 = an Experts4 (serving): its 4-bit weights and activation in place of w1, w2 and act; nothing is
+    kept for a backward pass. norms = (BlockNorms, w_pre, w_post, gate or None): x is the residual
+    stream, the layer runs on its norm, buf.out holds the layer's output and the BlockNorms' out the block's."""
+    x_in = x
+    if norms is not None:
+        x = norms[0].before(x_in, norms[1])
     if router is not None:
         logits = router[0].project(x, router[1])
-    moe_route_counts(logits, buf.k, buf.topk_idx, buf.topk_w, buf.counts, buf.offsets, buf.row_of,
-                     buf.src_of, buf.M_cap, buf.err, buf.route_ws, renorm)
+    if routing is not None:
+        moe_route_scores(logits, buf.k, buf.topk_idx, buf.topk_w, buf.counts, buf.offsets, buf.row_of, buf.src_of,
+                         buf.err, buf.route_ws, routing)
+    else:
+        moe_route_counts(logits, buf.k, buf.topk_idx, buf.topk_w, buf.counts, buf.offsets, buf.row_of,
+                         buf.src_of, buf.M_cap, buf.err, buf.route_ws, renorm)
     if router is not None:
         router[0].losses(buf.topk_idx)
     buf.xt_from_forward = bool(mx)
-    if mx:
+    buf.served = experts4 is not None
+    if experts4 is not None:
+        experts4.forward(x, buf.offsets, buf.counts, buf.src_of, buf.a, buf.y)
+    elif mx:
         if gather:
             raise ValueError("the MXFP8 FC1 reads the quantized permuted copy: no row gather")
         # X_perm only as its MXFP8 copies: row-wise (FC1) and column-wise (FC1 wgrad)
@@ -951,16 +1040,21 @@ def forward(buf: Buffers, x, logits, w1, w2, renorm=False, fwd_stages=MOE_STAGES
         moe_permute(x, buf.row_of, buf.src_of, buf.offsets, buf.k, buf.E, buf.x_perm)
         moe_grouped_mlp_fwd(buf.x_perm, w1, w2, buf.offsets, buf.h if store_h else None, buf.a,
                             buf.y, fwd_stages, act=act)
-    if buf.ckpt8 and store_h and (fwd_stages & MOE_STAGE_FC1):
+    if buf.ckpt8 and store_h and (fwd_stages & MOE_STAGE_FC1) and experts4 is None:
         moe_quant_mxfp8(buf.h, MOE_QUANT_ROWWISE, buf.h_q, buf.h_s)
+    if norms is not None and shared is None:   # the combination is the post norm's first step
+        norms[0].after(x_in, *norms[2:], buf.y, row_of=buf.row_of, topk_w=buf.topk_w, total=buf.out)
+        return
     moe_combine(buf.y, buf.row_of, buf.topk_w, buf.k, buf.out)
     if shared is not None:
         shared[0].forward(x, *shared[1:], buf.out)
+    if norms is not None:
+        norms[0].after(x_in, *norms[2:], buf.out)
 
 
 def backward(buf: Buffers, dout, w1, w2, stages=MOE_STAGES_BWD, act=MOE_ACT_SWIGLU, logits=None,
              renorm=False, x=None, mx=False, dgrad2_mx=True, mx_bf16_copies=True, router=None, shared=None,
-             x_tokens=None):
+             x_tokens=None, routing=None, norms=None):
     """gather dO -> dgrad2+dGLU (+dS) -> wgrad2 -> dgrad1 -> unpermute-sum -> wgrad1, and with
     the forward's logits also the router backward dS -> dlogits. With x given (the un-permuted
     input), the GEMMs read x and dO through src_of instead of permuted copies. With mx (buffers
@@ -971,8 +1065,19 @@ def backward(buf: Buffers, dout, w1, w2, stages=MOE_STAGES_BWD, act=MOE_ACT_SWIG
     buf.a_w are left untouched), which is all the later MXFP8 stages read. The FC1 wgrad runs
     last, after the unpermute-sum has read dX_perm. router and shared as in forward (x_tokens:
     the layer's input x [T, d] for their weight gradients, unless x is given or they keep an 8-bit
-    checkpoint of it): their gradients are added to dx."""
+    checkpoint of it): their gradients are added to dx. routing as in forward. norms as in forward, with x or
+    x_tokens the residual stream that it was given: dout is the gradient of the block's output, and the BlockNorms' dx
+    that of the residual stream."""
+    if buf.served:
+        raise ValueError("the last forward ran on 4-bit weights and kept nothing for a backward pass")
     x_in = x if x is not None else x_tokens
+    if norms is not None:
+        if x_in is None:
+            raise ValueError("the norms' backward needs x or x_tokens")
+        stream, dblock = x_in, dout
+        dout = norms[0].back_after(dblock, *norms[2:], buf.out)
+        x_in = norms[0].y
+        x = x_in if x is not None else None
     if x_in is None and (router is not None or (shared is not None and not shared[0].x8)):
         raise ValueError("the router's and the shared expert's weight gradients need x or x_tokens")
     if buf.ckpt8 and (stages & MOE_STAGE_DGRAD2):
@@ -1012,6 +1117,11 @@ def backward(buf: Buffers, dout, w1, w2, stages=MOE_STAGES_BWD, act=MOE_ACT_SWIG
     if router is not None:
         logits = router[0].logits
     if logits is not None:
-        moe_route_bwd(logits, buf.topk_idx, buf.ds, buf.dlogits, renorm)
+        if routing is not None:
+            moe_route_scores_bwd(logits, buf.topk_idx, buf.ds, buf.dlogits, routing)
+        else:
+            moe_route_bwd(logits, buf.topk_idx, buf.ds, buf.dlogits, renorm)
     if router is not None:
         router[0].backward(x_in, router[1], buf.dlogits, buf.dx)
+    if norms is not None:
+        norms[0].back_before(buf.dx, dblock, stream, norms[1])
