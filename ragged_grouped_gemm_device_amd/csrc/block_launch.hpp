@@ -27,15 +27,6 @@ int launch_route_scores(const RouteCall& c, hipStream_t s);
 int launch_route_scores_bwd(const float* logits, const float* bias, const int32_t* topk_idx, const float* ds, int T,
                             int E, int k, int sigmoid, int renorm, float scale, float* dlogits, hipStream_t s);
 
-// The ragged layout of given choices (route.hip). Fused: the histograms of `nchunks` chunks of CT tokens are
-// in hist and src_of is filled with -1; else both are made here (hist: 2 nchunks E words, chunks of
-// kChunkPairs pairs).
-bool layout_fused_fits(int64_t nchunks, int E);
-void launch_layout_fused(const int32_t* topk_idx, int T, int k, int E, int CT, int nchunks, const int32_t* hist,
-                         int32_t* counts, int32_t* offsets, int32_t* row_of, int32_t* src_of, hipStream_t s);
-void launch_layout(const int32_t* topk_idx, int T, int k, int E, int nchunks, int32_t* hist, int32_t* counts,
-                   int32_t* offsets, int32_t* row_of, int32_t* src_of, int64_t M_cap, hipStream_t s);
-
 // ---- 4-bit blocks (MXFP4: E2M1 codes, two a byte, the first in the low half; E8M0 scales over 32)
 int launch_quant_mxfp4(const uint16_t* src, int batch, int64_t R, int C, int mode, uint8_t* q_row, uint8_t* s_row,
                        uint8_t* q_col, uint8_t* s_col, hipStream_t s);

@@ -20,9 +20,9 @@
 //   per (token, expert) pair, regions padded to the alignment unit.]
 #include <mutex>
 
-#include "block_launch.hpp"
 #include "common.hpp"
 #include "launch.hpp"
+#include "route_common.hpp"
 
 namespace moe {
 
@@ -231,18 +231,6 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const float* __restrict
                             s_x[threadIdx.x >> 6]);
 }
 
-// Lanes of this wavefront whose value of e (0 <= e < 2^nbits) equals ours.
-__device__ __forceinline__ uint64_t match_lanes(int e, bool valid, int nbits) {
-    uint64_t m = __ballot(valid);
-    for (int b = 0; b < nbits; ++b) {
-        const bool bit = (e >> b) & 1;
-        const uint64_t bb = __ballot(bit);
-        m &= bit ? bb : ~bb;
-    }
-    return valid ? m : 0ull;
-}
-
-
 // Inclusive prefix sum of v over the 256 threads of a workgroup (part: 256
 // ints of LDS); *total receives the sum of all. Begins and ends with a barrier.
 __device__ __forceinline__ int32_t block_scan256(int32_t v, int32_t* part, int32_t* total) {
@@ -284,31 +272,6 @@ __device__ __forceinline__ void aligned_offsets(const int32_t* tot, int E, int32
     }
     if (tid == 0) off[E] = all;
     __syncthreads();
-}
-
-// In-order ranks of the pairs [q0, q1) by one wavefront, 64 at a time: pair p
-// with expert e gets row cnt[e] + (earlier lanes with the same e), and the
-// group's first lane advances cnt[e] (cnt: the wavefront's own LDS row).
-__device__ __forceinline__ void rank_pairs(const int32_t* __restrict__ topk_idx, int64_t q0, int64_t q1,
-                                           int nbits, int32_t* cnt, int32_t* __restrict__ row_of,
-                                           int32_t* __restrict__ src_of) {
-    const int lane = lane_id();
-    const uint64_t lt = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
-    for (int64_t sb = q0; sb < q1; sb += 64) {
-        const int64_t p = sb + lane;
-        const bool valid = p < q1;
-        const int e = valid ? topk_idx[p] : 0;
-        const uint64_t m = match_lanes(e, valid, nbits);
-        int32_t row = 0;
-        if (valid) row = cnt[e] + __popcll(m & lt);
-        wave_lds_sync();
-        if (valid && (m & lt) == 0ull) cnt[e] = row + __popcll(m);  // group leader advances
-        wave_lds_sync();
-        if (valid) {
-            row_of[p] = row;
-            src_of[row] = (int32_t)p;
-        }
-    }
 }
 
 // ---- Fused path (two kernels) ----------------------------------------------
@@ -676,17 +639,13 @@ struct RoutePlan {
 constexpr int64_t kFusedHist = 65536, kFusedHistReads = (int64_t)8 << 20;
 constexpr int kFusedPasses = 2;
 
-bool layout_fused_fits(int64_t nchunks, int E) {
-    return nchunks * E <= kFusedHist && nchunks * nchunks * E <= kFusedHistReads;
-}
-
 static RoutePlan route_plan(int T, int k, int E) {
     RoutePlan pl{};
     pl.G = E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64;
     for (int passes = 1; passes <= kFusedPasses; passes *= 2) {
         const int64_t ct = (int64_t)(kRouteBlock / pl.G) * passes;
         const int64_t nc = ((int64_t)T + ct - 1) / ct;
-        if (layout_fused_fits(nc, E)) {
+        if (nc * E <= kFusedHist && nc * nc * E <= kFusedHistReads) {
             pl.fused = true;
             pl.nchunks = (int)nc;
             pl.CT = (int)ct;
@@ -698,35 +657,14 @@ static RoutePlan route_plan(int T, int k, int E) {
     return pl;
 }
 
-static int expert_bits(int E) {
-    int nbits = 0;
-    while ((1 << nbits) < E) ++nbits;
-    return nbits;
-}
-
-void launch_layout_fused(const int32_t* topk_idx, int T, int k, int E, int CT, int nchunks, const int32_t* hist,
-                         int32_t* counts, int32_t* offsets, int32_t* row_of, int32_t* src_of, hipStream_t s) {
-    layout_chunk_kernel<<<nchunks, 256, 0, s>>>(topk_idx, T, k, E, expert_bits(E), CT, nchunks, hist, counts, offsets,
-                                                row_of, src_of);
-}
-
-void launch_layout(const int32_t* topk_idx, int T, int k, int E, int nchunks, int32_t* hist, int32_t* counts,
-                   int32_t* offsets, int32_t* row_of, int32_t* src_of, int64_t M_cap, hipStream_t s) {
-    const int64_t P = (int64_t)T * k;
-    int32_t* base = hist + (int64_t)nchunks * E;
-    const int nblk = (nchunks + 3) / 4;
-    const size_t lds = 4 * (size_t)E * sizeof(int32_t);
-    layout_hist_kernel<<<nblk, 256, lds, s>>>(topk_idx, P, E, nchunks, hist, src_of, M_cap);
-    layout_scan_kernel<<<E, 256, 0, s>>>(hist, nchunks, E, base, counts);
-    layout_scatter_kernel<<<nblk, 256, lds, s>>>(topk_idx, P, E, expert_bits(E), nchunks, base, counts, offsets,
-                                                 row_of, src_of);
-}
-
 int launch_route(const float* logits, int T, int E, int k, int renorm, int32_t* topk_idx,
                  float* topk_w, int32_t* counts, int32_t* offsets, int32_t* row_of,
                  int32_t* src_of, int64_t M_cap, int32_t* err_word, void* ws, hipStream_t s) {
     const RoutePlan pl = route_plan(T, k, E);
+    const int64_t P = (int64_t)T * k;
     int32_t* hist = (int32_t*)ws;
+    int nbits = 0;
+    while ((1 << nbits) < E) ++nbits;
     if (pl.fused) {
         auto first = [&](auto kern) {
             kern<<<pl.nchunks, kRouteBlock, 0, s>>>(logits, T, E, k, renorm, pl.CT, topk_idx, topk_w, err_word,
@@ -746,9 +684,11 @@ int launch_route(const float* logits, int T, int E, int k, int renorm, int32_t* 
             first(route_chunk_kernel<64, 8>);
         else
             first(route_chunk_kernel<64, MOE_MAX_E / 64>);
-        launch_layout_fused(topk_idx, T, k, E, pl.CT, pl.nchunks, hist, counts, offsets, row_of, src_of, s);
+        layout_chunk_kernel<<<pl.nchunks, 256, 0, s>>>(topk_idx, T, k, E, nbits, pl.CT, pl.nchunks, hist,
+                                                       counts, offsets, row_of, src_of);
         return hipGetLastError() == hipSuccess ? 0 : -4;
     }
+    int32_t* base = hist + (int64_t)pl.nchunks * E;
     auto topk = [&](auto kern) {
         const int64_t blocks = ((int64_t)T * pl.G + 255) / 256;
         kern<<<(unsigned)blocks, 256, 0, s>>>(logits, T, E, k, renorm, topk_idx, topk_w, err_word);
@@ -767,7 +707,12 @@ int launch_route(const float* logits, int T, int E, int k, int renorm, int32_t* 
         topk(route_topk_kernel<64, 8>);
     else
         topk(route_topk_kernel<64, MOE_MAX_E / 64>);
-    launch_layout(topk_idx, T, k, E, pl.nchunks, hist, counts, offsets, row_of, src_of, M_cap, s);
+    const int nblk = (pl.nchunks + 3) / 4;
+    const size_t lds = 4 * (size_t)E * sizeof(int32_t);
+    layout_hist_kernel<<<nblk, 256, lds, s>>>(topk_idx, P, E, pl.nchunks, hist, src_of, M_cap);
+    layout_scan_kernel<<<E, 256, 0, s>>>(hist, pl.nchunks, E, base, counts);
+    layout_scatter_kernel<<<nblk, 256, lds, s>>>(topk_idx, P, E, nbits, pl.nchunks, base, counts, offsets,
+                                                 row_of, src_of);
     return hipGetLastError() == hipSuccess ? 0 : -4;
 }
 

@@ -19,11 +19,13 @@
 
 #include "block_common.hpp"
 #include "launch.hpp"
+#include "route_common.hpp"
 
 namespace moe {
 
-constexpr int kScoresThreads = 256;
-constexpr float kUnavailable = -INFINITY;
+constexpr int kScoresThreads = 1024;  // 64 tokens a pass and workgroup with 16 lanes a token
+constexpr int kScoresGroups = 256;    // workgroups at most: one a compute unit
+constexpr int kMaxCand = 64;          // candidates that are ranked in fp32
 
 struct RouteArgs {
     const float* logits;
@@ -36,28 +38,81 @@ struct RouteArgs {
     float* topk_w;
     int32_t* err_word;  // nullable
     int CT;             // tokens a workgroup
-    int32_t* hist;      // [workgroups, E], or nullptr: no counts
-    int32_t* src_of;    // filled with -1 beside the counts
+    int32_t* hist;      // [workgroups, E]
+    int32_t* src_of;
     int64_t M_cap;
 };
 
-// LDS of a wavefront: candidates (or, for a 64-bit choice, all scores), the groups' values, and the
-// chosen experts of its tokens.
+// LDS of a wavefront: its tokens' choice values (or all 64-bit ones of a token), the candidates, the groups'
+// values, and the chosen experts.
 template <int L, int PER>
-struct RouteLds {
-    static constexpr int kTokens = 64 / L, kRow = L * PER;
+struct __align__(16) RouteLds {
+    static constexpr int kTokens = 64 / L, kRow = L * PER, kSel = (L == 16 ? 16 : kRouteMaxTopk) + 2;
     union {
-        uint2 cand[kTokens][kRow];  // key, expert
         float key[kTokens][kRow];
-        double exact[64 * PER];
+        double exact[kRow];
     };
-    double gexact[kRouteMaxGroups];
-    float gval[kTokens][kRouteMaxGroups];
-    uint16_t sel[kTokens][kRouteMaxTopk];
-    uint8_t gkept[kTokens][kRouteMaxGroups];
+    union {
+        int who[kTokens][kMaxCand];  // candidates
+        int chosen[kRouteMaxTopk];
+    };
+    uint64_t cand[kTokens][kMaxCand];  // their order: see order_of
+    union {
+        float gval[kTokens][kRouteMaxGroups];
+        double gexact[kRouteMaxGroups];
+        uint64_t sel[kTokens][kSel];  // the first k + 1 candidates
+    };
+    uint8_t gkept[kRouteMaxGroups];
 };
 
-__device__ __forceinline__ float logistic(float x) { return 1.f / (1.f + __expf(-x)); }
+// Integers in the order of the floats, and back. (-0 comes before 0: good for a bound, not for a choice.)
+__device__ __forceinline__ int ordered(float v) {
+    const int u = __float_as_int(v);
+    return u ^ (int)((uint32_t)(u >> 31) >> 1);
+}
+__device__ __forceinline__ float from_ordered(int u) { return __int_as_float(u ^ (int)((uint32_t)(u >> 31) >> 1)); }
+
+// One number in which larger keys, and of equal ones lower experts, are larger; 0 sorts behind them all.
+__device__ __forceinline__ uint64_t order_of(float key, int e) {
+    const uint32_t k = (uint32_t)ordered(key + 0.f) ^ 0x80000000u;  // -0 + 0 = 0
+    return (uint64_t)k << 32 | (uint32_t)(0xffff - e);
+}
+__device__ __forceinline__ float key_of(uint64_t o) { return from_ordered((int)((uint32_t)(o >> 32) ^ 0x80000000u)); }
+__device__ __forceinline__ int expert_of(uint64_t o) { return 0xffff - (int)(uint32_t)o; }
+
+// The larger of two numbers of which none is a NaN: fmaxf first makes both quiet, one more instruction each.
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
+__device__ __forceinline__ float smaller(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -INFINITY); }
+
+template <int CTRL>
+__device__ __forceinline__ int lane_dpp_i(int v) { return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true); }
+
+template <int L>
+__device__ __forceinline__ int lanes_max_i(int v) {
+    v = max(v, lane_dpp_i<0xB1>(v));
+    v = max(v, lane_dpp_i<0x4E>(v));
+    v = max(v, lane_dpp_i<0x141>(v));
+    v = max(v, lane_dpp_i<0x140>(v));
+    if constexpr (L == 64) {
+        v = max(v, __shfl_xor(v, 16, 64));
+        v = max(v, __shfl_xor(v, 32, 64));
+    }
+    return v;
+}
+
+// Inclusive prefix sum over the lanes of a group (row shifts bring 0 in from outside a row).
+template <int L>
+__device__ __forceinline__ int lanes_scan(int v, int gl) {
+    v += lane_dpp_i<0x111>(v);
+    v += lane_dpp_i<0x112>(v);
+    v += lane_dpp_i<0x114>(v);
+    v += lane_dpp_i<0x118>(v);
+    if constexpr (L == 64) {
+        const int a = __shfl(v, 15, 64), b = __shfl(v, 31, 64), c = __shfl(v, 47, 64);
+        v += (gl >= 16 ? a : 0) + (gl >= 32 ? b : 0) + (gl >= 48 ? c : 0);
+    }
+    return v;
+}
 
 // exp(a - b) with the rounding of the difference made good: it would be an error of up to 2^-24 |a - b| of
 // the result.
@@ -78,21 +133,16 @@ struct SlotScore {
     }
 };
 
-// Are the scores of two experts with equal fp32 values certainly equal, or only near?
-__device__ __forceinline__ bool same_inputs(const RouteArgs& p, const float* row, int a, int b) {
-    return row[a] == row[b] && (!p.bias || p.bias[a] == p.bias[b]);
-}
-
 __device__ __forceinline__ bool available(const RouteArgs& p, const float* row, int e) {
     return isfinite(row[e]) && (!p.bias || isfinite(p.bias[e]));
 }
 
-// The choice for token t by a whole wavefront, with 64-bit scores. A dropped expert's key is NaN, which
-// no comparison prefers.
-__device__ __forceinline__ void choose_exact(const RouteArgs& p, int t, double* key, double* gval, uint8_t* gkept,
-                                             uint16_t* sel) {
+// Token t by a whole wavefront, with 64-bit scores: its choice, weights and counts. A dropped expert's key is
+// NaN, which no comparison prefers. sel: LDS of kRouteMaxTopk experts.
+__device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t, double* key, double* gval, uint8_t* gkept,
+                                            int* sel, int32_t* cnt) {
     const int lane = lane_id();
-    const float* row = p.logits + (int64_t)t * p.E;
+    const float* row = p.logits + t * p.E;
     double mx = -INFINITY, sum = 0;
     if (!p.sigmoid) {
         for (int e = lane; e < p.E; e += 64)
@@ -103,7 +153,9 @@ __device__ __forceinline__ void choose_exact(const RouteArgs& p, int t, double* 
         for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
     }
     auto score = [&](int e) -> double {
-        return p.sigmoid ? 1.0 / (1.0 + exp(-(double)row[e])) : exp((double)row[e] - mx) / sum;
+        const double x = row[e];
+        const double v = exp(p.sigmoid ? -x : x - mx);
+        return p.sigmoid ? 1.0 / (1.0 + v) : v / sum;
     };
     const bool by_score = p.bias || (p.groups > 1 && p.top == 2);
     wave_lds_sync();
@@ -157,14 +209,39 @@ __device__ __forceinline__ void choose_exact(const RouteArgs& p, int t, double* 
             }
         }
         if (lane == 0) {
-            sel[j] = (uint16_t)be;
+            sel[j] = be;
             key[be] = NAN;
         }
         wave_lds_sync();
     }
+    const bool mine = lane < p.k;
+    const int e = mine ? sel[lane] : 0;
+    const bool ok = mine && available(p, row, e);
+    double w = 0;
+    if (p.renorm) {  // over the best chosen logit, so that scores that underflow keep their ratios
+        const double x = ok ? (double)row[e] : -INFINITY;
+        double xs = x;
+        for (int o = 32; o > 0; o >>= 1) xs = fmax(xs, __shfl_xor(xs, o, 64));
+        if (ok) w = p.sigmoid ? exp(fmin(x, 0.0) - fmin(xs, 0.0)) / (1.0 + exp(-fabs(x))) : exp(x - xs);
+        double total = w;
+        for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o, 64);
+        if (ok) w /= total;
+    } else if (ok) {
+        w = score(e);
+    }
+    if (mine) {
+        p.topk_idx[t * p.k + lane] = e;
+        p.topk_w[t * p.k + lane] = (float)(p.scale * w);
+        atomicAdd(&cnt[e], 1);
+    }
+    wave_lds_sync();
 }
 
-template <int L, int PER>
+// SIGMOID: the scores; BIAS: there is one, so that scores and not logits are compared. Bound by its
+// instructions (about 700 for the four tokens of a wavefront), so the steps are written to be few: values that
+// take no part are -inf, not NaN; maxima are integers where lanes exchange them; the candidates are found from
+// a bit mask a lane; their order is one 64-bit comparison.
+template <int L, int PER, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kScoresThreads) route_scores_kernel(RouteArgs p) {
     constexpr int TW = 64 / L, TB = kScoresThreads / L;  // tokens a wavefront, a workgroup and pass
     __shared__ RouteLds<L, PER> s_lds[kScoresThreads / 64];
@@ -172,193 +249,342 @@ __global__ void __launch_bounds__(kScoresThreads) route_scores_kernel(RouteArgs 
     const int lane = lane_id(), gl = lane % L, tw = lane / L;
     RouteLds<L, PER>& lds = s_lds[threadIdx.x >> 6];
     const int E = p.E, k = p.k;
-    if (p.hist) {
-        for (int e = threadIdx.x; e < E; e += kScoresThreads) s_cnt[e] = 0;
-        for (int64_t r = (int64_t)blockIdx.x * kScoresThreads + threadIdx.x; r < p.M_cap;
-             r += (int64_t)gridDim.x * kScoresThreads)
-            p.src_of[r] = -1;
-        __syncthreads();
-    }
-    const bool whole = (E & 3) == 0 && ((uintptr_t)p.logits & 15) == 0;  // rows in 16-byte pieces
-    const bool by_score = p.bias != nullptr;
+    const bool whole = (E & 3) == 0 && (((uintptr_t)p.logits | (uintptr_t)p.bias) & 15) == 0;  // rows in 16-byte pieces
     auto expert = [&](int i) { return 4 * (gl + L * (i >> 2)) + (i & 3); };
-    // every lane of a workgroup runs the token loop equally often; a token past the end is idle
-    const int64_t t0 = (int64_t)blockIdx.x * p.CT, t1 = min((int64_t)p.T, t0 + p.CT);
-    for (int64_t tb = t0; tb < t1; tb += TB) {
-        const int64_t t = tb + threadIdx.x / L;
-        const bool live = t < t1;
-        const float* row = p.logits + (live ? t : t0) * E;
-        float x[PER], key[PER];
-        bool bad = false;
+    // a row of E values, 16 bytes at a time, -inf past its end; other rows by way of LDS
+    auto load_row = [&](const float* row, float (&v)[PER]) {
+        if (!whole) {
+            wave_lds_sync();
+            for (int e = gl; e < ((E + 3) & ~3); e += L) lds.key[tw][e] = e < E ? row[e] : -INFINITY;
+            wave_lds_sync();
+        }
 #pragma unroll
         for (int q = 0; q < PER / 4; ++q) {
             const int e = expert(4 * q);
-            if (whole) {
-                const float4 v = e < E ? *(const float4*)(row + e) : make_float4(0, 0, 0, 0);
-                x[4 * q] = v.x, x[4 * q + 1] = v.y, x[4 * q + 2] = v.z, x[4 * q + 3] = v.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[4 * q + j] = e + j < E ? row[e + j] : 0.f;
-            }
+            float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (e < E) f = whole ? *(const float4*)(row + e) : *(const float4*)&lds.key[tw][e];
+            v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
         }
-        float mx = -INFINITY;
+        if (!whole) wave_lds_sync();
+    };
+    int absent = 0;  // values that this lane holds past the last expert
+#pragma unroll
+    for (int i = 0; i < PER; ++i) absent += expert(i) >= E;
+    const int64_t t0 = (int64_t)blockIdx.x * p.CT, t1 = min((int64_t)p.T, t0 + p.CT);
+    const int64_t mine = t0 + threadIdx.x / L;  // this group's first token
+    float x[PER], bias[PER];
+    if (whole && mine - tw < t1) load_row(p.logits + min(mine, t1 - 1) * E, x);
+    if constexpr (BIAS) {
+        load_row(p.bias, bias);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) bias[i] = isfinite(bias[i]) ? bias[i] : -INFINITY;
+    }
+    for (int e = threadIdx.x; e < E; e += kScoresThreads) s_cnt[e] = 0;
+    for (int64_t r = (int64_t)blockIdx.x * kScoresThreads + threadIdx.x; r < p.M_cap;
+         r += (int64_t)gridDim.x * kScoresThreads)
+        p.src_of[r] = -1;
+    __syncthreads();
+    const int gs = E / p.groups;
+    // lanes that share a group's members, in whole 16-byte pieces
+    int per_group = 1;
+    while (2 * per_group * p.groups <= L && gs % (8 * per_group) == 0) per_group *= 2;
+    // a wavefront's tokens leave the loop together (lane exchanges need all of them); one past the end is idle
+    for (int64_t t = mine; t - tw < t1; t += TB) {
+        const bool live = t < t1;
+        const float* row = p.logits + min(t, t1 - 1) * E;
+        if (!whole) load_row(row, x);
+        // Opaque, so that what follows from it for each of PER values is formed where it is used: kept over the
+        // loop, those indexes take more registers than there are.
+        uint32_t mul = p.group_mul;
+        asm volatile("" : "+s"(mul));
+        float key[PER];
+        int unfit = 0;
+        float mx = -INFINITY, inv = 1.f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const bool fin = isfinite(x[i]);
-            bad |= live && !fin && expert(i) < E;
-            if (!fin || expert(i) >= E) x[i] = -INFINITY;  // never preferred
-            mx = fmaxf(mx, x[i]);
+            const bool fin = fabsf(x[i]) < INFINITY;
+            unfit += !fin;
+            x[i] = fin ? x[i] : -INFINITY;  // never preferred
         }
-        if (__ballot(bad) != 0ull && lane == 0 && p.err_word) atomicOr(p.err_word, MOE_ERRBIT_NONFINITE_LOGIT);
-        mx = lanes_max<L>(mx);
-        // a score is p.sigmoid ? logistic(x) : exp(x - mx) * inv
-        float inv = 1.f;
-        if (!p.sigmoid) {
+        if (__ballot(live && unfit != absent) != 0ull && lane == 0 && p.err_word)
+            atomicOr(p.err_word, MOE_ERRBIT_NONFINITE_LOGIT);
+        if constexpr (!SIGMOID) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) mx = larger(mx, x[i]);
+            mx = from_ordered(lanes_max_i<L>(ordered(mx)));
+            const float shift = mx > -INFINITY ? mx : 0.f;
             float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) sum += x[i] > -INFINITY ? __expf(x[i] - mx) : 0.f;
+            for (int i = 0; i < PER; ++i) sum += __expf(x[i] - shift);
             sum = lanes_sum<L>(sum);
             inv = sum > 0.f ? 1.f / sum : 0.f;
         }
-        auto score = [&](float v) { return p.sigmoid ? logistic(v) : __expf(v - mx) * inv; };
+        auto score = [&](float v) { return SIGMOID ? sigmoid_f(v) : __expf(v - mx) * inv; };
         // How far apart two fp32 values have to be for their order to be that of the exact ones: a score is
-        // off by at most 8 steps of 2^-24 of itself (exponential, sum, reciprocal, product) and its sum with
-        // the bias by one of 2^-24 of that; twice, and doubled for the margin.
-        const float smax = p.sigmoid ? 1.f : inv;
-        auto near = [&](float v) { return v > -INFINITY ? 0x1p-19f * smax + 0x1p-21f * fabsf(v) : 0.f; };
+        // off by at most 8 steps of 2^-24 of the largest (exponential, sum, reciprocal, product) and its sum
+        // with the bias by one of 2^-24 of that; twice, and doubled for the margin.
+        const float smax = SIGMOID ? 1.f : inv;
+        auto near = [&](float v) { return 0x1p-19f * smax + 0x1p-21f * fabsf(v); };
         bool doubt = false;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             key[i] = x[i];
-            if (by_score) {
-                const int e = expert(i);
-                const float b = e < E ? p.bias[e] : 0.f;
-                key[i] = x[i] > -INFINITY && isfinite(b) ? score(x[i]) + b : kUnavailable;
+            if constexpr (BIAS) {
+                float c = score(x[i]) + bias[i];
+                asm("" : "+v"(c));  // a selection, not a branch around the score
+                key[i] = x[i] > -INFINITY ? c : -INFINITY;
             }
         }
+        const bool plain = BIAS || p.top == 1;  // groups are valued by the keys themselves
+#pragma unroll
+        for (int q = 0; q < PER / 4; ++q) {
+            float4 f = make_float4(key[4 * q], key[4 * q + 1], key[4 * q + 2], key[4 * q + 3]);
+            if (p.groups > 1 && !plain) {
+                auto valued = [&](float c) { return c > -INFINITY ? score(c) : c; };
+                f = make_float4(valued(f.x), valued(f.y), valued(f.z), valued(f.w));
+            }
+            *(float4*)&lds.key[tw][expert(4 * q)] = f;
+        }
+        wave_lds_sync();
         if (p.groups > 1) {
-            const bool exact = !by_score && p.top == 1;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                if (expert(i) < E)
-                    lds.key[tw][expert(i)] = by_score || exact || !(x[i] > -INFINITY) ? key[i] : score(x[i]);
-            }
-            wave_lds_sync();
-            const int gs = E / p.groups;
-            for (int g = gl; g < p.groups; g += L) {
+            const bool exact = !BIAS && p.top == 1;
+            const int g4 = (p.groups + 3) & ~3, part = gs / per_group;
+            for (int j = gl; j < g4 * per_group; j += L) {
+                const int g = j / per_group;
                 float a = -INFINITY, b = -INFINITY;
-                for (int e = g * gs; e < (g + 1) * gs; ++e) {
-                    const float v = lds.key[tw][e];
-                    b = fmaxf(b, fminf(a, v));
-                    a = fmaxf(a, v);
+                auto take = [&](float v) {
+                    b = __builtin_amdgcn_fmed3f(a, b, v);
+                    a = larger(a, v);
+                };
+                if (g < p.groups) {
+                    const float* m = &lds.key[tw][j * part];
+                    if ((part & 3) == 0) {
+#pragma unroll 4
+                        for (int i = 0; i < part; i += 4) {
+                            const float4 f = *(const float4*)(m + i);
+                            take(f.x), take(f.y), take(f.z), take(f.w);
+                        }
+                    } else {
+#pragma unroll 4
+                        for (int i = 0; i < part; ++i) take(m[i]);
+                    }
                 }
-                lds.gval[tw][g] = p.top == 2 && b > -INFINITY ? a + b : a;
+                for (int o = 1; o < per_group; o <<= 1) {  // then groups * per_group <= L: one turn, all lanes in it
+                    const float a2 = __shfl_xor(a, o, L), b2 = __shfl_xor(b, o, L);
+                    b = larger(smaller(a, a2), larger(b, b2));
+                    a = larger(a, a2);
+                }
+                if (j % per_group == 0) lds.gval[tw][g] = p.top == 2 && b > -INFINITY ? a + b : a;
             }
             wave_lds_sync();
-            for (int g = gl; g < p.groups; g += L) {
-                const float v = lds.gval[tw][g];
-                int rank = 0;
-                bool close = false;
-                for (int o = 0; o < p.groups; ++o) {
-                    const float u = lds.gval[tw][o];
-                    rank += u > v || (u == v && o < g);
-                    close |= o != g && fabsf(u - v) <= 2.f * near(v);  // not where both are -inf
+            uint64_t kept = 0;  // this token's groups
+            for (int g0 = 0; g0 < p.groups; g0 += L) {
+                const int g = g0 + gl;
+                const float v = g < p.groups ? lds.gval[tw][g] : -INFINITY;
+                const float d = 2.f * near(v);
+                int rank = 0, close = 0;
+#pragma unroll 2
+                for (int o = 0; o < g4; o += 4) {
+                    const float4 f = *(const float4*)&lds.gval[tw][o];
+                    const float u[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        rank += (int)(u[j] > v) | ((int)(u[j] == v) & (int)(o + j < g));
+                        close += fabsf(u[j] - v) <= d;  // itself; not where both are -inf
+                    }
                 }
-                lds.gkept[tw][g] = rank < p.kept;
+                const bool keep = g < p.groups && rank < p.kept;
                 // a pair on two sides of the border holds one that is kept and near another
-                doubt |= !exact && close && rank < p.kept;
+                doubt |= !exact && keep && v > -INFINITY && close > 1;
+                const uint64_t all = __ballot(keep);
+                kept |= (L == 64 ? all : (all >> (lane & 48)) & 0xffffull) << g0;
             }
-            wave_lds_sync();
+            auto dropped = [&](int i) { return !((kept >> (((uint32_t)expert(i) * mul >> 22) & 63)) & 1); };
+            if ((gs & 3) == 0) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int e = expert(i);
-                if (e >= E || !lds.gkept[tw][(uint32_t)e * p.group_mul >> 22]) key[i] = NAN;  // dropped
+                for (int q = 0; q < PER / 4; ++q) {
+                    const bool drop = dropped(4 * q);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) key[4 * q + j] = drop ? -INFINITY : key[4 * q + j];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) key[i] = dropped(i) ? -INFINITY : key[i];
             }
-            wave_lds_sync();
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (expert(i) >= E) key[i] = NAN;
         }
+        // the next tokens' logits, on the way while these are chosen
+        if (whole && t + TB - tw < t1) load_row(p.logits + min(t + TB, t1 - 1) * E, x);
         // a value that at least k keys reach: the k-th largest of the lanes' maxima
-        float most = -INFINITY, least = -INFINITY;
+        float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) most = fmaxf(most, key[i]);  // not the NaN
+        for (int i = 0; i < PER; ++i) top = larger(top, key[i]);
+        int most = ordered(top), least = most;
         for (int r = 0; r < k; ++r) {
-            least = lanes_max<L>(most);
-            if (most == least) most = -INFINITY;
+            least = lanes_max_i<L>(most);
+            most = most == least ? INT32_MIN : most;
         }
-        const float floor_ = by_score ? least - near(least) : least;
-        int mine = 0;
+        const float reached = from_ordered(least);
+        // too few that are available: the exact form tells those apart that are kept from those that are not
+        bool odd = !(least > ordered(-INFINITY));
+        const float from = odd ? INFINITY : BIAS ? reached - near(reached) : reached;
+        uint32_t hits = 0;  // bit PER - 1 - i: key i
 #pragma unroll
-        for (int i = 0; i < PER; ++i) mine += key[i] >= floor_ ? 1 : 0;
-        int at = mine;  // inclusive prefix over the token's lanes
-#pragma unroll
-        for (int o = 1; o < L; o <<= 1) {
-            const int u = __shfl_up(at, o, L);
-            if (gl >= o) at += u;
+        for (int i = 0; i < PER; ++i) hits = 2 * hits + (key[i] >= from ? 1u : 0u);
+        const int n = __popc(hits);
+        int at = lanes_scan<L>(n, gl);
+        int m = L == 64 ? __shfl(at, 63, 64) : __shfl(at, 15, 16);
+        at -= n;
+        if (m > kMaxCand) odd = true;  // many equal values
+        if (odd) hits = 0, m = 0;
+        while (hits) {
+            const int b = 31 - __clz((int)hits), i = PER - 1 - b;
+            hits ^= 1u << b;
+            lds.who[tw][at++] = expert(i);
         }
-        const int m = __shfl(at, L - 1, L);
-        at -= mine;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            if (key[i] >= floor_) lds.cand[tw][at++] = make_uint2(__float_as_uint(key[i]), (uint32_t)expert(i));
+        wave_lds_sync();
+        // The candidates' order. Their keys are in LDS, but as scores where groups are valued so and logits compared.
+        const bool reread = !BIAS && p.groups > 1 && !plain;
+        for (int c = gl; c < m; c += L) {
+            const int e = lds.who[tw][c];
+            lds.cand[tw][c] = order_of(reread ? row[e] : lds.key[tw][e], e);
         }
         wave_lds_sync();
         for (int c = gl; c < m; c += L) {
-            const uint2 own = lds.cand[tw][c];
-            const float v = __uint_as_float(own.x);
-            const float d = near(v);
+            const uint64_t own = lds.cand[tw][c];
             int rank = 0;
-            bool close = false;
-            for (int j = 0; j < m; ++j) {
-                const uint2 o = lds.cand[tw][j];
-                const float u = __uint_as_float(o.x);
-                rank += u > v || (u == v && o.y < own.y);
-                if (by_score && fabsf(u - v) <= d && j != c) close |= !(u == v && same_inputs(p, row, (int)o.y, (int)own.y));
-            }
-            if (rank < k) {
-                lds.sel[tw][rank] = (uint16_t)own.y;
-                doubt |= close;
-            }
+#pragma unroll 4
+            for (int j = 0; j < m; ++j) rank += lds.cand[tw][j] > own;
+            if (rank <= k) lds.sel[tw][rank] = own;
         }
-        // the tokens in doubt, one after the other, by the whole wavefront
-        uint64_t todo = __ballot(doubt && live);
-        while (todo) {
-            const int w = (__ffsll((unsigned long long)todo) - 1) / L;
-            wave_lds_sync();
-            choose_exact(p, (int)(tb + (threadIdx.x >> 6) * TW + w), lds.exact, lds.gexact, lds.gkept[w], lds.sel[w]);
-            todo &= L == 64 ? 0ull : ~(((1ull << (L & 63)) - 1) << (w * L));
-        }
+        if (m == k && gl == 0) lds.sel[tw][k] = 0;  // none behind the last
         wave_lds_sync();
-        // weights, slot by slot
-        float xs = -INFINITY;
-        for (int j = gl; j < k; j += L) {
-            const int e = lds.sel[tw][j];
-            if (live && available(p, row, e)) xs = fmaxf(xs, row[e]);
-        }
-        xs = lanes_max<L>(xs);
-        const SlotScore slot{p.sigmoid != 0, p.renorm != 0, p.sigmoid ? fminf(xs, 0.f) : xs, mx, inv};
-        auto weight = [&](int e) { return available(p, row, e) ? slot(row[e]) : 0.f; };
-        float total = 0.f;
+        // slot by slot: every lane has at most one
+        const bool slots = gl < k && !odd;
+        const uint64_t own = slots ? lds.sel[tw][gl] : 0, next = slots ? lds.sel[tw][gl + 1] : 0;
+        const int e = expert_of(own);
+        const float value = key_of(own);
+        float logit = value;
+        if (BIAS && slots) logit = row[e];
+        if (BIAS && slots) doubt |= next != 0 && value - key_of(next) <= near(value);
+        // a token in doubt is marked, and left for below
+        const uint64_t any = __ballot(doubt || odd);
+        const bool sure = live && (L == 64 ? any : (any >> (lane & 48)) & 0xffffull) == 0;
+        const bool mine_ = slots && sure;
+        const float xs = p.renorm ? lanes_max<L>(mine_ ? logit : -INFINITY) : 0.f;
+        const SlotScore slot{SIGMOID, p.renorm != 0, SIGMOID ? fminf(xs, 0.f) : xs, mx, inv};
+        float w = mine_ ? slot(logit) : 0.f;
         if (p.renorm) {
-            for (int j = gl; j < k; j += L) total += live ? weight(lds.sel[tw][j]) : 0.f;
-            total = lanes_sum<L>(total);
+            const float total = lanes_sum<L>(w);
+            w = total > 0.f ? w / total : 0.f;
         }
-        const float f = !p.renorm ? p.scale : total > 0.f ? p.scale / total : 0.f;
-        for (int j = gl; j < k; j += L) {
-            if (!live) continue;
-            const int e = lds.sel[tw][j];
-            p.topk_idx[t * k + j] = e;
-            p.topk_w[t * k + j] = f * weight(e);
-            if (p.hist) atomicAdd(&s_cnt[e], 1);
+        if (mine_) {
+            p.topk_idx[t * k + gl] = e;
+            p.topk_w[t * k + gl] = p.scale * w;
+            atomicAdd(&s_cnt[e], 1);
+        } else if (live && !sure && gl == 0) {
+            p.topk_idx[t * k] = -1;
         }
         wave_lds_sync();  // the next tokens may overwrite the lists
     }
-    if (p.hist) {
-        __syncthreads();
-        for (int e = threadIdx.x; e < E; e += kScoresThreads) p.hist[(int64_t)blockIdx.x * E + e] = s_cnt[e];
+    __syncthreads();
+    // the tokens in doubt, 64 marks at a time; in a loop of its own, or its 64-bit values would take the
+    // registers of the one above
+    for (int64_t b = t0 + (threadIdx.x & ~63); b < t1; b += kScoresThreads) {
+        uint64_t todo = __ballot(b + lane < t1 && p.topk_idx[(b + lane) * k] < 0);
+        while (todo) {
+            const int at = __ffsll((unsigned long long)todo) - 1;
+            route_exact(p, b + at, lds.exact, lds.gexact, lds.gkept, lds.chosen, s_cnt);
+            todo &= todo - 1;
+        }
     }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kScoresThreads) p.hist[(int64_t)blockIdx.x * E + e] = s_cnt[e];
+}
+
+// The layout from the workgroups' counts, one workgroup of 16 wavefronts a chunk of CT tokens: it sums all
+// counts (the experts' totals) and those before its own, forms the regions' starts, and ranks its pairs in
+// order, each wavefront a sixteenth of them after those before it. Integer sums: the order does not matter.
+__global__ void __launch_bounds__(kScoresThreads) scores_layout_kernel(const int32_t* __restrict__ topk_idx, int T,
+                                                                       int k, int E, int nbits, int CT, int nchunks,
+                                                                       const int32_t* __restrict__ hist,
+                                                                       int32_t* __restrict__ counts,
+                                                                       int32_t* __restrict__ offsets,
+                                                                       int32_t* __restrict__ row_of,
+                                                                       int32_t* __restrict__ src_of) {
+    constexpr int NW = kScoresThreads / 64;
+    __shared__ int32_t s_tot[MOE_MAX_E], s_base[MOE_MAX_E];
+    __shared__ int32_t s_q[NW][MOE_MAX_E];  // the wavefronts' counts, then their first rows
+    const int tid = threadIdx.x, wave = tid >> 6, lane = lane_id(), c = blockIdx.x;
+    s_tot[tid] = s_base[tid] = 0;
+    for (int e = lane; e < E; e += 64) s_q[wave][e] = 0;
+    __syncthreads();
+    const int64_t p0 = (int64_t)c * CT * k, p1 = min((int64_t)T * k, p0 + (int64_t)CT * k);
+    const int64_t len = (p1 - p0 + NW - 1) / NW;
+    const int64_t q0 = min(p1, p0 + wave * len), q1 = min(p1, q0 + len);
+    for (int64_t q = q0 + lane; q < q1; q += 64) atomicAdd(&s_q[wave][topk_idx[q]], 1);
+    {
+        // thread (e, part) sums the chunks part, part + parts, ... of expert e, 8 loads in flight
+        const int parts = kScoresThreads / E, part = tid / E, e = tid - part * E;
+        if (part < parts) {
+            int32_t tot = 0, base = 0;
+            for (int cb = part; cb < nchunks; cb += 8 * parts) {
+                int32_t h[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int cc = cb + u * parts;
+                    h[u] = cc < nchunks ? hist[(int64_t)cc * E + e] : 0;
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    tot += h[u];
+                    base += cb + u * parts < c ? h[u] : 0;
+                }
+            }
+            atomicAdd(&s_tot[e], tot);
+            atomicAdd(&s_base[e], base);
+        }
+    }
+    __syncthreads();
+    // regions' starts by one wavefront, 16 experts a lane
+    if (wave == 0) {
+        constexpr int PL = MOE_MAX_E / 64;
+        int32_t v[PL], run = 0;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            v[i] = (s_tot[PL * lane + i] + MOE_ALIGN_ROWS - 1) / MOE_ALIGN_ROWS * MOE_ALIGN_ROWS;
+            run += v[i];
+        }
+        int32_t at = run;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int32_t u = __shfl_up(at, o, 64);
+            if (lane >= o) at += u;
+        }
+        at -= run;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            const int e = PL * lane + i;
+            s_base[e] += at;
+            if (c == 0 && e < E) {
+                counts[e] = s_tot[e];
+                offsets[e] = at;
+                if (e == E - 1) offsets[E] = at + v[i];
+            }
+            at += v[i];
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += kScoresThreads) {
+        int32_t run = s_base[e];
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const int32_t h = s_q[w][e];
+            s_q[w][e] = run;
+            run += h;
+        }
+    }
+    __syncthreads();
+    rank_pairs(topk_idx, q0, q1, nbits, s_q[wave], row_of, src_of);
 }
 
 // ---- backward --------------------------------------------------------------
@@ -504,46 +730,38 @@ static void by_experts(int E, int k, F&& f) {
     }
 }
 
-// Two kernels where a chunk's workgroup of the second can afford to read all chunks' counts (the limits of
-// moe_route_counts), a chunk being at most 64 tokens; else choice, counts, their scan and the ranks.
-struct ScoresPlan {
-    bool fused;
-    int CT, nchunks;
-};
-static ScoresPlan scores_plan(int T, int k, int E) {
+// Tokens a workgroup: whole passes, at most kScoresGroups workgroups.
+static int scores_chunk(int T, int k, int E) {
     const int tb = kScoresThreads / (E <= 256 && k <= 16 ? 16 : 64);
-    for (int ct = tb; ct <= 64; ct *= 2) {
-        const int64_t nc = ((int64_t)T + ct - 1) / ct;
-        if (layout_fused_fits(nc, E)) return {true, ct, (int)nc};
-    }
-    return {false, tb, (int)(((int64_t)T * k + kChunkPairs - 1) / kChunkPairs)};
+    const int64_t passes = ((int64_t)T + (int64_t)tb * kScoresGroups - 1) / ((int64_t)tb * kScoresGroups);
+    return (int)(tb * passes);
 }
 
 size_t route_scores_workspace_bytes(int T, int k, int E) {
-    const ScoresPlan pl = scores_plan(T, k, E);
-    return (pl.fused ? 1 : 2) * (size_t)pl.nchunks * E * sizeof(int32_t);
+    const int ct = scores_chunk(T, k, E);
+    return (size_t)(((int64_t)T + ct - 1) / ct) * E * sizeof(int32_t);
 }
 
 int launch_route_scores(const RouteCall& c, hipStream_t s) {
-    const ScoresPlan pl = scores_plan(c.T, c.k, c.E);
     RouteArgs p{};
     p.logits = c.logits, p.bias = c.bias, p.T = c.T, p.E = c.E, p.k = c.k;
     p.sigmoid = c.sigmoid, p.groups = c.groups, p.kept = c.kept, p.top = c.top, p.renorm = c.renorm, p.scale = c.scale;
     const uint32_t gs = (uint32_t)(c.E / c.groups);
     p.group_mul = ((1u << 22) + gs - 1) / gs;
     p.topk_idx = c.topk_idx, p.topk_w = c.topk_w, p.err_word = c.err_word;
-    p.CT = pl.CT;
-    if (pl.fused) p.hist = (int32_t*)c.ws, p.src_of = c.src_of, p.M_cap = c.M_cap;
-    const unsigned grid = (unsigned)(((int64_t)c.T + pl.CT - 1) / pl.CT);
+    p.CT = scores_chunk(c.T, c.k, c.E);
+    p.hist = (int32_t*)c.ws, p.src_of = c.src_of, p.M_cap = c.M_cap;
+    const int nchunks = (int)(((int64_t)c.T + p.CT - 1) / p.CT);
     by_experts(c.E, c.k, [&](auto A, auto B) {
-        route_scores_kernel<decltype(A)::value, decltype(B)::value><<<grid, kScoresThreads, 0, s>>>(p);
+        constexpr int L = decltype(A)::value, PER = decltype(B)::value;
+        auto go = [&](auto kern) { kern<<<nchunks, kScoresThreads, 0, s>>>(p); };
+        if (p.sigmoid) p.bias ? go(route_scores_kernel<L, PER, true, true>) : go(route_scores_kernel<L, PER, true, false>);
+        else p.bias ? go(route_scores_kernel<L, PER, false, true>) : go(route_scores_kernel<L, PER, false, false>);
     });
-    if (pl.fused)
-        launch_layout_fused(c.topk_idx, c.T, c.k, c.E, pl.CT, pl.nchunks, (const int32_t*)c.ws, c.counts, c.offsets,
-                            c.row_of, c.src_of, s);
-    else
-        launch_layout(c.topk_idx, c.T, c.k, c.E, pl.nchunks, (int32_t*)c.ws, c.counts, c.offsets, c.row_of, c.src_of,
-                      c.M_cap, s);
+    int nbits = 0;
+    while ((1 << nbits) < c.E) ++nbits;
+    scores_layout_kernel<<<nchunks, kScoresThreads, 0, s>>>(c.topk_idx, c.T, c.k, c.E, nbits, p.CT, nchunks, p.hist,
+                                                            c.counts, c.offsets, c.row_of, c.src_of);
     return hipGetLastError() == hipSuccess ? 0 : -4;
 }
 
