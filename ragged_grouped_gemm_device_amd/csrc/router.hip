@@ -604,111 +604,94 @@ struct RouteBwdArgs {
 //   renormalised     dL/dl_j = scale r_j (1 - p_j) (ds_j - sum_i r_i ds_i)  (sigmoid; a softmax without 1 - p_j)
 //   sigmoid, plain   dL/dl_j = scale ds_j p_j (1 - p_j)
 //   softmax, plain   dL/dl_e = scale p_e (g_e - sum_j p_j ds_j), g_e = ds_j for a chosen one, else 0
-// and 0 for every other expert. L lanes a token; the slots' values go through an LDS row.
-template <int L, int PER>
+// and 0 for every other expert. L lanes a token, one slot each; the slots' values go through an LDS row. DENSE:
+// the softmax that is not renormalised, the one form that reads all logits. Bound by the latency of a slot's
+// loads (expert, then its logit) and the write of dlogits.
+template <int L, int PER, bool DENSE>
 __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs p) {
     __shared__ __align__(16) float s_row[256 / L][L * PER];
     const int gl = lane_id() % L;
     const int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
     const bool live = t < p.T;
-    const int E = p.E, k = p.k;
+    const int E = p.E;
     float* g = s_row[threadIdx.x / L];
     const float* row = p.logits + (live ? t : 0) * E;
     const bool whole = (E & 3) == 0 && (((uintptr_t)p.logits | (uintptr_t)p.dlogits) & 15) == 0;
     auto expert = [&](int i) { return 4 * (gl + L * (i >> 2)) + (i & 3); };
-#pragma unroll
-    for (int q = 0; q < PER / 4; ++q) *(float4*)(g + expert(4 * q)) = make_float4(0, 0, 0, 0);
-    const bool dense = !p.sigmoid && !p.renorm;
-    float x[PER], mx = -INFINITY, inv = 0.f;
-    if (dense) {
-#pragma unroll
-        for (int q = 0; q < PER / 4; ++q) {
-            const int e = expert(4 * q);
-            if (whole) {
-                const float4 v = e < E ? *(const float4*)(row + e) : make_float4(0, 0, 0, 0);
-                x[4 * q] = v.x, x[4 * q + 1] = v.y, x[4 * q + 2] = v.z, x[4 * q + 3] = v.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[4 * q + j] = e + j < E ? row[e + j] : 0.f;
-            }
+    // this lane's slot; none that is out of range or unavailable has a gradient
+    int e = -1;
+    float v = 0.f, d = 0.f;
+    if (live && gl < p.k) {
+        e = p.topk_idx[t * p.k + gl];
+        d = p.ds[t * p.k + gl];
+        if ((uint32_t)e >= (uint32_t)E) e = -1;
+    }
+    if (e >= 0) {
+        v = row[e];
+        if (!isfinite(v) || (p.bias && !isfinite(p.bias[e]))) e = -1;
+    }
+    float x[DENSE ? PER : 1], mx = -INFINITY, inv = 0.f;
+    if constexpr (DENSE) {
+        if (!whole) {
+            for (int q = gl; q < E; q += L) g[q] = row[q];
+            wave_lds_sync();
         }
 #pragma unroll
+        for (int q = 0; q < PER / 4; ++q) {
+            const int c = expert(4 * q);
+            float4 f = make_float4(0, 0, 0, 0);
+            if (c < E) f = whole ? *(const float4*)(row + c) : *(const float4*)(g + c);
+            x[4 * q] = f.x, x[4 * q + 1] = f.y, x[4 * q + 2] = f.z, x[4 * q + 3] = f.w;
+        }
+        if (!whole) wave_lds_sync();
+#pragma unroll
         for (int i = 0; i < PER; ++i) {
-            if (!isfinite(x[i]) || expert(i) >= E) x[i] = -INFINITY;
+            x[i] = isfinite(x[i]) && expert(i) < E ? x[i] : -INFINITY;
             mx = fmaxf(mx, x[i]);
         }
         mx = lanes_max<L>(mx);
+        const float shift = mx > -INFINITY ? mx : 0.f;
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            x[i] = x[i] > -INFINITY ? __expf(x[i] - mx) : 0.f;
+            x[i] = __expf(x[i] - shift);
             sum += x[i];
         }
         sum = lanes_sum<L>(sum);
         inv = sum > 0.f ? 1.f / sum : 0.f;
     }
-    auto slot = [&](int j) -> int {  // the expert of slot j, or -1: none that has a gradient
-        if (!live) return -1;
-        const int e = p.topk_idx[t * k + j];
-        if ((uint32_t)e >= (uint32_t)E) return -1;
-        return isfinite(row[e]) && (!p.bias || isfinite(p.bias[e])) ? e : -1;
-    };
-    float xs = -INFINITY;
-    if (p.renorm) {
-        for (int j = gl; j < k; j += L) {
-            const int e = slot(j);
-            if (e >= 0) xs = fmaxf(xs, row[e]);
-        }
-        xs = lanes_max<L>(xs);
+#pragma unroll
+    for (int q = 0; q < PER / 4; ++q) *(float4*)(g + expert(4 * q)) = make_float4(0, 0, 0, 0);
+    const float xs = p.renorm ? lanes_max<L>(e >= 0 ? v : -INFINITY) : 0.f;
+    const SlotScore score{p.sigmoid != 0, p.renorm != 0, p.sigmoid ? fminf(xs, 0.f) : xs, mx, inv};
+    float w = e >= 0 ? score(v) : 0.f;
+    if (p.renorm) {  // divided, not times a reciprocal: a lone weight is 1 and has no gradient
+        const float total = lanes_sum<L>(w);
+        w = e >= 0 ? w / total : 0.f;
     }
-    const SlotScore weight{p.sigmoid != 0, p.renorm != 0, p.sigmoid ? fminf(xs, 0.f) : xs, mx, inv};
-    float total = 1.f, dot = 0.f;
-    if (p.renorm) {
-        total = 0.f;
-        for (int j = gl; j < k; j += L) {
-            const int e = slot(j);
-            if (e >= 0) total += weight(row[e]);
-        }
-        total = lanes_sum<L>(total);
-    }
-    for (int j = gl; j < k; j += L) {
-        const int e = slot(j);  // divided, not times a reciprocal: a lone weight is 1 and has no gradient
-        if (e >= 0) dot = fmaf(weight(row[e]) / total, p.ds[t * k + j], dot);
-    }
-    dot = lanes_sum<L>(dot);
+    const float dot = lanes_sum<L>(w * d);
     wave_lds_sync();
-    for (int j = gl; j < k; j += L) {
-        const int e = slot(j);
-        if (e < 0) continue;
-        const float v = row[e], d = p.ds[t * k + j];
-        if (dense) {
-            g[e] = d;
-        } else {
-            const float w = weight(v) / total;
-            g[e] = p.scale * w * (p.sigmoid ? 1.f / (1.f + expf(v)) : 1.f) * (p.renorm ? d - dot : d);
-        }
-    }
+    if (e >= 0)
+        g[e] = DENSE ? d : p.scale * w * (p.sigmoid ? 1.f / (1.f + expf(v)) : 1.f) * (p.renorm ? d - dot : d);
     wave_lds_sync();
     if (!live) return;
     float* out = p.dlogits + t * E;
 #pragma unroll
     for (int q = 0; q < PER / 4; ++q) {
-        const int e = expert(4 * q);
-        float4 v = *(const float4*)(g + e);
-        if (dense) {
-            v.x = p.scale * x[4 * q] * inv * (v.x - dot);
-            v.y = p.scale * x[4 * q + 1] * inv * (v.y - dot);
-            v.z = p.scale * x[4 * q + 2] * inv * (v.z - dot);
-            v.w = p.scale * x[4 * q + 3] * inv * (v.w - dot);
+        const int c = expert(4 * q);
+        float4 f = *(const float4*)(g + c);
+        if constexpr (DENSE) {
+            f.x = p.scale * x[4 * q] * inv * (f.x - dot);
+            f.y = p.scale * x[4 * q + 1] * inv * (f.y - dot);
+            f.z = p.scale * x[4 * q + 2] * inv * (f.z - dot);
+            f.w = p.scale * x[4 * q + 3] * inv * (f.w - dot);
+            if (!whole) *(float4*)(g + c) = f;
         }
-        if (whole) {
-            if (e < E) *(float4*)(out + e) = v;
-        } else {
-            if (e < E) out[e] = v.x;
-            if (e + 1 < E) out[e + 1] = v.y;
-            if (e + 2 < E) out[e + 2] = v.z;
-            if (e + 3 < E) out[e + 3] = v.w;
-        }
+        if (whole && c < E) *(float4*)(out + c) = f;
+    }
+    if (!whole) {
+        wave_lds_sync();
+        for (int q = gl; q < E; q += L) out[q] = g[q];
     }
 }
 
@@ -771,7 +754,8 @@ int launch_route_scores_bwd(const float* logits, const float* bias, const int32_
     by_experts(E, k, [&](auto A, auto B) {
         constexpr int L = decltype(A)::value, PER = decltype(B)::value;
         const unsigned grid = (unsigned)(((int64_t)T + 256 / L - 1) / (256 / L));
-        route_scores_bwd_kernel<L, PER><<<grid, 256, 0, s>>>(p);
+        if (!sigmoid && !renorm) route_scores_bwd_kernel<L, PER, true><<<grid, 256, 0, s>>>(p);
+        else route_scores_bwd_kernel<L, PER, false><<<grid, 256, 0, s>>>(p);
     });
     return hipGetLastError() == hipSuccess ? 0 : -4;
 }
