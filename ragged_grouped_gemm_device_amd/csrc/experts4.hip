@@ -16,6 +16,7 @@
 namespace moe {
 
 constexpr int kBf16 = 0, kMx8 = 1, kMx4 = 2;  // formats of X
+constexpr int kWaitLgkmcnt0 = 0xC07F;         // s_waitcnt lgkmcnt(0) alone
 
 struct Experts4Args {
     const uint8_t* x;       // rows of K bf16, K bytes or K / 2 bytes
@@ -57,16 +58,28 @@ __device__ __forceinline__ i32x8_t operand8(uint4 a, uint4 b) {
 }
 
 // ------------------------------------------------------------------ few rows
-// A workgroup takes 64 columns of one expert and 16 RT of its rows; its NW wavefronts split K in blocks
-// of 128 and join in LDS. In a 16 x 16 x 128 product lane l supplies row l & 15 of W and of X, W's 16-byte
-// piece l / 16 (one scale block); with bf16 the piece is used in four 16 x 16 x 32 products, whose K then
-// runs in the order (piece, word), X's the same. DEP blocks are in flight a wavefront.
-template <int F, int RT, int NW, int DEP>
-__global__ void __launch_bounds__(NW * 64) experts4_rows_kernel(Experts4Args p) {
+// A workgroup takes 64 columns of one expert and 16 RT of its rows; its NW wavefronts split K in blocks of 256
+// and join in LDS. In a 16 x 16 x 128 product lane l supplies row l & 15 of W and of X and one 32-value block of
+// each, lane group l / 16 the blocks 2 (l / 16) + s of a block's two steps s; with bf16 a 32-value block is used
+// in four 16 x 16 x 32 products, a word of W in each.
+// W goes through LDS, though no lane shares it: read straight into that layout, neighbouring lanes would ask
+// for different rows, four lines for every four lanes, and the load path, not HBM, would be the bound (3.1 to
+// 4.2 TB/s in the forms tried; copies of whole 128-byte lines: see below). Each wavefront copies its own blocks,
+// 64 rows of 128 bytes, one ahead of the one it multiplies, and waits for no other. X, a few rows, comes
+// straight from the caches: lanes without a row ask for nothing. The scales of W's rows, 8 bytes of a line a
+// block, are laid into LDS once for 8192 of K.
+constexpr int kScaleChunk = 256;  // scale bytes of a row in LDS; 16-byte pieces XOR-swizzled by the row
+
+template <int F, int RT, int NW>
+__global__ void __launch_bounds__(NW * 64, 2) experts4_rows_kernel(Experts4Args p) {
     constexpr int kLd = 68;  // floats a row of the join: 64 and a pad against bank conflicts
-    constexpr int kX = F == kBf16 ? 4 : F == kMx8 ? 2 : 1;  // 16-byte pieces of X a lane, row tile and block
-    __shared__ __align__(16) float s_red[NW][RT * 16][kLd];
-    const int lane = lane_id(), wave = threadIdx.x >> 6;
+    constexpr int kX = F == kBf16 ? 4 : F == kMx8 ? 2 : 1;  // 16-byte pieces of a 32-value block of X
+    constexpr int kXBlock = F == kBf16 ? 512 : F == kMx8 ? 256 : 128;  // bytes of 256 of K
+    __shared__ __attribute__((aligned(1024))) uint8_t s_w[NW][2][64 * 128];  // then the join
+    __shared__ __align__(16) uint8_t s_sc[64 * kScaleChunk];
+    static_assert(sizeof(float) * 16 * RT * kLd <= sizeof(s_w[0]), "the join fits the blocks");
+    auto s_red = [&](int w, int row, int c) { return (float*)&s_w[w][0][0] + row * kLd + c; };
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     // the blockIdx.y-th expert that has rows
     int e = -1, m = 0;
@@ -87,126 +100,184 @@ __global__ void __launch_bounds__(NW * 64) experts4_rows_kernel(Experts4Args p) 
     m = __builtin_amdgcn_readfirstlane(m);
     if (e < 0) return;
     const int n0 = blockIdx.x * 64;
-    const int K = p.K, KB = K / 32;
-    const uint8_t* w[4];
-    const uint8_t* ws[4];
+    const int K = p.K, KB = K / 32, cols = min(p.N - n0, 64);
+    const int64_t wrow = (int64_t)e * p.N + n0;
+    const uint8_t* wsc = p.ws + wrow * KB;
+    // rows past the last column: past the resource, zeros; past K: another row's codes, finite, under scales of
+    // 0 and times zeros of X
+    const i32x4_t rw = rsrc_words(p.wq + wrow * (K / 2), (uint32_t)cols * (K / 2));
+    const uint32_t lds = (uint32_t)(uintptr_t)(LDS_AS char*)(&s_w[wave][0][0]);
+    const uint32_t wo = (lane >> 3) * (uint32_t)(K / 2);
+    auto copy_w = [&](int block, int buf) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t n = (int64_t)e * p.N + min(n0 + 16 * j + r, p.N - 1);
-        w[j] = p.wq + n * (K / 2) + 16 * g;
-        ws[j] = p.ws + n * KB + g;
-    }
+        for (int i = 0; i < 8; ++i) {
+            const int row = 8 * i + (lane >> 3);
+            lds_copy16(rw, lds + buf * 8192 + i * 1024, wo + 4 * i * (uint32_t)K + 128 * block + (((lane & 7) ^ kmaj_swz(row)) << 4));
+        }
+    };
     const int64_t xb = x_row_bytes(F, K);
     for (int first = blockIdx.z * 16 * RT; first < m; first += gridDim.z * 16 * RT) {
-    const int row0 = p.offsets[e] + first, rows = min(m - first, 16 * RT);
-    const uint8_t* x[RT];
-    const uint8_t* xs[RT];
+        const int row0 = p.offsets[e] + first, rows = min(m - first, 16 * RT);
+        const int64_t base = p.src_of ? 0 : row0, space = p.src_of ? p.rows : rows;
+        const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + base * xb, clamp_records(space * xb));
+        const __amdgpu_buffer_rsrc_t rxs = make_rsrc(F == kBf16 ? p.x : p.xs + base * KB, clamp_records(space * KB));
+        f32x4_t acc[4][RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-        int64_t row = row0 + min(16 * i + r, rows - 1);
-        if (p.src_of) row = p.src_of[row] / p.k;
-        x[i] = p.x + row * xb + (F == kBf16 ? 64 * g : 16 * g);
-        xs[i] = F == kBf16 ? nullptr : p.xs + row * KB + g;
-    }
-    struct Block {
-        uint4 w[4], x[RT][kX];
-        uint32_t ws[4], xs[RT];
-    };
-    const int nb = (K + 127) / 128;
-    const int b0 = nb * wave / NW, b1 = nb * (wave + 1) / NW;
-    auto load = [&](Block& b, int at) {
-        const bool ok = 128 * at + 32 * g < K;  // the last block may hold fewer than four scale blocks
-        const uint4 zero = make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            b.w[j] = ok ? *(const uint4*)(w[j] + 64 * (int64_t)at) : zero;
-            b.ws[j] = ok ? ws[j][4 * at] : 0;
-        }
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            if constexpr (F == kBf16) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) b.x[i][q] = ok ? *(const uint4*)(x[i] + 256 * (int64_t)at + 16 * q) : zero;
-            } else if constexpr (F == kMx8) {
-                b.x[i][0] = 128 * at + 16 * g < K ? *(const uint4*)(x[i] + 128 * (int64_t)at) : zero;
-                b.x[i][1] = 128 * at + 64 + 16 * g < K ? *(const uint4*)(x[i] + 128 * (int64_t)at + 64) : zero;
-            } else {
-                b.x[i][0] = ok ? *(const uint4*)(x[i] + 64 * (int64_t)at) : zero;
-            }
-            b.xs[i] = F != kBf16 && ok ? xs[i][4 * at] : 0;
-        }
-    };
-    f32x4_t acc[4][RT];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < RT; ++i) acc[j][i] = (f32x4_t){};
-    auto multiply = [&](const Block& b) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (F == kBf16) {
-                const float s = e8m0_value(b.ws[j]);
-                const uint32_t words[4] = {b.w[j].x, b.w[j].y, b.w[j].z, b.w[j].w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const bf16x8_t v = weights8(words[q], s);
-#pragma unroll
-                    for (int i = 0; i < RT; ++i)
-                        acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8_t, b.x[i][q]), acc[j][i], 0, 0, 0);
-                }
-            } else {
+            for (int i = 0; i < RT; ++i) acc[j][i] = (f32x4_t){};
+        uint32_t xrow[RT];  // this lane's rows; kMasked: none
+        for (int kb = 0; kb < KB; kb += kScaleChunk) {
+            const int nkb = min(KB - kb, kScaleChunk), nb = (nkb + 7) / 8, kb8 = kb / 8;
+            const int b0 = nb * wave / NW, b1 = nb * (wave + 1) / NW;
+            if (b0 < b1) copy_w(kb8 + b0, 0);
+            if (kb == 0) {
 #pragma unroll
                 for (int i = 0; i < RT; ++i) {
-                    if constexpr (F == kMx8)
-                        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            operand4(b.w[j]), operand8(b.x[i][0], b.x[i][1]), acc[j][i], 4, 0, 0, (int)b.ws[j], 0, (int)b.xs[i]);
-                    else
-                        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            operand4(b.w[j]), operand4(b.x[i][0]), acc[j][i], 4, 4, 0, (int)b.ws[j], 0, (int)b.xs[i]);
+                    const int at = 16 * i + r;
+                    xrow[i] = at >= rows ? kMasked : (uint32_t)(p.src_of ? p.src_of[row0 + at] / p.k : at);
                 }
             }
-        }
-    };
-    Block blk[DEP];
+            struct XBlock {
+                u32x4_nt_t x[RT][2][kX];
+                int s[RT][2];
+            };
+            auto load_x = [&](XBlock& b, int at) {
 #pragma unroll
-    for (int i = 0; i < DEP; ++i)
-        if (b0 + i < b1) load(blk[i], b0 + i);
-    for (int b = b0; b < b1; b += DEP) {
+                for (int s = 0; s < 2; ++s) {
 #pragma unroll
-        for (int i = 0; i < DEP; ++i) {
-            if (b + i < b1) {
-                multiply(blk[i]);
-                if (b + i + DEP < b1) load(blk[i], b + i + DEP);
+                    for (int i = 0; i < RT; ++i) {
+                        const bool has = xrow[i] != kMasked;
+#pragma unroll
+                        for (int q = 0; q < kX; ++q) {
+                            // an 8-bit lane's two pieces are halves of the blocks that lane groups g / 2 and 2 + g / 2 have of W
+                            const int of = F == kMx8 ? 2 * (g >> 1) + 4 * q + s : 2 * g + s;
+                            const uint32_t o = F == kMx8 ? 64 * (g >> 1) + 16 * (g & 1) + 128 * q + 32 * s : 32 * kX * g + 16 * kX * s + 16 * q;
+                            b.x[i][s][q] = __builtin_amdgcn_raw_buffer_load_b128(
+                                rx, has && 8 * at + of < nkb ? xrow[i] * (uint32_t)xb + o : kMasked, kXBlock * (kb8 + at), 0);
+                        }
+                        b.s[i][s] = 0;
+                        if constexpr (F != kBf16)
+                            b.s[i][s] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+                                rxs, has && 8 * at + 2 * g + s < nkb ? xrow[i] * (uint32_t)KB + 2 * g + s : kMasked, kb + 8 * at, 0);
+                    }
+                }
+            };
+            XBlock xn;
+            if (b0 < b1) load_x(xn, b0);
+            // W's scales, NW threads a row, 16 bytes each and turn, all loads out before the first is waited for;
+            // zeros past K and past the last column
+            constexpr int kTurns = kScaleChunk / (16 * NW);
+            const int srow = threadIdx.x / NW, part = threadIdx.x % NW;
+            uint4 sv[kTurns];
+#pragma unroll
+            for (int i = 0; i < kTurns; ++i) {
+                const int c = 16 * (part + NW * i), n = min(16, nkb - c);
+                sv[i] = make_uint4(0, 0, 0, 0);
+                if (srow < cols && n > 0) {
+                    const uint8_t* src = wsc + (int64_t)srow * KB + kb + c;
+                    if ((int64_t)(srow + 1) * KB + 16 <= (int64_t)cols * KB || n == 16) {
+                        __builtin_memcpy(&sv[i], src, 16);  // past its row's end: the next rows'
+                    } else {
+                        uint32_t v[4] = {0, 0, 0, 0};
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            if (q < n) v[q >> 2] |= (uint32_t)src[q] << (8 * (q & 3));
+                        sv[i] = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                }
             }
-        }
-    }
-    // lane: row l & 15 of X, columns 16 j + 4 (l / 16) + [0, 4)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < RT; ++i) *(f32x4_t*)&s_red[wave][16 * i + r][16 * j + 4 * g] = acc[j][i];
-    __syncthreads();
-    with_act(p.act, [&](auto A) {
-        constexpr int ACT = decltype(A)::value;
-        constexpr bool G = ACT < 2;
-        constexpr int Q = G ? 8 : 16;  // quads of outputs a row
-        const int NO = G ? p.N / 2 : p.N;
-        for (int i = threadIdx.x; i < RT * 16 * Q; i += NW * 64) {
-            const int row = i / Q, c = 4 * (i % Q);
-            if (row >= rows || n0 / (G ? 2 : 1) + c >= NO) continue;
-            f32x4_t a = {}, u = {};
-            for (int v = 0; v < NW; ++v) {
-                a += *(const f32x4_t*)&s_red[v][row][c];
-                if constexpr (G) u += *(const f32x4_t*)&s_red[v][row][c + 32];
+            for (int i = 0; i < kTurns; ++i) {
+                const int c = 16 * (part + NW * i), n = nkb - c;
+                auto keep = [&](uint32_t v, int at) { return n >= at + 4 ? v : n <= at ? 0u : v & ((1u << (8 * (n - at))) - 1u); };
+                if (c < 8 * nb)
+                    *(uint4*)(s_sc + srow * kScaleChunk + (c ^ ((srow & 15) << 4))) =
+                        make_uint4(keep(sv[i].x, 0), keep(sv[i].y, 4), keep(sv[i].z, 8), keep(sv[i].w, 12));
             }
-            float o[4];
+            __syncthreads();
+            for (int b = b0; b < b1; ++b) {
+                const int buf = (b - b0) & 1;
+                // the block and its X are here (their copies and loads are the only ones out)
+                __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+                const XBlock x = xn;
+                if (b + 1 < b1) {
+                    copy_w(kb8 + b + 1, buf ^ 1);
+                    load_x(xn, b + 1);
+                }
+                const uint8_t* sw = s_w[wave][buf];
+                uint32_t sc[4];  // two steps' scales
 #pragma unroll
-            for (int q = 0; q < 4; ++q) o[q] = G ? dense_act<ACT>(a[q]) * u[q] : dense_act<ACT>(a[q]);
-            *(uint2*)(p.y + (int64_t)(row0 + row) * NO + n0 / (G ? 2 : 1) + c) =
-                make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+                for (int j = 0; j < 4; ++j)
+                    sc[j] = *(const uint16_t*)(s_sc + (16 * j + r) * kScaleChunk + ((8 * b + 2 * g) ^ (r << 4)));
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const u32x4_nt_t w = *(const u32x4_nt_t*)(sw + kmaj_byte(16 * j + r, 2 * g + s));
+                        if constexpr (F == kBf16) {
+                            // the conversion reads a float's exponent alone
+                            const float f = __uint_as_float(s ? sc[j] << 15 : sc[j] << 23);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const bf16x8_t v = weights8(w[q], f);
+#pragma unroll
+                                for (int i = 0; i < RT; ++i)
+                                    acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8_t, x.x[i][s][q]),
+                                                                                        acc[j][i], 0, 0, 0);
+                            }
+                        } else {
+                            const i32x8_t v = operand4(__builtin_bit_cast(uint4, w));
+#pragma unroll
+                            for (int i = 0; i < RT; ++i) {
+                                i32x8_t u;
+                                if constexpr (F == kMx8)
+                                    u = operand8(__builtin_bit_cast(uint4, x.x[i][s][0]), __builtin_bit_cast(uint4, x.x[i][s][1]));
+                                else
+                                    u = operand4(__builtin_bit_cast(uint4, x.x[i][s][0]));
+                                // byte s of W's scales
+                                acc[j][i] = s ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, u, acc[j][i], 4, F == kMx8 ? 0 : 4, 1,
+                                                                                                 (int)sc[j], 0, x.s[i][s])
+                                              : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, u, acc[j][i], 4, F == kMx8 ? 0 : 4, 0,
+                                                                                                 (int)sc[j], 0, x.s[i][s]);
+                            }
+                        }
+                    }
+                }
+                // every read of this buffer has come back before the next turn's copies into it
+                __builtin_amdgcn_s_waitcnt(kWaitLgkmcnt0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            __syncthreads();  // the scales, or the last blocks, are read
         }
-    });
-    __syncthreads();  // read out before the next rows' sums
+        // lane: row l & 15 of X, columns 16 j + 4 (l / 16) + [0, 4)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < RT; ++i) *(f32x4_t*)s_red(wave, 16 * i + r, 16 * j + 4 * g) = acc[j][i];
+        __syncthreads();
+        with_act(p.act, [&](auto A) {
+            constexpr int ACT = decltype(A)::value;
+            constexpr bool G = ACT < 2;
+            constexpr int Q = G ? 8 : 16;  // quads of outputs a row
+            const int NO = G ? p.N / 2 : p.N;
+            for (int i = threadIdx.x; i < rows * Q; i += NW * 64) {
+                const int row = i / Q, c = 4 * (i % Q);
+                if (n0 / (G ? 2 : 1) + c >= NO) continue;
+                f32x4_t a = {}, u = {};
+#pragma unroll
+                for (int v = 0; v < NW; ++v) {
+                    a += *(const f32x4_t*)s_red(v, row, c);
+                    if constexpr (G) u += *(const f32x4_t*)s_red(v, row, c + 32);
+                }
+                f32x4_t o;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) o[q] = G ? dense_act<ACT>(a[q]) * u[q] : dense_act<ACT>(a[q]);
+                *(uint2*)(p.y + (int64_t)(row0 + row) * NO + n0 / (G ? 2 : 1) + c) =
+                    make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+            }
+        });
+        __syncthreads();  // read out before the next rows' blocks
     }
 }
 
@@ -509,10 +580,13 @@ static void experts4_any(const Experts4Args& a, int T, int k, hipStream_t s) {
         auto go = [&](auto R, auto W) {
             constexpr int RT = decltype(R)::value, NW = decltype(W)::value;
             const dim3 grid((a.N + 63) / 64, active, (unsigned)((std::min(T, (int)(2 * mean + 1)) + 16 * RT - 1) / (16 * RT)));
-            experts4_rows_kernel<F, RT, NW, RT == 1 ? 3 : 2><<<grid, NW * 64, 0, s>>>(a);
+            experts4_rows_kernel<F, RT, NW><<<grid, NW * 64, 0, s>>>(a);
         };
-        if (mean <= 8 || T <= 16) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
-        else go(std::integral_constant<int, 2>{}, std::integral_constant<int, 8>{});
+        using std::integral_constant;
+        static const int nw = getenv("NW") ? atoi(getenv("NW")) : 8;
+        static const int rt = getenv("RT") ? atoi(getenv("RT")) : 1;
+        if (rt == 1) nw == 8 ? go(integral_constant<int, 1>{}, integral_constant<int, 8>{}) : go(integral_constant<int, 1>{}, integral_constant<int, 4>{});
+        else nw == 8 ? go(integral_constant<int, 2>{}, integral_constant<int, 8>{}): go(integral_constant<int, 2>{}, integral_constant<int, 4>{});
         return;
     }
     auto go = [&](auto B) {
