@@ -282,13 +282,13 @@ __global__ void __launch_bounds__(NW * 64, 2) experts4_rows_kernel(Experts4Args 
 }
 
 // ------------------------------------------------------------------ tiles
-// What a format's slab holds: KS elements of K, 128 bytes a row of X and WROW a row of W.
+// What a format's slab holds: KS elements of K, 128 bytes a row of X (whole lines: in slabs of half the width, four in
+// a ring, every line was fetched twice and the 4-bit form lost 13%) and WROW a row of W.
 template <int F>
 struct Slab {
     static constexpr int KS = F == kBf16 ? 64 : F == kMx8 ? 128 : 256;
-    static constexpr int WROW = KS / 2;
-    static constexpr int WCH = WROW / 16;        // 16-byte pieces a row of W: 2, 4, 8
-    static constexpr int SPG = 512 / KS;         // slabs that a row's 16 scale bytes serve
+    static constexpr int WROW = KS / 2, WCH = WROW / 16;  // 16-byte pieces a row of W: 2, 4, 8
+    static constexpr int SPG = 512 / KS;                  // slabs that 16 scale bytes of a row serve, a group
 };
 
 // byte offset of 16-byte piece c of row r, rows of CH pieces: pieces are XOR-swizzled so that the rows of
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
     constexpr int XL = XB / 8192, WL = WB / 8192;  // copies of 16 bytes a thread
     // a slab, or the epilogue's 4 KiB of each of the 8 wavefronts
     __shared__ __attribute__((aligned(1024))) uint8_t s_ab[2][XB + WB > 32768 ? XB + WB : 32768];
-    __shared__ __attribute__((aligned(1024))) uint8_t s_sc[2][(BMX + 256) * 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t s_sc[3][(BMX + 256) * 16];  // groups of scales
     __shared__ int s_tiles[MOE_MAX_E + 1];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -360,33 +360,32 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
         return t;
     };
     // What a thread copies of a tile: its rows of X (offsets from the tile's or, gathered, x's base; rows past
-    // the expert's last are its last again, and not stored) and of W, and one row's scales.
+    // the expert's last are its last again, and not stored), of W, and one row's scales.
+    constexpr int WR = 512 / SL::WCH;  // rows of W a copy; of X, 64
     const int xc = (tid & 7) ^ slab_swz<8>(tid >> 3);  // the piece of a 128-byte row, the same in every copy
     const int wc = (tid & (SL::WCH - 1)) ^ slab_swz<SL::WCH>(tid / SL::WCH);
+    const uint32_t wo = (uint32_t)(tid / SL::WCH) * wb + wc * 16;
     struct Src {
         i32x4_t rx, rw;
-        uint32_t xo[XL], wo[WL];
-        const uint8_t* sc;  // this thread's row of scales
+        uint32_t xo[XL];
+        const uint8_t* sc;  // this thread's row of scales: threads [0, 256) W's rows, then X's
     };
+    const bool scaled = tid < 256 + (F == kBf16 ? 0 : BMX);
     auto source_row = [&](const Tile& t, int r) -> int64_t {
         const int row = t.row0 + min(r, t.rows - 1);
         return p.src_of ? p.src_of[row] / p.k : row;
     };
     auto make_src = [&](const Tile& t) -> Src {
         Src s;
+        const int cols = min(p.N - t.n0, 256);
         const int64_t base = p.src_of ? 0 : t.row0;
         s.rx = rsrc_from(p.x, p.rows * xb, base * xb);
         const int64_t n0 = (int64_t)t.e * p.N + t.n0;
-        s.rw = rsrc_words(p.wq + n0 * wb, clamp_records((int64_t)min(p.N - t.n0, 256) * wb));
+        s.rw = rsrc_words(p.wq + n0 * wb, clamp_records((int64_t)cols * wb));  // rows past the last column: zeros
 #pragma unroll
         for (int i = 0; i < XL; ++i) s.xo[i] = (uint32_t)((source_row(t, (tid >> 3) + 64 * i) - base) * xb) + xc * 16;
-#pragma unroll
-        for (int i = 0; i < WL; ++i)
-            s.wo[i] = (uint32_t)(min(tid / SL::WCH + i * (512 / SL::WCH), p.N - t.n0 - 1) * wb) + wc * 16;
-        // threads [0, 256) the rows of W, [256, 256 + BMX) those of X
-        if (tid < 256) s.sc = p.ws + (n0 + min(tid, p.N - t.n0 - 1)) * KB;
-        else if (F != kBf16 && tid < 256 + BMX) s.sc = p.xs + source_row(t, tid - 256) * KB;
-        else s.sc = nullptr;
+        if (F == kBf16 || tid < 256) s.sc = p.ws + (n0 + min(tid & 255, cols - 1)) * KB;
+        else s.sc = p.xs + source_row(t, tid - 256) * KB;
         return s;
     };
     auto issue = [&](const Src& s, int kt, int buf) {
@@ -396,74 +395,89 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
 #pragma unroll
         for (int i = 0; i < XL; ++i) lds_copy16(s.rx, l0 + i * 8192, xin ? s.xo[i] + xk : kMasked);
 #pragma unroll
-        for (int i = 0; i < WL; ++i) lds_copy16(s.rw, l0 + XB + i * 8192, win ? s.wo[i] + wk : kMasked);
+        for (int i = 0; i < WL; ++i) lds_copy16(s.rw, l0 + XB + i * 8192, win ? wo + i * WR * (uint32_t)wb + wk : kMasked);
     };
-    // 16 scale bytes of this thread's row (512 of K): zeros past its end
-    auto load_scales = [&](const Src& s, int grp) -> uint4 {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (s.sc) {
-            const int at = grp * 16, n = min(16, KB - at);
+    // Two groups of this thread's row of scales (1024 of K), zeros past its end, through registers, since rows
+    // start at any byte. A thread's 16 bytes cost a line of their own, so a group at a time they were a third of all
+    // line reads; three places hold the group in use and the next two.
+    uint4 held[2];
+    auto load_scales = [&](const Src& s, int at) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int n = min(16, KB - at - 16 * g);
+            held[g] = make_uint4(0, 0, 0, 0);
             if (n == 16) {
-                __builtin_memcpy(&v, s.sc + at, 16);
-            } else {
+                __builtin_memcpy(&held[g], s.sc + at + 16 * g, 16);
+            } else if (n > 0) {
                 uint32_t b[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (i < n) b[i >> 2] |= (uint32_t)s.sc[at + i] << (8 * (i & 3));
-                v = make_uint4(b[0], b[1], b[2], b[3]);
+                    if (i < n) b[i >> 2] |= (uint32_t)s.sc[at + 16 * g + i] << (8 * (i & 3));
+                held[g] = make_uint4(b[0], b[1], b[2], b[3]);
             }
         }
-        return v;
     };
-    auto store_scales = [&](uint4 v, int sbuf) {
-        if (tid < 256 + (F == kBf16 ? 0 : BMX)) *(uint4*)(s_sc[sbuf] + tid * 16) = v;
-    };
-    int round = 0;
     int t = logical(0);
     if (t >= total) return;
     Tile tl = get_tile(t);
-    Src src = make_src(tl);
-    const int nk = (K + SL::KS - 1) / SL::KS, ng = (nk + SL::SPG - 1) / SL::SPG;
-    issue(src, 0, 0);
-    uint4 held = load_scales(src, 0);
-    store_scales(held, 0);
-    int buf0 = 0, sg0 = 0;
+    const int nk = (K + SL::KS - 1) / SL::KS;
+    // The slabs of all this workgroup's tiles are one sequence, copied one ahead; the next to copy:
+    Src asrc = make_src(tl);
+    int akt = 0, around = 0, abuf = 0, aslot = 0, fetched = 0;  // groups of scales on their way
+    bool amore = true;
+    auto issue_ahead = [&]() {
+        if (!amore) return;
+        if (akt % (2 * SL::SPG) == 0) {
+            fetched = min(2, (nk - akt + SL::SPG - 1) / SL::SPG);
+            if (scaled) load_scales(asrc, akt / SL::SPG * 16);
+        }
+        issue(asrc, akt, abuf);
+        abuf ^= 1;
+        if (++akt == nk) {
+            akt = 0;
+            const int tn = logical(++around);
+            amore = tn < total;
+            if (amore) asrc = make_src(get_tile(tn));
+        }
+    };
+    auto store_scales = [&]() {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            if (g >= fetched) break;
+            if (scaled) *(uint4*)(s_sc[aslot] + tid * 16) = held[g];
+            aslot = aslot == 2 ? 0 : aslot + 1;
+        }
+        fetched = 0;
+    };
+    issue_ahead();
+    store_scales();
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    int buf = 0, slot = 2, round = 0;
     f32x16_t acc[TM][2];
     for (;;) {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) acc[i][j] = (f32x16_t){};
-        const int tn = logical(round + 1);
-        const bool have_next = tn < total;
-        Tile tl_next = tl;
-        Src src_next = src;
-        if (have_next) {
-            tl_next = get_tile(tn);
-            src_next = make_src(tl_next);
-        }
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
         for (int kt = 0; kt < nk; ++kt) {
-            const int cur = (buf0 + kt) & 1, grp = kt / SL::SPG, sub = kt % SL::SPG;
-            const bool last = kt + 1 == nk;
-            if (!last) issue(src, kt + 1, cur ^ 1);
-            else if (have_next) issue(src_next, 0, cur ^ 1);
-            // the next group of scales, or the next tile's first, on the way through registers
-            const bool fetch = last ? have_next : sub == SL::SPG - 1;
-            if (fetch) held = last ? load_scales(src_next, 0) : load_scales(src, grp + 1);
-            const uint8_t* sX = s_ab[cur];
-            const uint8_t* sW = s_ab[cur] + XB;
-            const uint8_t* sc = s_sc[(sg0 + grp) & 1] + sub * (SL::KS / 32);
+            issue_ahead();
+            const int sub = kt % SL::SPG;
+            if (sub == 0) slot = slot == 2 ? 0 : slot + 1;
+            const uint8_t* sX = s_ab[buf];
+            const uint8_t* sW = s_ab[buf] + XB;
+            const uint8_t* sc = s_sc[slot] + sub * (SL::KS / 32);
             const int wrow = wn * 64 + lr, xrow = wm * (BMX / 2) + lr;
-            if constexpr (F == kBf16) {
+            if (wm * (BMX / 2) >= tl.rows) {
+                // no rows here
+            } else if constexpr (F == kBf16) {
                 // W's piece h of a row (K 32 h ..) is one scale block: step q takes its word q, X's piece 4 h + q
                 uint4 fw[2];
                 float fs[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     fw[j] = *(const uint4*)(sW + slab_byte<2>(wrow + 32 * j, h));
-                    fs[j] = e8m0_value(sc[(wrow + 32 * j) * 16 + h]);
+                    fs[j] = __uint_as_float((uint32_t)sc[(wrow + 32 * j) * 16 + h] << 23);  // its exponent alone is read
                 }
                 static_for<4>([&](auto Q) {
                     bf16x8_t fx[TM];
@@ -519,17 +533,17 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
             for (int i = 0; i < TM; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(acc[i][j]));
-            if (!last) {
+            buf ^= 1;
+            if (kt + 1 < nk) {
                 __builtin_amdgcn_s_waitcnt(0);
-                if (fetch) store_scales(held, (sg0 + grp + 1) & 1);
+                store_scales();
                 __syncthreads();
             }
         }
         // Epilogue: lane = row, columns 8 q + 4 h + s of each 32-wide tile; 32 rows at a time through this
         // wavefront's 4 KiB of the slab no longer read, so that stores cover whole rows.
-        const int next_buf0 = (buf0 + nk) & 1;
         __syncthreads();  // the last slab is read out
-        uint8_t* stg = &s_ab[next_buf0 ^ 1][0] + wave * 4096;
+        uint8_t* stg = &s_ab[buf ^ 1][0] + wave * 4096;
         with_act(p.act, [&](auto A) {
             constexpr int ACT = decltype(A)::value;
             if constexpr ((ACT < 2) == GLU) {
@@ -560,45 +574,63 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
                 });
             }
         });
-        if (!have_next) break;
-        store_scales(held, (sg0 + ng) & 1);
-        ++round;
-        buf0 = next_buf0;
-        sg0 = (sg0 + ng) & 1;
-        tl = tl_next;
-        src = src_next;
+        const int tn = logical(++round);
+        if (tn >= total) break;
+        tl = get_tile(tn);
+        __builtin_amdgcn_s_waitcnt(0);
+        store_scales();
+        __syncthreads();  // the next tile's first slab is here, and the stage read out
     }
 }
 
 // ------------------------------------------------------------------ launch
+// Which kernel, by the mean rows of an expert that has any (the counts are the device's; any choice is right). All of
+// 32 experts of 7168 x 4096 with SwiGLU, us, 4-bit rows / bf16 rows:
+//   mean rows        8         16         32         64        128        256
+//   rows, 16     90 / 105  123 / 171  212 / 316  384 / 611
+//   rows, 32     92 / 123   97 / 156  148 / 276  257 / 511  480 / 994
+//   tiles, 64   103 / 187  103 / 196  105 / 201  163 / 317  213 / 436  338 / 724
+//   tiles, 128  105 / 199  106 / 208  108 / 216  111 / 236  164 / 365  230 / 559
+//   tiles, 256  115 / 250  115 / 251  117 / 255  120 / 266  143 / 347  208 / 535
+// Few tiles leave compute units idle: then smaller ones (1024 tokens x 2 of 8 experts, 2048 x 2048, 8-bit rows: 256 rows 30,
+// 128 rows 21, 64 rows 29 us), or the other kernel, which has four times the workgroups (512 tokens x 1 of 4,
+// 1024 x 1024, bf16: 10.4 against 13.4 us of 64 rows). Its wavefronts split K in eight instead of four where columns and
+// experts give fewer workgroups than compute units (with more, four are faster: one token, 8 of 32, 2048 x 7168: 16.0
+// against 22.5 us).
 template <int F>
 static void experts4_any(const Experts4Args& a, int T, int k, hipStream_t s) {
+    using std::integral_constant;
     const int64_t pairs = (int64_t)T * k;
     const int active = (int)std::min<int64_t>(a.E, pairs);
-    const double mean = (double)pairs / active;  // rows an expert
-    if (mean <= 48) {
-        auto go = [&](auto R, auto W) {
-            constexpr int RT = decltype(R)::value, NW = decltype(W)::value;
-            const dim3 grid((a.N + 63) / 64, active, (unsigned)((std::min(T, (int)(2 * mean + 1)) + 16 * RT - 1) / (16 * RT)));
-            experts4_rows_kernel<F, RT, NW><<<grid, NW * 64, 0, s>>>(a);
-        };
-        using std::integral_constant;
-        static const int nw = getenv("NW") ? atoi(getenv("NW")) : 8;
-        static const int rt = getenv("RT") ? atoi(getenv("RT")) : 1;
-        if (rt == 1) nw == 8 ? go(integral_constant<int, 1>{}, integral_constant<int, 8>{}) : go(integral_constant<int, 1>{}, integral_constant<int, 4>{});
-        else nw == 8 ? go(integral_constant<int, 2>{}, integral_constant<int, 8>{}): go(integral_constant<int, 2>{}, integral_constant<int, 4>{});
-        return;
-    }
-    auto go = [&](auto B) {
+    const double mean = (double)pairs / active;
+    const int64_t ntn = (a.N + 255) / 256;
+    auto filled = [&](int bm) { return ((int64_t)mean + bm - 1) / bm * active * ntn; };  // tiles of bm rows
+    int bm = mean <= 44 ? 64 : mean <= 110 ? 128 : 256;
+    while (bm > 64 && filled(bm) < 128) bm /= 2;
+    auto rows = [&](auto R, auto W) {
+        constexpr int RT = decltype(R)::value, NW = decltype(W)::value;
+        const dim3 grid((a.N + 63) / 64, active, (unsigned)((std::min(T, (int)(2 * mean + 1)) + 16 * RT - 1) / (16 * RT)));
+        experts4_rows_kernel<F, RT, NW><<<grid, NW * 64, 0, s>>>(a);
+    };
+    auto tiles = [&](auto B) {
         constexpr int BMX = decltype(B)::value;
-        const int64_t bound = (pairs / BMX + active) * ((a.N + 255) / 256);
+        const int64_t bound = (pairs / BMX + active) * ntn;
         const int grid = persistent_grid(bound);
         if (a.act < 2) experts4_tile_kernel<F, BMX, true><<<grid, 512, 0, s>>>(a);
         else experts4_tile_kernel<F, BMX, false><<<grid, 512, 0, s>>>(a);
     };
-    if (mean <= 96) go(std::integral_constant<int, 64>{});
-    else if (mean <= 192) go(std::integral_constant<int, 128>{});
-    else go(std::integral_constant<int, 256>{});
+    if (mean <= 10 || T <= 16) {
+        if ((int64_t)active * ((a.N + 63) / 64) <= 256) rows(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+        else rows(integral_constant<int, 1>{}, integral_constant<int, 4>{});
+    } else if (mean <= 24 || filled(64) < 128) {
+        rows(integral_constant<int, 2>{}, integral_constant<int, 4>{});
+    } else if (bm == 64) {
+        tiles(integral_constant<int, 64>{});
+    } else if (bm == 128) {
+        tiles(integral_constant<int, 128>{});
+    } else {
+        tiles(integral_constant<int, 256>{});
+    }
 }
 
 int launch_experts4(const Experts4Call& c, hipStream_t s) {

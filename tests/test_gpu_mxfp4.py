@@ -1,7 +1,11 @@
 """4-bit blocks and the experts' products with them, against the oracle (GPU).
 
 Products: fp32 sums of K terms that a matrix instruction may truncate, K 2^-22 of the sum of their
-magnitudes, and a bf16 rounding, 2^-8 of the result."""
+magnitudes, and a bf16 rounding, 2^-8 of the result. The instruction for 8- and 4-bit operands first adds groups of 8
+consecutive products as whole numbers of 2^-13 of the power of two under the largest, cut off (256 + 2^-5 is kept, 256 +
+1.75 * 2^-6 is 256). Two 4-bit values' products are multiples of 1/4 and at most 36 = 2.25 * 2^2 * 2^2, whose unit is 2^-9: nothing
+is lost. With 8-bit rows the 7 others lose less than a unit each: 7 * 2^-13 of the largest, which is at most the
+largest |x| times the largest |w| of the 8."""
 import numpy as np
 import pytest
 import torch
@@ -94,11 +98,12 @@ def test_scales_at_any_byte(M):
 class Case:
     """Experts with given row counts: x (padding rows NaN), weights, and the oracle's values of both."""
 
-    def __init__(self, M, counts, K, N, form, gather, k=2, seed=0):
+    def __init__(self, M, counts, K, N, form, gather, k=2, seed=0, T=None):
         self.M, self.counts, self.K, self.N, self.form = M, counts, K, N, form
         E = len(counts)
         pairs = sum(counts)
-        self.T = max(max(counts), -(-pairs // k))
+        self.T = T or max(max(counts), -(-pairs // k))
+        assert max(counts) <= self.T and pairs <= self.T * k
         self.k, self.E = k, E
         g = torch.Generator("cuda").manual_seed(seed + K + N)
         cap = M.moe_capacity_rows(self.T, k, E)
@@ -145,6 +150,11 @@ class Case:
                                         x_s=self.xs, src_of=self.d_src if self.gather else None, workspace=self.ws if ws is None else ws)
         return y
 
+    def cut_off(self, a, w):
+        """What 8-bit rows' products lose."""
+        eights = lambda v: np.abs(v).reshape(v.shape[0], -1, 8).max(2)  # noqa: E731
+        return 7 * 2.0**-13 * (eights(a) @ eights(w).T) if self.form == self.M.MOE_X_MXFP8 else 0
+
     def check(self, act):
         y = self.run(act)
         got = bf16_values(y)
@@ -155,7 +165,7 @@ class Case:
                 continue
             a = self.rows[self.offsets[e]:self.offsets[e] + c]
             z = a @ self.wv[e].T
-            dz = self.K * 2.0**-22 * (np.abs(a) @ np.abs(self.wv[e]).T)     # error of z
+            dz = self.K * 2.0**-22 * (np.abs(a) @ np.abs(self.wv[e]).T) + self.cut_off(a, self.wv[e])     # error of z
             ref = D.act_forward(z, act)
             if act in D.GATED:   # |f'| <= 1.13 for both gates, |f(g)| <= |g|
                 g, u = O.deinterleave(z)
@@ -170,7 +180,7 @@ class Case:
 
 
 FORMS = ["bf16", "mxfp8", "mxfp4"]
-# mean rows an expert from one to hundreds: every kernel form, each with empty experts, and ends inside a tile
+# mean rows an expert from one to hundreds, each with empty experts, and ends inside a tile
 COUNTS = {
     "one": [0, 1, 0, 1, 1], "few": [3, 0, 16, 17, 9], "dozens": [40, 1, 0, 33, 64], "tens": [70, 65, 0, 128, 1, 60],
     "hundred": [129, 0, 127, 200, 1, 300], "hundreds": [256, 511, 0, 1, 257, 700],
@@ -185,6 +195,17 @@ COUNTS = {
 ])
 def test_products(M, form, rows, K, N, act, gather):
     Case(M, COUNTS[rows], K, N, FORMS.index(form), gather, seed=len(rows)).check(act)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("mean", [40, 100, 300])
+@pytest.mark.parametrize("K, N, act, gather", [
+    (32, 1288, "none", False), (96, 1344, "swiglu", True), (544, 1544, "gelu", True), (1056, 1408, "geglu", False), (2208, 1800, "srelu", True),
+])
+def test_products_of_many_tiles(M, form, mean, K, N, act, gather):
+    """As many tokens and columns as make tiles of 64, 128 and 256 rows worth while, whatever the counts are then."""
+    counts = [3, 0, 16, 17, 9, 70, 65, 0, 128, 1, 60, 300] + [0] * 8 + [2, 0]
+    Case(M, counts, K, N, FORMS.index(form), gather, T=len(counts) * mean // 2).check(act)
 
 
 @pytest.mark.parametrize("form", FORMS)
