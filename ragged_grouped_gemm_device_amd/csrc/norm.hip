@@ -7,7 +7,9 @@
 //           ds = rho (g - h mean(g h)),  dw = sum over rows of dy h
 //
 // All are bound by HBM traffic: a row stays in registers between its statistics and its
-// output, so every tensor is read once and written once.
+// output, so every tensor is read once and written once. 32768 x 8192 with the residual: forward 370 us (5.8
+// TB/s), backward 428 (5.0); 16384 x 7168 of 8 experts with a full gate: forward 561 (5.0), backward 229 (5.1). A large
+// copy reaches 5.0.
 #include <algorithm>
 
 #include "block_common.hpp"
@@ -17,39 +19,40 @@ namespace moe {
 // TPR threads hold a row, NC chunks of 8 values each; a workgroup of 256 holds 256 / TPR rows.
 constexpr int kNormThreads = 256;
 
-// Sums of a row's TPR threads, the same in all of them. `part` is LDS of the workgroup that no
+// Sum over a row's TPR threads, the same in all of them. `part` is LDS of the workgroup that no
 // wavefront still reads: callers in a loop alternate two.
-template <int TPR, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*part)[N]) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) v[n] = lanes_sum<64>(v[n]);
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* part) {
+    v = lanes_sum<64>(v);
     if constexpr (TPR > 64) {
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-            for (int n = 0; n < N; ++n) part[wave][n] = v[n];
-        }
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
         __syncthreads();
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            float t = 0.f;
-#pragma unroll
-            for (int i = 0; i < TPR / 64; ++i) t += part[i][n];
-            v[n] = t;
-        }
+        v = (part[0] + part[1]) + (part[2] + part[3]);
     }
+    return v;
+}
+
+// sigmoid(v) and its derivative, e / (1 + e)^2 with e = exp(-|v|): no cancellation far from zero. The hardware's
+// reciprocal is good to one unit of fp32; a division by the rounding rules takes ten instructions, and with two a
+// value a full gate's backward pass was bound by arithmetic (16384 x 7168: 359 us, so 290).
+struct Sigmoid {
+    float value, slope;
+};
+__device__ __forceinline__ Sigmoid sigmoid_of(float v) {
+    const float e = __expf(-fabsf(v)), q = __builtin_amdgcn_rcpf(1.f + e);
+    return {v < 0.f ? e * q : q, e * q * q};
 }
 
 template <int TPR, int NC>
 __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormFwd p) {
-    __shared__ float s_part[4][1];
+    __shared__ float s_part[4];
     const int tid = threadIdx.x % TPR;
     const int64_t t = (int64_t)blockIdx.x * (kNormThreads / TPR) + threadIdx.x / TPR;
     const int cpr = p.d / 8;
     const bool live = t < p.T;
     const int64_t row = t * cpr;
     uint4 v[NC];
-    float ss[1] = {0.f};
+    float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = tid + TPR * i;
@@ -69,10 +72,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormFwd p) {
         float a[8];
         unpack8(v[i], a);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss[0] = fmaf(a[j], a[j], ss[0]);
+        for (int j = 0; j < 8; ++j) ss = fmaf(a[j], a[j], ss);
     }
-    row_sums<TPR>(ss, s_part);
-    const float r = rsqrtf(ss[0] / (float)p.d + p.eps);
+    const float r = rsqrtf(row_sum<TPR>(ss, s_part) / (float)p.d + p.eps);
     if (live && tid == 0 && p.rstd) p.rstd[t] = r;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -88,10 +90,11 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormFwd p) {
     }
 }
 
-// A workgroup walks rows and keeps its column sums of dw in registers; part: [parts, d].
+// A workgroup walks rows and keeps its column sums of dw in registers; part: [parts, d], joined by norm_join_kernel
+// (11 us for 1024 parts).
 template <int TPR, int NC>
 __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormBwd p, float* part) {
-    __shared__ float s_part[2][4][1];
+    __shared__ float s_part[2][4];
     const int tid = threadIdx.x % TPR;
     constexpr int RPB = kNormThreads / TPR;
     const int64_t me = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR, n = (int64_t)gridDim.x * RPB;
@@ -109,13 +112,11 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormBwd p, float
         const int64_t row = t * cpr;
         const float r = live ? p.rstd[t] : 0.f;
         uint4 x[NC], dy[NC];
-        float m[1] = {0.f};
+        float m = 0.f;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = tid + TPR * i;
-            const bool ok = live && c < cpr;
-            x[i] = dy[i] = make_uint4(0, 0, 0, 0);
-            if (ok) {
+            if (live && c < cpr) {
                 x[i] = ((const uint4*)p.x)[row + c];
                 dy[i] = ((const uint4*)p.dy)[row + c];
                 float a[8], b[8], w[8];
@@ -126,12 +127,11 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormBwd p, float
                 for (int j = 0; j < 8; ++j) {
                     const float bh = b[j] * (a[j] * r);
                     dw[i][j] += bh;
-                    m[0] = fmaf(bh, w[j], m[0]);
+                    m = fmaf(bh, w[j], m);
                 }
             }
         }
-        row_sums<TPR>(m, s_part[turn]);
-        const float mean = m[0] / (float)p.d;
+        const float mean = row_sum<TPR>(m, s_part[turn]) / (float)p.d;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = tid + TPR * i;
@@ -165,14 +165,14 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormBwd p, float
 
 template <int TPR, int NC>
 __global__ void __launch_bounds__(kNormThreads) post_norm_fwd_kernel(PostNormFwd p) {
-    __shared__ float s_part[4][1];
+    __shared__ float s_part[4];
     const int tid = threadIdx.x % TPR;
     const int64_t t = (int64_t)blockIdx.x * (kNormThreads / TPR) + threadIdx.x / TPR;
     const int cpr = p.d / 8;
     const bool live = t < p.T;
     const int64_t row = t * cpr;
     uint4 v[NC];
-    float ss[1] = {0.f};
+    float ss = 0.f;
     if (!p.row_of) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -212,16 +212,15 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_fwd_kernel(PostNormFwd
         float a[8];
         unpack8(v[i], a);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss[0] = fmaf(a[j], a[j], ss[0]);
+        for (int j = 0; j < 8; ++j) ss = fmaf(a[j], a[j], ss);
     }
-    row_sums<TPR>(ss, s_part);
-    const float r = rsqrtf(ss[0] / (float)p.d + p.eps);
+    const float r = rsqrtf(row_sum<TPR>(ss, s_part) / (float)p.d + p.eps);
     if (!live) return;
     if (tid == 0 && p.rstd) p.rstd[t] = r;
     float g1 = 1.f;
     if (p.gate && p.gate_cols == 1) {
         g1 = bf16_to_f32(p.gate[t]);
-        if (p.sigmoid) g1 = 1.f / (1.f + __expf(-g1));
+        if (p.sigmoid) g1 = sigmoid_of(g1).value;
     }
     g1 *= p.scale;
 #pragma unroll
@@ -238,7 +237,7 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_fwd_kernel(PostNormFwd
                 float g[8];
                 unpack8(((const uint4*)p.gate)[row + c], g);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) a[j] *= p.sigmoid ? 1.f / (1.f + __expf(-g[j])) : g[j];
+                for (int j = 0; j < 8; ++j) a[j] *= p.sigmoid ? sigmoid_of(g[j]).value : g[j];
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) a[j] += x[j];
@@ -247,10 +246,12 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_fwd_kernel(PostNormFwd
     }
 }
 
-// Through out = x + scale gate(c) (y rho w); the gradient of x is dout itself.
+// Through out = x + scale gate(c) (y rho w); the gradient of x is dout itself. A row's loads are all on their way before
+// the first is used, at two wavefronts a SIMD (16384 x 7168 with a full gate: 229 us, 5.1 TB/s; 290 with loads and
+// arithmetic mixed at three. norm_bwd_kernel, with less to hold, is better mixed, at four: 428 against 518 us).
 template <int TPR, int NC>
 __global__ void __launch_bounds__(kNormThreads) post_norm_bwd_kernel(PostNormBwd p, float* part) {
-    __shared__ float s_part[2][4][1];
+    __shared__ float s_part[2][4];
     const int tid = threadIdx.x % TPR;
     constexpr int RPB = kNormThreads / TPR;
     const int64_t me = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR, n = (int64_t)gridDim.x * RPB;
@@ -270,20 +271,26 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_bwd_kernel(PostNormBwd
         if (p.gate_cols == 1 && live) {
             g1 = bf16_to_f32(p.gate[t]);
             if (p.sigmoid) {
-                const float e = __expf(-fabsf(g1));
-                slope = e / ((1.f + e) * (1.f + e));
-                g1 = 1.f / (1.f + __expf(-g1));
+                const Sigmoid s = sigmoid_of(g1);
+                g1 = s.value, slope = s.slope;
             }
         }
         uint4 y[NC], dv[NC], gt[NC];
-        float m[1] = {0.f};  // sum of scale dout h w, times the gate where there is one a channel
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
+        for (int i = 0; i < NC; ++i) {  // all on their way before the first is used
             const int c = tid + TPR * i;
-            y[i] = dv[i] = gt[i] = make_uint4(0, 0, 0, 0);
             if (live && c < cpr) {
                 y[i] = ((const uint4*)p.y)[row + c];
                 dv[i] = ((const uint4*)p.dout)[row + c];
+                if (p.gate_cols > 1) gt[i] = ((const uint4*)p.gate)[row + c];
+            }
+        }
+        float u[NC][8];  // the gradient of h: scale dout w, times the gate where there is one a channel
+        float m = 0.f;   // sum of u h
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = tid + TPR * i;
+            if (live && c < cpr) {
                 float a[8], b[8], w[8];
                 unpack8(y[i], a);
                 unpack8(dv[i], b);
@@ -294,50 +301,36 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_bwd_kernel(PostNormBwd
                     b[j] *= p.scale;
                 }
                 if (p.gate_cols > 1) {
-                    gt[i] = ((const uint4*)p.gate)[row + c];
                     float g[8], dg[8];
                     unpack8(gt[i], g);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        float sl = 1.f;
-                        if (p.sigmoid) {
-                            const float e = __expf(-fabsf(g[j]));
-                            const float q = 1.f / (1.f + e);
-                            sl = e * q * q;
-                            g[j] = g[j] < 0.f ? e * q : q;
-                        }
-                        dg[j] = b[j] * a[j] * w[j] * sl;
-                        b[j] *= g[j];
+                        Sigmoid s = {g[j], 1.f};
+                        if (p.sigmoid) s = sigmoid_of(g[j]);
+                        dg[j] = b[j] * a[j] * w[j] * s.slope;
+                        b[j] *= s.value;
                     }
                     if (p.dgate) ((uint4*)p.dgate)[row + c] = pack8(dg);
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float bh = b[j] * a[j];
-                    dw[i][j] = fmaf(bh, g1, dw[i][j]);
-                    m[0] = fmaf(bh, w[j], m[0]);
+                    dw[i][j] = fmaf(b[j] * a[j], g1, dw[i][j]);
+                    u[i][j] = b[j] * w[j];
+                    m = fmaf(u[i][j], a[j], m);
                 }
             }
         }
-        row_sums<TPR>(m, s_part[turn]);
-        if (p.gate_cols == 1 && p.dgate && live && tid == 0) ((float*)p.dgate)[t] = m[0] * slope;
-        const float mean = m[0] * g1 / (float)p.d;
+        m = row_sum<TPR>(m, s_part[turn]);
+        if (p.gate_cols == 1 && p.dgate && live && tid == 0) ((float*)p.dgate)[t] = m * slope;
+        const float mean = m * g1 * r / (float)p.d;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = tid + TPR * i;
             if (live && c < cpr) {
-                float a[8], b[8], w[8];
+                float a[8];
                 unpack8(y[i], a);
-                unpack8(dv[i], b);
-                unpack8(((const uint4*)p.w)[c], w);
-                if (p.gate_cols > 1) {
-                    float g[8];
-                    unpack8(gt[i], g);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) b[j] *= p.sigmoid ? 1.f / (1.f + __expf(-g[j])) : g[j];
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) a[j] = r * (b[j] * p.scale * g1 * w[j] - a[j] * r * mean);
+                for (int j = 0; j < 8; ++j) a[j] = r * (u[i][j] * g1 - a[j] * mean);
                 ((uint4*)p.dy)[row + c] = pack8(a);
             }
         }
