@@ -302,6 +302,13 @@ __device__ __forceinline__ int slab_byte(int r, int c) {
     return r * CH * 16 + ((c ^ slab_swz<CH>(r)) << 4);
 }
 
+// Tiles of BMX rows x 256 columns, 2 x 4 wavefronts, each every other block of 32 rows and 64 columns; two slabs in LDS, the
+// next on its way by copies that pass no registers while one is multiplied. The slabs of all of a workgroup's tiles are
+// one sequence, so that the next tile's first arrives during the last's epilogue. 16384 tokens x 8 of 32 experts,
+// 7168 x 4096, SwiGLU: 4-bit rows 2040 us (3770 TFLOP/s), 8-bit 3230 (2380), bf16 6240 (1230, what a large library product
+// reaches). bf16 is bound by the matrix cores; in the others they are busy 45% (at 1.77 GHz, the power limit's clock):
+// multiplying alone took 1588 us of the 4-bit form, copying alone 1650, both not quite hidden behind each other.
+// Tried without gain: four slabs of 64-byte rows, 4 wavefronts of 128 x 128, copies sent half a slab ahead.
 template <int F, int BMX, bool GLU>
 __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
     using SL = Slab<F>;
@@ -311,32 +318,40 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
     // a slab, or the epilogue's 4 KiB of each of the 8 wavefronts
     __shared__ __attribute__((aligned(1024))) uint8_t s_ab[2][XB + WB > 32768 ? XB + WB : 32768];
     __shared__ __attribute__((aligned(1024))) uint8_t s_sc[3][(BMX + 256) * 16];  // groups of scales
-    __shared__ int s_tiles[MOE_MAX_E + 1];
+    __shared__ int s_tiles[MOE_MAX_E + 1];       // first large tile of every expert
+    __shared__ uint16_t s_small[MOE_MAX_E + 1];  // its small one, if the next expert's is another
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave >> 2, wn = wave & 3, h = lane >> 5, lr = lane & 31;
+    const int wm = wave >> 2, wn = wave & 3;
     const int K = p.K, KB = K / 32, ntn = (p.N + 255) / 256;
     const int64_t xb = x_row_bytes(F, K);
     const int wb = K / 2;
-    // first M tile of every expert
-    for (int i = tid; i < p.E; i += 512) s_tiles[i + 1] = (p.counts[i] + BMX - 1) / BMX;
-    if (tid == 0) s_tiles[0] = 0;
+    // Experts' last tiles with at most half the rows are small, and come after all others: workgroups take tiles in turn,
+    // the small ones level out what they have.
+    for (int e = tid; e < p.E; e += 512) {
+        const int c = p.counts[e], left = c % BMX;
+        s_tiles[e + 1] = c / BMX + (left > BMX / 2);
+        s_small[e + 1] = left > 0 && left <= BMX / 2;
+    }
+    if (tid == 0) s_tiles[0] = s_small[0] = 0;
     __syncthreads();
     if (tid < 64) {
-        int carry = 0;
+        int carry = 0, carry_small = 0;
         for (int base = 0; base < p.E; base += 64) {
-            int v = base + lane < p.E ? s_tiles[base + lane + 1] : 0;
+            const int e = base + lane + 1;
+            int v = e <= p.E ? s_tiles[e] : 0, u = e <= p.E ? s_small[e] : 0;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
-                const int u = __shfl_up(v, o, 64);
-                if (lane >= o) v += u;
+                const int v2 = __shfl_up(v, o, 64), u2 = __shfl_up(u, o, 64);
+                if (lane >= o) v += v2, u += u2;
             }
-            if (base + lane < p.E) s_tiles[base + lane + 1] = v + carry;
+            if (e <= p.E) s_tiles[e] = v + carry, s_small[e] = (uint16_t)(u + carry_small);
             carry += __shfl(v, 63, 64);
+            carry_small += __shfl(u, 63, 64);
         }
     }
     __syncthreads();
-    const int mtiles = s_tiles[p.E], total = mtiles * ntn;
+    const int large = s_tiles[p.E], mtiles = large + s_small[p.E], total = mtiles * ntn;
     const int nbl = gridDim.x;  // a multiple of 8
     auto logical = [&](int round) { return round * nbl + (blockIdx.x & 7) * (nbl >> 3) + (blockIdx.x >> 3); };
     struct Tile {
@@ -346,16 +361,20 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
         constexpr int G = 8;  // bands of 8 M tiles: an XCD's neighbouring tiles share operand panels in its L2
         const int band = tt / (G * ntn), within = tt - band * G * ntn, bm = min(G, mtiles - band * G);
         const int mt = band * G + within % bm;
-        int lo = 0, hi = p.E;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s_tiles[mid] <= mt) lo = mid; else hi = mid;
+        const bool small = mt >= large;
+        int e = 0;  // experts whose tiles all come before
+        for (int base = 0; base < p.E; base += 64) {
+            const int at = min(base + lane, p.E - 1) + 1;
+            const bool before = small ? s_small[at] <= mt - large : s_tiles[at] <= mt;
+            e += __popcll(__ballot(base + lane < p.E && before));
         }
         Tile t;
-        t.e = __builtin_amdgcn_readfirstlane(lo);
-        const int skip = __builtin_amdgcn_readfirstlane((mt - s_tiles[lo]) * BMX);
-        t.row0 = __builtin_amdgcn_readfirstlane(p.offsets[lo]) + skip;
-        t.rows = min(__builtin_amdgcn_readfirstlane(p.counts[lo]) - skip, BMX);
+        t.e = e;
+        // scalar loads: they wait for no copies
+        const int count = ((const __attribute__((address_space(4))) int32_t*)p.counts)[e];
+        const int skip = small ? count / BMX * BMX : __builtin_amdgcn_readfirstlane(mt - s_tiles[e]) * BMX;
+        t.row0 = ((const __attribute__((address_space(4))) int32_t*)p.offsets)[e] + skip;
+        t.rows = min(count - skip, BMX);
         t.n0 = __builtin_amdgcn_readfirstlane(within / bm * 256);
         return t;
     };
@@ -367,26 +386,36 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
     const uint32_t wo = (uint32_t)(tid / SL::WCH) * wb + wc * 16;
     struct Src {
         i32x4_t rx, rw;
-        uint32_t xo[XL];
-        const uint8_t* sc;  // this thread's row of scales: threads [0, 256) W's rows, then X's
+        uint32_t xo[XL];  // the rows, or the slots they come from; from the tile's first copies on, byte offsets
+        int row;          // of this thread's scales
+        const uint8_t* sc;  // threads [0, 256) W's rows, then X's
     };
     const bool scaled = tid < 256 + (F == kBf16 ? 0 : BMX);
-    auto source_row = [&](const Tile& t, int r) -> int64_t {
-        const int row = t.row0 + min(r, t.rows - 1);
-        return p.src_of ? p.src_of[row] / p.k : row;
-    };
-    auto make_src = [&](const Tile& t) -> Src {
+    auto begin = [&](const Tile& t) -> Src {
         Src s;
         const int cols = min(p.N - t.n0, 256);
         const int64_t base = p.src_of ? 0 : t.row0;
         s.rx = rsrc_from(p.x, p.rows * xb, base * xb);
         const int64_t n0 = (int64_t)t.e * p.N + t.n0;
         s.rw = rsrc_words(p.wq + n0 * wb, clamp_records((int64_t)cols * wb));  // rows past the last column: zeros
+        auto row_of = [&](int r) {
+            const int row = min(r, t.rows - 1);
+            return p.src_of ? p.src_of[t.row0 + row] : row;
+        };
 #pragma unroll
-        for (int i = 0; i < XL; ++i) s.xo[i] = (uint32_t)((source_row(t, (tid >> 3) + 64 * i) - base) * xb) + xc * 16;
-        if (F == kBf16 || tid < 256) s.sc = p.ws + (n0 + min(tid & 255, cols - 1)) * KB;
-        else s.sc = p.xs + source_row(t, tid - 256) * KB;
+        for (int i = 0; i < XL; ++i) s.xo[i] = (uint32_t)row_of((tid >> 3) + 64 * i);
+        s.row = min(tid & 255, cols - 1);
+        s.sc = p.ws + n0 * KB;
+        if (F != kBf16 && tid >= 256) {
+            s.row = row_of(tid - 256);
+            s.sc = p.xs + base * KB;
+        }
         return s;
+    };
+    auto resolve = [&](Src& s) {
+#pragma unroll
+        for (int i = 0; i < XL; ++i) s.xo[i] = (uint32_t)((p.src_of ? s.xo[i] / (uint32_t)p.k : s.xo[i]) * xb) + xc * 16;
+        s.sc += (int64_t)(F != kBf16 && tid >= 256 && p.src_of ? s.row / p.k : s.row) * KB;
     };
     auto issue = [&](const Src& s, int kt, int buf) {
         const uint32_t l0 = (uint32_t)(uintptr_t)(LDS_AS char*)(&s_ab[buf][0]) + wave * 1024;
@@ -422,11 +451,12 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
     Tile tl = get_tile(t);
     const int nk = (K + SL::KS - 1) / SL::KS;
     // The slabs of all this workgroup's tiles are one sequence, copied one ahead; the next to copy:
-    Src asrc = make_src(tl);
+    Src asrc = begin(tl);
     int akt = 0, around = 0, abuf = 0, aslot = 0, fetched = 0;  // groups of scales on their way
     bool amore = true;
     auto issue_ahead = [&]() {
         if (!amore) return;
+        if (akt == 0) resolve(asrc);  // a slab after its loads went out
         if (akt % (2 * SL::SPG) == 0) {
             fetched = min(2, (nk - akt + SL::SPG - 1) / SL::SPG);
             if (scaled) load_scales(asrc, akt / SL::SPG * 16);
@@ -437,7 +467,7 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
             akt = 0;
             const int tn = logical(++around);
             amore = tn < total;
-            if (amore) asrc = make_src(get_tile(tn));
+            if (amore) asrc = begin(get_tile(tn));
         }
     };
     auto store_scales = [&]() {
@@ -454,10 +484,16 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     int buf = 0, slot = 2, round = 0;
-    f32x16_t acc[TM][2];
-    for (;;) {
+    // A tile whose wavefronts have NB blocks of 32 rows each, then its epilogue.
+    auto tile = [&](auto Blocks) {
+        constexpr int NB = decltype(Blocks)::value;
+        int ln = lane;  // opaque, or the addresses of all forms are kept in registers over the tiles
+        asm volatile("" : "+v"(ln));
+        const int h = ln >> 5, lr = ln & 31;
+        const int wrow = wn * 64 + lr, xrow = wm * 32 + lr;  // a wavefront's blocks of 32 rows: every other one
+        f32x16_t acc[NB][2];
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) acc[i][j] = (f32x16_t){};
         for (int kt = 0; kt < nk; ++kt) {
@@ -467,10 +503,7 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
             const uint8_t* sX = s_ab[buf];
             const uint8_t* sW = s_ab[buf] + XB;
             const uint8_t* sc = s_sc[slot] + sub * (SL::KS / 32);
-            const int wrow = wn * 64 + lr, xrow = wm * (BMX / 2) + lr;
-            if (wm * (BMX / 2) >= tl.rows) {
-                // no rows here
-            } else if constexpr (F == kBf16) {
+            if constexpr (F == kBf16) {
                 // W's piece h of a row (K 32 h ..) is one scale block: step q takes its word q, X's piece 4 h + q
                 uint4 fw[2];
                 float fs[2];
@@ -479,46 +512,51 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
                     fw[j] = *(const uint4*)(sW + slab_byte<2>(wrow + 32 * j, h));
                     fs[j] = __uint_as_float((uint32_t)sc[(wrow + 32 * j) * 16 + h] << 23);  // its exponent alone is read
                 }
-                static_for<4>([&](auto Q) {
-                    bf16x8_t fx[TM];
+                bf16x8_t fx[2][NB];
+                auto load_x = [&](int q) {
 #pragma unroll
-                    for (int i = 0; i < TM; ++i) fx[i] = *(const bf16x8_t*)(sX + slab_byte<8>(xrow + 32 * i, 4 * h + Q));
+                    for (int i = 0; i < NB; ++i) fx[q & 1][i] = *(const bf16x8_t*)(sX + slab_byte<8>(xrow + 64 * i, 4 * h + q));
+                };
+                load_x(0);
+                static_for<4>([&](auto Q) {
+                    if constexpr (Q < 3) load_x(Q + 1);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t word = Q == 0 ? fw[j].x : Q == 1 ? fw[j].y : Q == 2 ? fw[j].z : fw[j].w;
                         const bf16x8_t v = weights8(word, fs[j]);
 #pragma unroll
-                        for (int i = 0; i < TM; ++i)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, fx[i], acc[i][j], 0, 0, 0);
+                        for (int i = 0; i < NB; ++i)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, fx[Q & 1][i], acc[i][j], 0, 0, 0);
                     }
+                    __builtin_amdgcn_sched_barrier(0);  // the compiler would put the loads off to their use
                 });
             } else {
                 constexpr int NS = SL::KS / 64;  // steps of 64
                 // scale words of 128 of K, shifted by the lane half's block: byte 0 serves the word's first
                 // step, byte 2 its second
-                uint32_t ss[2][NS / 2], sx[TM][NS / 2];
+                uint32_t ss[2][NS / 2], sx[NB][NS / 2];
 #pragma unroll
                 for (int u = 0; u < NS / 2; ++u) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) ss[j][u] = *(const uint32_t*)(sc + (wrow + 32 * j) * 16 + 4 * u) >> (8 * h);
 #pragma unroll
-                    for (int i = 0; i < TM; ++i) sx[i][u] = *(const uint32_t*)(sc + (256 + xrow + 32 * i) * 16 + 4 * u) >> (8 * h);
+                    for (int i = 0; i < NB; ++i) sx[i][u] = *(const uint32_t*)(sc + (256 + xrow + 64 * i) * 16 + 4 * u) >> (8 * h);
                 }
                 auto frag_w = [&](int j, int s) { return operand4(*(const uint4*)(sW + slab_byte<SL::WCH>(wrow + 32 * j, 2 * s + h))); };
                 auto frag_x = [&](int i, int s) {
-                    if constexpr (F == kMx4) return operand4(*(const uint4*)(sX + slab_byte<8>(xrow + 32 * i, 2 * s + h)));
-                    else return operand8(*(const uint4*)(sX + slab_byte<8>(xrow + 32 * i, 4 * s + h)),
-                                         *(const uint4*)(sX + slab_byte<8>(xrow + 32 * i, 4 * s + 2 + h)));
+                    if constexpr (F == kMx4) return operand4(*(const uint4*)(sX + slab_byte<8>(xrow + 64 * i, 2 * s + h)));
+                    else return operand8(*(const uint4*)(sX + slab_byte<8>(xrow + 64 * i, 4 * s + h)),
+                                         *(const uint4*)(sX + slab_byte<8>(xrow + 64 * i, 4 * s + 2 + h)));
                 };
-                i32x8_t fw[2], fx[TM];
+                i32x8_t fw[2], fx[NB];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) fw[j] = frag_w(j, 0);
 #pragma unroll
-                for (int i = 0; i < TM; ++i) fx[i] = frag_x(i, 0);
+                for (int i = 0; i < NB; ++i) fx[i] = frag_x(i, 0);
                 static_for<NS>([&](auto S) {
                     constexpr bool more = S + 1 < NS;
                     static_for<2>([&](auto J) {
-                        static_for<TM>([&](auto I) {
+                        static_for<NB>([&](auto I) {
                             acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                                 fw[J], fx[I], acc[I][J], 4, F == kMx4 ? 4 : 0, 2 * (S & 1), (int)ss[J][S / 2], 2 * (S & 1),
                                 (int)sx[I][S / 2]);
@@ -530,7 +568,7 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
             }
             // pinned before the wait below (the compiler would sink them past it)
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+            for (int i = 0; i < NB; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(acc[i][j]));
             buf ^= 1;
@@ -550,7 +588,7 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
                 const int NO = GLU ? p.N / 2 : p.N;
                 constexpr int PC = GLU ? 4 : 8;  // 16-byte pieces a row
                 const int col0 = (tl.n0 + wn * 64) / (GLU ? 2 : 1);
-                static_for<TM>([&](auto I) {
+                static_for<NB>([&](auto I) {
                     static_for<GLU ? 1 : 2>([&](auto J) {
                         static_for<4>([&](auto Q) {
                             float o[4];
@@ -565,15 +603,23 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
                     });
                     wave_lds_sync();
                     static_for<PC / 2>([&](auto It) {
-                        const int R = It * (64 / PC) + lane / PC, c = lane % PC;
+                        const int R = It * (64 / PC) + ln / PC, c = ln % PC;
                         const uint4 v = *(const uint4*)(stg + slab_byte<PC>(R, c));
-                        const int m = wm * (BMX / 2) + 32 * I + R, col = col0 + 8 * c;
+                        const int m = 64 * I + 32 * wm + R, col = col0 + 8 * c;
                         if (m < tl.rows && col < NO) st_nt16(p.y + (int64_t)(tl.row0 + m) * NO + col, v);
                     });
                     wave_lds_sync();
                 });
             }
         });
+    };
+    for (;;) {
+        // Experts' last tiles hold what is left of their rows: a quarter or half of the work where that is enough. Each
+        // form passes the same barriers, so the wavefronts' halves need not take the same one.
+        const int blocks = (tl.rows - 32 * wm + 63) / 64;
+        if (blocks <= 1) tile(std::integral_constant<int, 1>{});
+        else if (blocks <= 2 && TM > 2) tile(std::integral_constant<int, 2>{});
+        else tile(std::integral_constant<int, TM>{});
         const int tn = logical(++round);
         if (tn >= total) break;
         tl = get_tile(tn);
@@ -585,16 +631,16 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
 
 // ------------------------------------------------------------------ launch
 // Which kernel, by the mean rows of an expert that has any (the counts are the device's; any choice is right). All of
-// 32 experts of 7168 x 4096 with SwiGLU, us, 4-bit rows / bf16 rows:
-//   mean rows        8         16         32         64        128        256
-//   rows, 16     90 / 105  123 / 171  212 / 316  384 / 611
-//   rows, 32     92 / 123   97 / 156  148 / 276  257 / 511  480 / 994
-//   tiles, 64   103 / 187  103 / 196  105 / 201  163 / 317  213 / 436  338 / 724
-//   tiles, 128  105 / 199  106 / 208  108 / 216  111 / 236  164 / 365  230 / 559
-//   tiles, 256  115 / 250  115 / 251  117 / 255  120 / 266  143 / 347  208 / 535
-// Few tiles leave compute units idle: then smaller ones (1024 tokens x 2 of 8 experts, 2048 x 2048, 8-bit rows: 256 rows 30,
-// 128 rows 21, 64 rows 29 us), or the other kernel, which has four times the workgroups (512 tokens x 1 of 4,
-// 1024 x 1024, bf16: 10.4 against 13.4 us of 64 rows). Its wavefronts split K in eight instead of four where columns and
+// 32 experts of 7168 x 4096 with SwiGLU, us, 4-bit rows / bf16 rows (where the card's memory lands moves some by a tenth):
+//   mean rows        8         16         32         64         96        128        256
+//   rows, 16     90 / 105  123 / 172  213 / 318  385 / 612
+//   rows, 32     92 / 123   98 / 156  149 / 277  257 / 513
+//   tiles, 64   105 / 195  104 / 203  107 / 211  175 / 357  188 / 371  230 / 481  353 / 778
+//   tiles, 128  111 / 248  112 / 257  113 / 264  117 / 263  121 / 253  182 / 393  246 / 580
+//   tiles, 256  111 / 227  111 / 234  113 / 242  116 / 251  121 / 267  128 / 309  203 / 497
+// Few tiles leave compute units idle: then smaller ones (1024 tokens x 2 of 8 experts, 2048 x 2048, 8-bit rows: 256 rows 31,
+// 128 rows 22, 64 rows 30 us), or the other kernel, which has four times the workgroups (512 tokens x 1 of 4,
+// 1024 x 1024, bf16: 10.2 against 14.2 us of 64 rows). Its wavefronts split K in eight instead of four where columns and
 // experts give fewer workgroups than compute units (with more, four are faster: one token, 8 of 32, 2048 x 7168: 16.0
 // against 22.5 us).
 template <int F>
