@@ -302,19 +302,26 @@ __device__ __forceinline__ int slab_byte(int r, int c) {
     return r * CH * 16 + ((c ^ slab_swz<CH>(r)) << 4);
 }
 
+// s_waitcnt vmcnt(n) alone
+constexpr int wait_vmcnt(int n) { return 0x0F70 | (n & 15) | (n >> 4 << 14); }
+
 // Tiles of BMX rows x 256 columns, 2 x 4 wavefronts, each every other block of 32 rows and 64 columns; two slabs in LDS, the
 // next on its way by copies that pass no registers while one is multiplied. The slabs of all of a workgroup's tiles are
 // one sequence, so that the next tile's first arrives during the last's epilogue. 16384 tokens x 8 of 32 experts,
-// 7168 x 4096, SwiGLU: 4-bit rows 2040 us (3770 TFLOP/s), 8-bit 3230 (2380), bf16 6240 (1230, what a large library product
-// reaches). bf16 is bound by the matrix cores; in the others they are busy 45% (at 1.77 GHz, the power limit's clock):
-// multiplying alone took 1588 us of the 4-bit form, copying alone 1650, both not quite hidden behind each other.
-// Tried without gain: four slabs of 64-byte rows, 4 wavefronts of 128 x 128, copies sent half a slab ahead.
+// 7168 x 4096, SwiGLU: 4-bit rows 1990 to 2060 us (3800 TFLOP/s), 8-bit 3130 to 3230 (2430), bf16 5980 to 6240 (1260, as a
+// large library product). bf16 is bound by the matrix cores; in the 4-bit form they are busy 46% at the 1.8 GHz that the
+// power limit leaves: multiplying alone took 1588 us, copying alone 1650, neither quite hidden behind the other.
+// Tiles of fewer rows wait for W from HBM: there (kEarly) a slab's copies go out before the one they replace is multiplied to
+// its end, as soon as all wavefronts have its last fragments: a barrier more a slab, and 7 to 11% less time (32 rows
+// an expert, bf16: 210 -> 190 us, 4-bit 107 -> 98); with 256 rows it brought nothing (-1% to +3%).
+// Tried without gain: four slabs of 64-byte rows, 4 wavefronts of 128 x 128.
 template <int F, int BMX, bool GLU>
 __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
     using SL = Slab<F>;
     constexpr int TM = BMX / 64;        // 32-row tiles a wavefront (2 x 4 wavefronts)
     constexpr int XB = BMX * 128, WB = 256 * SL::WROW;
     constexpr int XL = XB / 8192, WL = WB / 8192;  // copies of 16 bytes a thread
+    constexpr bool kEarly = BMX < 256;  // copies go out before the slab they replace is multiplied to its end
     // a slab, or the epilogue's 4 KiB of each of the 8 wavefronts
     __shared__ __attribute__((aligned(1024))) uint8_t s_ab[2][XB + WB > 32768 ? XB + WB : 32768];
     __shared__ __attribute__((aligned(1024))) uint8_t s_sc[3][(BMX + 256) * 16];  // groups of scales
@@ -450,24 +457,24 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
     if (t >= total) return;
     Tile tl = get_tile(t);
     const int nk = (K + SL::KS - 1) / SL::KS;
-    // The slabs of all this workgroup's tiles are one sequence, copied one ahead; the next to copy:
+    // The slabs of all this workgroup's tiles are one sequence; the next to copy:
     Src asrc = begin(tl);
     int akt = 0, around = 0, abuf = 0, aslot = 0, fetched = 0;  // groups of scales on their way
     bool amore = true;
-    auto issue_ahead = [&]() {
+    auto advance = [&]() {
+        akt = 0;
+        const int tn = logical(++around);
+        amore = tn < total;
+        if (amore) asrc = begin(get_tile(tn));
+    };
+    // its scales, where it begins a pair of groups
+    auto fetch_scales = [&]() {
+        if (kEarly && akt == nk) advance();
         if (!amore) return;
-        if (akt == 0) resolve(asrc);  // a slab after its loads went out
+        if (akt == 0) resolve(asrc);
         if (akt % (2 * SL::SPG) == 0) {
             fetched = min(2, (nk - akt + SL::SPG - 1) / SL::SPG);
             if (scaled) load_scales(asrc, akt / SL::SPG * 16);
-        }
-        issue(asrc, akt, abuf);
-        abuf ^= 1;
-        if (++akt == nk) {
-            akt = 0;
-            const int tn = logical(++around);
-            amore = tn < total;
-            if (amore) asrc = begin(get_tile(tn));
         }
     };
     auto store_scales = [&]() {
@@ -479,10 +486,26 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
         }
         fetched = 0;
     };
-    issue_ahead();
-    store_scales();
+    auto copy_slab = [&]() {
+        if (!amore) return;
+        issue(asrc, akt, abuf);
+        abuf ^= 1;
+        ++akt;
+        if (!kEarly && akt == nk) advance();  // its rows' loads have a slab's time
+    };
+    auto barrier = [&]() {  // no wait for copies in it
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < 1 + kEarly; ++i) {
+        fetch_scales();
+        store_scales();
+        copy_slab();
+    }
     __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
+    barrier();
     int buf = 0, slot = 2, round = 0;
     // A tile whose wavefronts have NB blocks of 32 rows each, then its epilogue.
     auto tile = [&](auto Blocks) {
@@ -497,12 +520,22 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) acc[i][j] = (f32x16_t){};
         for (int kt = 0; kt < nk; ++kt) {
-            issue_ahead();
+            // sent early, copies take the place of this slab, the tile's last one excepted: the epilogue's stage
+            if (!kEarly || kt + 1 < nk) fetch_scales();
+            const bool early = kEarly && kt + 1 < nk && amore;
+            if (!kEarly) copy_slab();
             const int sub = kt % SL::SPG;
             if (sub == 0) slot = slot == 2 ? 0 : slot + 1;
             const uint8_t* sX = s_ab[buf];
             const uint8_t* sW = s_ab[buf] + XB;
             const uint8_t* sc = s_sc[slot] + sub * (SL::KS / 32);
+            auto release = [&]() {  // once all have read their last fragments
+                if (!early) return;
+                __builtin_amdgcn_s_waitcnt(kWaitLgkmcnt0);
+                barrier();
+                store_scales();
+                copy_slab();
+            };
             if constexpr (F == kBf16) {
                 // W's piece h of a row (K 32 h ..) is one scale block: step q takes its word q, X's piece 4 h + q
                 uint4 fw[2];
@@ -520,6 +553,7 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
                 load_x(0);
                 static_for<4>([&](auto Q) {
                     if constexpr (Q < 3) load_x(Q + 1);
+                    else if constexpr (kEarly) release();
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t word = Q == 0 ? fw[j].x : Q == 1 ? fw[j].y : Q == 2 ? fw[j].z : fw[j].w;
@@ -542,28 +576,35 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
 #pragma unroll
                     for (int i = 0; i < NB; ++i) sx[i][u] = *(const uint32_t*)(sc + (256 + xrow + 64 * i) * 16 + 4 * u) >> (8 * h);
                 }
-                auto frag_w = [&](int j, int s) { return operand4(*(const uint4*)(sW + slab_byte<SL::WCH>(wrow + 32 * j, 2 * s + h))); };
+                auto frag_w = [&](int j, int s) { return *(const uint4*)(sW + slab_byte<SL::WCH>(wrow + 32 * j, 2 * s + h)); };
                 auto frag_x = [&](int i, int s) {
-                    if constexpr (F == kMx4) return operand4(*(const uint4*)(sX + slab_byte<8>(xrow + 64 * i, 2 * s + h)));
+                    if constexpr (F == kMx4) return *(const uint4*)(sX + slab_byte<8>(xrow + 64 * i, 2 * s + h));
                     else return operand8(*(const uint4*)(sX + slab_byte<8>(xrow + 64 * i, 4 * s + h)),
                                          *(const uint4*)(sX + slab_byte<8>(xrow + 64 * i, 4 * s + 2 + h)));
                 };
-                i32x8_t fw[2], fx[NB];
+                uint4 fw[2];
+                std::conditional_t<F == kMx4, uint4, i32x8_t> fx[NB];
+                auto operand = [](auto v) {
+                    if constexpr (F == kMx4) return operand4(v);
+                    else return v;
+                };
 #pragma unroll
                 for (int j = 0; j < 2; ++j) fw[j] = frag_w(j, 0);
 #pragma unroll
                 for (int i = 0; i < NB; ++i) fx[i] = frag_x(i, 0);
                 static_for<NS>([&](auto S) {
                     constexpr bool more = S + 1 < NS;
+                    if constexpr (!more && kEarly) release();
                     static_for<2>([&](auto J) {
                         static_for<NB>([&](auto I) {
                             acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                fw[J], fx[I], acc[I][J], 4, F == kMx4 ? 4 : 0, 2 * (S & 1), (int)ss[J][S / 2], 2 * (S & 1),
+                                operand4(fw[J]), operand(fx[I]), acc[I][J], 4, F == kMx4 ? 4 : 0, 2 * (S & 1), (int)ss[J][S / 2], 2 * (S & 1),
                                 (int)sx[I][S / 2]);
                             if constexpr (more && J == 1) fx[I] = frag_x(I, S + 1);
                         });
                         if constexpr (more) fw[J] = frag_w(J, S + 1);
                     });
+                    __builtin_amdgcn_sched_barrier(0);  // or the sums move to other registers at the release
                 });
             }
             // pinned before the wait below (the compiler would sink them past it)
@@ -573,9 +614,12 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
                 for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(acc[i][j]));
             buf ^= 1;
             if (kt + 1 < nk) {
-                __builtin_amdgcn_s_waitcnt(0);
-                store_scales();
-                __syncthreads();
+                // the next slab is here; one sent early may still be on its way
+                if (early) __builtin_amdgcn_s_waitcnt(wait_vmcnt(XL + WL));
+                else __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+                if (!kEarly) store_scales();
+                __builtin_amdgcn_s_waitcnt(kWaitLgkmcnt0);
+                barrier();
             }
         }
         // Epilogue: lane = row, columns 8 q + 4 h + s of each 32-wide tile; 32 rows at a time through this
@@ -623,24 +667,32 @@ __global__ void __launch_bounds__(512, 1) experts4_tile_kernel(Experts4Args p) {
         const int tn = logical(++round);
         if (tn >= total) break;
         tl = get_tile(tn);
+        if (kEarly) fetch_scales();
         __builtin_amdgcn_s_waitcnt(0);
-        store_scales();
+        if (!kEarly) store_scales();
         __syncthreads();  // the next tile's first slab is here, and the stage read out
+        if (kEarly) {
+            store_scales();
+            copy_slab();
+            __builtin_amdgcn_s_waitcnt(kWaitLgkmcnt0);
+            barrier();
+        }
     }
 }
 
 // ------------------------------------------------------------------ launch
 // Which kernel, by the mean rows of an expert that has any (the counts are the device's; any choice is right). All of
 // 32 experts of 7168 x 4096 with SwiGLU, us, 4-bit rows / bf16 rows (where the card's memory lands moves some by a tenth):
-//   mean rows        8         16         32         64         96        128        256
-//   rows, 16     90 / 105  123 / 172  213 / 318  385 / 612
-//   rows, 32     92 / 123   98 / 156  149 / 277  257 / 513
-//   tiles, 64   105 / 195  104 / 203  107 / 211  175 / 357  188 / 371  230 / 481  353 / 778
-//   tiles, 128  111 / 248  112 / 257  113 / 264  117 / 263  121 / 253  182 / 393  246 / 580
-//   tiles, 256  111 / 227  111 / 234  113 / 242  116 / 251  121 / 267  128 / 309  203 / 497
+//   mean rows        8         16         32         48         64         96        128        256
+//   rows, 16     90 / 105  123 / 172  213 / 318  298 / 463
+//   rows, 32     92 / 123   97 / 156  149 / 277  203 / 392  257 / 514
+//   tiles, 64    96 / 186   96 / 190   98 / 189  100 / 195  159 / 325  161 / 349  198 / 448  300 / 717
+//   tiles, 128  105 / 217  106 / 225  106 / 232  108 / 237  112 / 237  114 / 246  168 / 360  234 / 540
+//   tiles, 256  111 / 226  111 / 235  112 / 243  114 / 247  116 / 249  121 / 263  130 / 296  205 / 480
+// (64 rows stop paying where most experts have more.)
 // Few tiles leave compute units idle: then smaller ones (1024 tokens x 2 of 8 experts, 2048 x 2048, 8-bit rows: 256 rows 31,
-// 128 rows 22, 64 rows 30 us), or the other kernel, which has four times the workgroups (512 tokens x 1 of 4,
-// 1024 x 1024, bf16: 10.2 against 14.2 us of 64 rows). Its wavefronts split K in eight instead of four where columns and
+// 128 rows 25, 64 rows 31 us), or the other kernel, which has four times the workgroups (512 tokens x 1 of 4,
+// 1024 x 1024, bf16: 10.3 against 15.0 us of 64 rows). Its wavefronts split K in eight instead of four where columns and
 // experts give fewer workgroups than compute units (with more, four are faster: one token, 8 of 32, 2048 x 7168: 16.0
 // against 22.5 us).
 template <int F>
@@ -651,7 +703,7 @@ static void experts4_any(const Experts4Args& a, int T, int k, hipStream_t s) {
     const double mean = (double)pairs / active;
     const int64_t ntn = (a.N + 255) / 256;
     auto filled = [&](int bm) { return ((int64_t)mean + bm - 1) / bm * active * ntn; };  // tiles of bm rows
-    int bm = mean <= 44 ? 64 : mean <= 110 ? 128 : 256;
+    int bm = mean <= 50 ? 64 : mean <= 110 ? 128 : 256;
     while (bm > 64 && filled(bm) < 128) bm /= 2;
     auto rows = [&](auto R, auto W) {
         constexpr int RT = decltype(R)::value, NW = decltype(W)::value;
