@@ -7,7 +7,8 @@
 // gfx950's packed conversion divides by the scale and rounds so for every bf16 value (checked over
 // all of them).
 //
-// Both directions are bound by HBM: 2 bytes in and 17/32 out a value, or the reverse.
+// Both directions are bound by HBM: 2 bytes in and 17/32 out a value, or the reverse. 8 x 7168 x 4096 values: by
+// columns 122 us (4.9 TB/s), restored 101 (5.9); 1021 x 2880: 3.2 us by rows, 3.4 restored, a launch's time.
 #include <algorithm>
 
 #include "block_common.hpp"
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(256) quant_mxfp4_col_kernel(const uint16_t* __
 }
 
 // 8 values a thread: 4 bytes in, one 16-byte store. NT: past the caches, for outputs that these would not
-// hold for their reader.
+// hold for their reader (from kDenseStreamBytes, as the 8-bit blocks').
 template <bool NT>
 __global__ void __launch_bounds__(256) dequant_mxfp4_kernel(const uint32_t* __restrict__ q,
                                                             const uint8_t* __restrict__ s, int64_t n8,

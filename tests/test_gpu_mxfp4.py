@@ -209,6 +209,16 @@ def test_products_of_many_tiles(M, form, mean, K, N, act, gather):
 
 
 @pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("counts, K, N, act", [
+    ([3, 0, 1, 7], 9248, 136, "none"),               # few columns: K in eighths, and past the scales that LDS holds
+    ([2, 0, 5, 1] * 5 + [9], 9248, 1088, "swiglu"),  # many: in quarters
+    ([17, 0, 33, 9, 20], 9248, 320, "gelu"),         # 32 rows at a time
+])
+def test_few_rows_of_a_long_width(M, form, counts, K, N, act):
+    Case(M, counts, K, N, FORMS.index(form), True).check(act)
+
+
+@pytest.mark.parametrize("form", FORMS)
 def test_many_tiles_a_workgroup(M, form):
     """More tiles than compute units, so that workgroups walk on; widths that end inside a tile."""
     c = Case(M, [300, 257, 1, 0, 1000, 640, 30], 192, 13 * 256 + 8, FORMS.index(form), True)
