@@ -179,3 +179,30 @@ def test_the_same_bits_every_time_and_in_a_graph(M):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, (dx, dw, dg))), rep
+
+
+@pytest.mark.parametrize("cols", [1, "d"])
+def test_gates_far_from_zero(M, cols):
+    """A sigmoid's tails: its slope is e / (1 + e)^2 with e = exp(-|g|), whose argument's rounding costs |g| 2^-24 of it; what
+    lies below fp32's normal range, 2^-126, may be 0."""
+    far = [-float("inf"), -100.0, -85.0, -40.0, -17.0, -9.0, 0.0, 9.0, 17.0, 40.0, 85.0, 100.0, float("inf")]
+    T, d = len(far), 512
+    cols = d if cols == "d" else cols
+    y, x, w, do = rand(T, d), torch.zeros(T, d, dtype=BF, device="cuda"), rand(d, std=0.3, mean=1.0, seed=2), rand(T, d, seed=3)
+    gate = torch.tensor(far, dtype=BF, device="cuda").view(T, 1).expand(T, cols).contiguous()
+    out, rstd = full(T, d), full(T, t=F32)
+    M.moe_post_norm_fwd(y, x, w, out, rstd, EPS, gate=gate, gate_act=M.MOE_GATE_SIGMOID)
+    yv, wv, dv, gv = bf16_values(y), bf16_values(w), bf16_values(do), bf16_values(gate)
+    v = B.norm(yv, wv, EPS)[0]
+    e = np.exp(-np.abs(gv))
+    value, slope = np.where(gv < 0, e, 1.0) / (1 + e), e / (1 + e)**2
+    arg = np.where(np.isfinite(gv), np.abs(gv), 0.0) * 2.0**-23 + 8 * 2.0**-24
+    close(out, v * value, (HALF + SUM + arg) * np.abs(v * value) + 2.0**-125 * np.abs(v), "out")
+    dy, dgate = full(T, d), full(T, cols, t=F32 if cols == 1 else BF)
+    M.moe_post_norm_bwd(do, y, w, rstd, dy, gate=gate, dgate=dgate, gate_act=M.MOE_GATE_SIGMOID)
+    if cols == 1:
+        close(dgate, (dv * v).sum(1, keepdims=True) * slope,
+              (2 * SUM + arg) * np.abs(dv * v).sum(1, keepdims=True) * slope + 2.0**-125 * np.abs(dv * v).sum(1, keepdims=True), "dgate")
+    else:
+        close(dgate, dv * v * slope, (HALF + SUM + arg) * np.abs(dv * v * slope) + 2.0**-125 * (1 + np.abs(dv * v)), "dgate")
+    assert not dy.isnan().any()
