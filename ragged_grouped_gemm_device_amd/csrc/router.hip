@@ -115,11 +115,12 @@ __device__ __forceinline__ int lanes_scan(int v, int gl) {
 }
 
 // exp(a - b) with the rounding of the difference made good: it would be an error of up to 2^-24 |a - b| of
-// the result.
+// the result. Below -104 the result is 0 in fp32, and there the difference itself may overflow (its rounding is
+// then a NaN).
 __device__ __forceinline__ float exp_of_difference(float a, float b) {
     const float d = a - b, bb = d - a;
     const float e = (a - (d - bb)) - (b + bb);
-    return expf(d) * (1.f + e);
+    return d > -104.f ? expf(d) * (1.f + e) : 0.f;
 }
 
 // A chosen expert's score from its logit. Renormalised weights take it over exp(shift), shift the best chosen
