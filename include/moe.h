@@ -603,7 +603,8 @@ int moe_route_scores(const float* logits, const float* bias, const moe_routing* 
  * moe_route_scores_bwd -- gradient w.r.t. the logits given ds = dL/dtopk_w, for
  *   the experts chosen (topk_idx as moe_route_scores wrote it; the choice itself
  *   and the bias have none). An expert that weighs 0 for want of a finite logit
- *   or bias has none either. dlogits [T, E] fp32 (out, every element).
+ *   or bias has none either, and its ds, finite or not, has no part in the others'.
+ *   dlogits [T, E] fp32 (out, every element).
  */
 int moe_route_scores_bwd(const float* logits, const float* bias, const moe_routing* how, const int32_t* topk_idx,
                          const float* ds, int T, int E, int k, float* dlogits, moe_stream_t stream);

@@ -633,6 +633,7 @@ __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs p) {
         v = row[e];
         if (!isfinite(v) || (p.bias && !isfinite(p.bias[e]))) e = -1;
     }
+    if (e < 0) d = 0.f;  // also where ds is not finite: the slot's weight is 0 whatever its expert gave
     float x[DENSE ? PER : 1], mx = -INFINITY, inv = 0.f;
     if constexpr (DENSE) {
         if (!whole) {

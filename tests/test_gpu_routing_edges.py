@@ -1,9 +1,13 @@
-"""The router with scores at the ends of fp32's range (GPU), against the fp64
-oracle; tolerances as in test_gpu_routing.py."""
+"""The router with scores at the ends of fp32's range, with gradients that are not finite, and with choices that
+few lanes or many candidates hold (GPU), against the fp64 oracle; tolerances as in test_gpu_routing.py."""
 import numpy as np
 import pytest
+import torch
 
-from .test_gpu_routing import M, check  # noqa: F401
+from oracle import block_oracle as B
+
+from ._util import f32_tensor
+from .test_gpu_routing import M, TOL, Call, check, logits  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 MOST = np.float32(np.finfo(np.float32).max)
@@ -21,3 +25,27 @@ def test_logits_whose_difference_is_past_fp32(M, score, E, k, renorm):
     check(M, lg, None, k, score, renorm=renorm)
     bias = np.zeros(E, np.float32)
     check(M, lg, bias, k, score, renorm=renorm)
+
+
+@pytest.mark.parametrize("score, renorm", [("sigmoid", True), ("sigmoid", False), ("softmax", True), ("softmax", False)])
+@pytest.mark.parametrize("E, k", [(16, 4), (512, 20)])
+def test_a_gradient_of_an_expert_without_weight(M, score, renorm, E, k):
+    """Slots that weigh 0 for want of a finite logit or bias have no part in the gradient, whatever dL/dtopk_w says
+    there: an expert out of service may well give an infinity or a NaN."""
+    rng = np.random.default_rng(k)
+    lg = logits(30, E, E)
+    bias = np.full(E, -np.inf, np.float32)
+    bias[rng.permutation(E)[:k // 2]] = 0.1
+    lg[5, :] = np.nan   # nothing left at all
+    c = Call(M, lg, bias, k, score, renorm=renorm).run()
+    idx = c.idx.cpu().numpy()
+    ds = rng.standard_normal(idx.shape).astype(np.float32)
+    away = ~(np.isfinite(np.take_along_axis(lg, idx, 1)) & np.isfinite(bias[idx]))
+    assert away.any() and not away.all()
+    zero = np.where(away, np.float32(0), ds)
+    want = c.bwd(f32_tensor(zero)).dlogits.clone()
+    ref = B.route_scores_bwd(lg, bias, idx, zero, score, renorm)
+    most = np.abs(c.w.cpu().numpy()).max(1, keepdims=True) * np.abs(zero).max(1, keepdims=True)
+    assert (np.abs(want.cpu().numpy() - ref) <= 2 * TOL * most + 1e-37).all()
+    for bad in (np.nan, np.inf, -np.inf):
+        assert torch.equal(c.bwd(f32_tensor(np.where(away, np.float32(bad), ds))).dlogits, want), bad
