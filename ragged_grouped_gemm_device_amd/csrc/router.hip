@@ -371,12 +371,14 @@ __global__ void __launch_bounds__(kScoresThreads) route_scores_kernel(RouteArgs 
                         for (int i = 0; i < part; ++i) take(m[i]);
                     }
                 }
-                for (int o = 1; o < per_group; o <<= 1) {  // then groups * per_group <= L: one turn, all lanes in it
+                for (int o = 1; o < per_group; o <<= 1) {  // partners are in the same turn: groups * per_group <= L
                     const float a2 = __shfl_xor(a, o, L), b2 = __shfl_xor(b, o, L);
                     b = larger(smaller(a, a2), larger(b, b2));
                     a = larger(a, a2);
                 }
-                if (j % per_group == 0) lds.gval[tw][g] = p.top == 2 && b > -INFINITY ? a + b : a;
+                const float worth = p.top == 2 && b > -INFINITY ? a + b : a;
+                doubt |= b > -INFINITY && fabsf(worth) == INFINITY;  // past fp32, where the exact sums have an order
+                if (j % per_group == 0) lds.gval[tw][g] = worth;
             }
             wave_lds_sync();
             uint64_t kept = 0;  // this token's groups

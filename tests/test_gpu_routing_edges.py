@@ -49,3 +49,21 @@ def test_a_gradient_of_an_expert_without_weight(M, score, renorm, E, k):
     assert (np.abs(want.cpu().numpy() - ref) <= 2 * TOL * most + 1e-37).all()
     for bad in (np.nan, np.inf, -np.inf):
         assert torch.equal(c.bwd(f32_tensor(np.where(away, np.float32(bad), ds))).dlogits, want), bad
+
+
+@pytest.mark.parametrize("E, k", [(256, 4), (320, 20)])
+def test_group_values_past_fp32(M, E, k):
+    """Sums of two biases that fp32 does not hold, at both ends: the groups' order is that of the exact sums."""
+    size = E // 8
+    rng = np.random.default_rng(E)
+    big = rng.permutation(np.linspace(1e38, 1.5e38, E)).astype(np.float32)
+    for g in range(8):   # sums from 3.6e38 up, no two alike, not in the groups' order
+        big[g * size + 3] = 1.8e38 + 1e36 * g
+        big[g * size + 5] = 1.8e38 + 1e37 * ((5 * g + 3) % 8)
+    for kept in (1, 3):
+        check(M, logits(30, E, 1), big, k, groups=8, kept=kept)
+        check(M, logits(30, E, 2), big, k, "softmax", groups=8, kept=kept)
+    check(M, logits(30, E, 3), -big, k, groups=8, kept=3)
+    low = np.full(E, -np.inf, np.float32)   # groups 0 to 2: nothing at all; 3 to 7: two experts and more, hardly
+    low[3 * size:] = -rng.permutation(np.linspace(3e38, 3.4e38, E - 3 * size)).astype(np.float32)
+    check(M, logits(30, E, 4), low, k, groups=8, kept=2, renorm=False)
