@@ -6,16 +6,22 @@
 //   the k best c within the best groups, ties to the lower index; w_j = scale s_j (/ sum_i s_i).
 //
 // The choice is that of 64-bit arithmetic at fp32 cost: scores are formed in fp32, whose error is
-// bounded; a token with two values nearer than that bound where their order matters (about one in
-// a thousand) is chosen again with 64-bit scores. Without a bias the logits themselves are
-// compared, which is exact.
+// bounded; a token with two values nearer than that bound where their order matters is chosen again with
+// 64-bit scores, by a wavefront of its own (normal logits, sigmoid with a bias: 1 to 2 tokens in 1000 for k = 8 of
+// up to 256 experts, 1 in 100 for 32 of 256, 7 in 100 for 64 of 1024; a softmax's fewer), and so is one with fewer
+// than k experts available, or with more nearly equal ones than are ranked. Without a bias the logits themselves
+// are compared, which is exact.
 //
 // Choosing k of E: L = 16 lanes hold a token (four tokens a wavefront; 64 lanes beyond 256 experts
 // or 16 choices). k rounds of a maximum over the lanes' own maxima give a value that at least k
 // experts reach and, the lanes being as random samples, few others (about k + 4 of 256 for k = 8);
 // those are gathered in LDS and each counts the ones ahead of it. A round costs four DPP steps, not
-// a pass over all E.
+// a pass over all E. Where fewer than k lanes hold an available expert (few experts, or few groups kept), all
+// available ones are candidates; where more than 64 would be, the bound is found by halving its range. 131072 tokens,
+// sigmoid with bias: 4 of 8 experts 38 us (2 of 8: 33), 8 of 64 in 3 of 8 groups 76 (in 4: 83), 16 of 256 173 (8:
+// 85), 64 of 512 1.6 ms.
 #include <algorithm>
+#include <cfloat>
 
 #include "block_common.hpp"
 #include "launch.hpp"
@@ -418,27 +424,56 @@ __global__ void __launch_bounds__(kScoresThreads) route_scores_kernel(RouteArgs 
         }
         // the next tokens' logits, on the way while these are chosen
         if (whole && t + TB - tw < t1) load_row(p.logits + min(t + TB, t1 - 1) * E, x);
-        // a value that at least k keys reach: the k-th largest of the lanes' maxima
+        // A value that at least k keys reach: the k-th largest of the lanes' maxima, their low bits the lane, so that
+        // of equal ones a round takes out one. Where fewer lanes have any, all that are available.
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < PER; ++i) top = larger(top, key[i]);
-        int most = ordered(top), least = most;
+        int most = (ordered(top) & -L) | gl, least = most;
         for (int r = 0; r < k; ++r) {
             least = lanes_max_i<L>(most);
             most = most == least ? INT32_MIN : most;
         }
-        const float reached = from_ordered(least);
-        // too few that are available: the exact form tells those apart that are kept from those that are not
-        bool odd = !(least > ordered(-INFINITY));
-        const float from = odd ? INFINITY : BIAS ? reached - near(reached) : reached;
+        const int lowest = ordered(-FLT_MAX);
+        int reached = max(least & -L, lowest);
         uint32_t hits = 0;  // bit PER - 1 - i: key i
+        int at = 0, m = 0;
+        auto gather = [&](float from) {  // the keys from there on
+            hits = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) hits = 2 * hits + (key[i] >= from ? 1u : 0u);
-        const int n = __popc(hits);
-        int at = lanes_scan<L>(n, gl);
-        int m = L == 64 ? __shfl(at, 63, 64) : __shfl(at, 15, 16);
-        at -= n;
-        if (m > kMaxCand) odd = true;  // many equal values
+            for (int i = 0; i < PER; ++i) hits = 2 * hits + (key[i] >= from ? 1u : 0u);
+            const int n = __popc(hits);
+            at = lanes_scan<L>(n, gl);
+            m = L == 64 ? __shfl(at, 63, 64) : __shfl(at, 15, 16);
+            at -= n;
+        };
+        auto from_reached = [&] {  // and those so near below that their order is not sure
+            const float v = from_ordered(reached);
+            return BIAS ? larger(v - near(v), -FLT_MAX) : v;
+        };
+        gather(from_reached());
+        if (__ballot(m > kMaxCand) != 0ull) {
+            // Too many to rank (k close to the lanes' number, or most lanes without a key): halve the range of
+            // values, the last of which none reaches, until few more than k reach the bound.
+            uint32_t span = (uint32_t)lanes_max_i<L>(ordered(top)) + 1u - (uint32_t)reached;
+            while (__ballot(m > (k + kMaxCand) / 2 && span > 1) != 0ull) {
+                const bool go = m > (k + kMaxCand) / 2 && span > 1;
+                const int was = m, mid = reached + (int)(span / 2);
+                gather(from_ordered(go ? mid : reached));
+                const bool enough = m >= k;
+                if (go) {
+                    reached = enough ? mid : reached;
+                    span = enough ? span - span / 2 : span / 2;
+                    m = enough ? m : was;
+                } else {
+                    m = was;
+                }
+            }
+            gather(from_reached());
+        }
+        // too few that are available: the exact form tells those apart that are kept from those that are not;
+        // too many: nearly equal values
+        const bool odd = m < k || m > kMaxCand;
         if (odd) hits = 0, m = 0;
         while (hits) {
             const int b = 31 - __clz((int)hits), i = PER - 1 - b;

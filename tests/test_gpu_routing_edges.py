@@ -67,3 +67,57 @@ def test_group_values_past_fp32(M, E, k):
     low = np.full(E, -np.inf, np.float32)   # groups 0 to 2: nothing at all; 3 to 7: two experts and more, hardly
     low[3 * size:] = -rng.permutation(np.linspace(3e38, 3.4e38, E - 3 * size)).astype(np.float32)
     check(M, logits(30, E, 4), low, k, groups=8, kept=2, renorm=False)
+
+
+@pytest.mark.parametrize("E, k, groups, kept", [
+    (8, 4, 1, 1), (8, 8, 1, 1), (16, 6, 1, 1), (32, 8, 1, 1), (64, 8, 8, 3), (64, 6, 8, 2), (48, 8, 8, 4), (48, 8, 4, 2), (128, 8, 8, 2),
+    (128, 32, 1, 1), (256, 16, 1, 1), (256, 16, 8, 2), (256, 9, 4, 1), (60, 60, 1, 1), (512, 64, 1, 1), (512, 40, 32, 5), (1024, 64, 1, 1),
+    (1024, 64, 64, 4), (333, 50, 3, 1),
+])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_choices_of_few_lanes_and_of_many_candidates(M, score, E, k, groups, kept):
+    """k near the number of lanes with an expert, or beyond it; logits that only bf16 tells apart, so that lanes
+    tie; and more equal values than are ranked."""
+    rng = np.random.default_rng(E + k)
+    lg = logits(70, E, E * k)
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    check(M, lg, bias, k, score, groups, kept)
+    check(M, lg, None, k, score, groups, kept, 1)
+    coarse = np.round(lg * 8) / 8
+    coarse[coarse == 0] = -0.0
+    check(M, coarse, None, k, score, groups, kept, 1, bwd=False)
+    check(M, coarse, np.zeros(E, np.float32), k, score, groups, kept, bwd=False)
+    out = bias.copy()   # experts out of service, among them whole lanes
+    out[rng.random(E) < 0.3] = -np.inf
+    out[:4] = -np.inf
+    check(M, lg, out, k, score, groups, kept, bwd=False)
+    check(M, -np.exp(lg * 20).clip(1e-30, 1e30), None, k, "sigmoid", groups, kept, 1, False, bwd=False)   # over all of fp32
+
+
+def microseconds(f, n=5):
+    f()
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    best = float("inf")
+    for _ in range(3):
+        a.record()
+        for _ in range(n):
+            f()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3 / n)
+    return best
+
+
+@pytest.mark.parametrize("size, beside", [
+    ((8, 4, 1, 1), (8, 2, 1, 1)), ((16, 6, 1, 1), (16, 4, 1, 1)), ((64, 8, 8, 3), (64, 8, 8, 4)), ((48, 8, 4, 2), (64, 8, 8, 4)),
+    ((256, 16, 1, 1), (256, 8, 1, 1)),
+])
+def test_no_size_leaves_the_fp32_form(M, size, beside):
+    """Times at 65536 tokens, beside those of a size with more lanes than choices: one token after another in 64
+    bits takes 4 to 11 times as long, the fp32 form at most about twice (k to the second at most: 16 against 8)."""
+    def us(E, k, groups, kept):
+        c = Call(M, logits(65536, E), np.linspace(-.1, .1, E).astype(np.float32), k, groups=groups, kept=kept)
+        return microseconds(c.run)
+
+    assert us(*size) <= 3 * us(*beside)
