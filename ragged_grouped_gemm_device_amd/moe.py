@@ -7,6 +7,7 @@ Failing to load the library raises immediately -- there is no fallback.
 """
 from __future__ import annotations
 
+import copy
 import ctypes as C
 import os
 
@@ -925,23 +926,39 @@ class Router:
 class Experts4:
     """The routed experts' weights as MXFP4, for serving: w1 [E, d, 2n] (gated; n wide otherwise) and w2
     [E, n, d] in 17 instead of 64 bytes for 32 values. x_form: how the products take their rows, as bf16, or
-    quantized to MXFP8 or MXFP4 on the way (the tokens once, before they are gathered)."""
+    quantized to MXFP8 or MXFP4 on the way (the tokens once, before they are gathered). It serves calls of T
+    tokens, one at a time: the rows' codes and the workspace are its own. sized(T) gives one for another number of
+    tokens, or another stream, on the same weights."""
 
     def __init__(self, T: int, k: int, E: int, d: int, n: int, act: int = MOE_ACT_SWIGLU, x_form: int = MOE_X_BF16,
                  device="cuda"):
-        self.T, self.k, self.act, self.x_form = T, k, act, x_form
+        self.k, self.act, self.x_form = k, act, x_form
         n1 = 2 * n if act in _GATED else n
         new = lambda *shape: torch.empty(*shape, dtype=_U8, device=device)  # noqa: E731
         self.w1_q, self.w1_s = new(E, n1, d // 2), new(E, n1, d // MOE_MX_BLOCK)
         self.w2_q, self.w2_s = new(E, d, n // 2), new(E, d, n // MOE_MX_BLOCK)
-        M = moe_capacity_rows(T, k, E)
+        self._scratch(T)
+
+    def _scratch(self, T):
+        (E, n1, d), n = self.w1_s.shape, self.w2_q.shape[2] * 2
+        d *= MOE_MX_BLOCK
+        new = lambda *shape: torch.empty(*shape, dtype=_U8, device=self.w1_q.device)  # noqa: E731
+        self.T = T
+        M = moe_capacity_rows(T, self.k, E)
         self.x_q = self.x_s = self.a_q = self.a_s = None
-        if x_form != MOE_X_BF16:
-            per = 1 if x_form == MOE_X_MXFP8 else 2
+        if self.x_form != MOE_X_BF16:
+            per = 1 if self.x_form == MOE_X_MXFP8 else 2
             self.x_q, self.x_s = new(T, d // per), new(T, d // MOE_MX_BLOCK)
             self.a_q, self.a_s = new(M, n // per), new(M, n // MOE_MX_BLOCK)
-        self.ws = new(max(16, moe_grouped_linear_mxfp4_workspace_bytes(T, k, E, d, n1),
-                          moe_grouped_linear_mxfp4_workspace_bytes(T, k, E, n, d)))
+        self.ws = new(max(16, moe_grouped_linear_mxfp4_workspace_bytes(T, self.k, E, d, n1),
+                          moe_grouped_linear_mxfp4_workspace_bytes(T, self.k, E, n, d)))
+
+    def sized(self, T: int):
+        """An Experts4 for T tokens a call on these weights (the same tensors: load on either fills both), with
+        codes and workspace of its own, so that both may run at once."""
+        other = copy.copy(self)
+        other._scratch(T)
+        return other
 
     def load(self, w1, w2):
         """Quantizes bf16 weights, once."""
