@@ -1,8 +1,17 @@
-"""Experts served on 4-bit weights: several token counts and streams on one set of weights (GPU)."""
+"""Experts served on 4-bit weights: the chain of both products, each from the codes that the run itself made of its
+rows, and several token counts and streams on one set of weights (GPU).
+
+Bounds of a product: sums of K terms in fp32, K * 2^-22 of their magnitudes; with 8-bit rows 7 * 2^-13 of the largest product of
+each 8 as well (the matrix cores cut smaller ones off there); the activation's, with |f'| <= 1.13; half a step of bf16."""
+import numpy as np
 import pytest
 import torch
 
+from oracle import block_oracle as B
 from oracle import dense_oracle as D
+from oracle import moe_oracle as O
+
+from ._util import bf16_values
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -40,6 +49,69 @@ def weights(M, T, k, E, d, n, act, form):
     four.load((torch.randn(E, d, n1, device="cuda", generator=g) * d**-0.5).to(BF),
               (torch.randn(E, n, d, device="cuda", generator=g) * n**-0.5).to(BF))
     return four
+
+
+def product(x, w, act, form):
+    """f(x w^T) in 64 bits and how far off it may come out."""
+    z = x @ w.T
+    dz = x.shape[1] * 2.0**-22 * (np.abs(x) @ np.abs(w).T)
+    if form == 1:
+        eights = lambda v: np.abs(v).reshape(v.shape[0], -1, 8).max(2)  # noqa: E731
+        dz = dz + 7 * 2.0**-13 * (eights(x) @ eights(w).T)
+    ref = D.act_forward(z, act)
+    if act in D.GATED:   # |f'| <= 1.13 for both gates, |f(g)| <= |g|
+        (g, u), (dg, du) = O.deinterleave(z), O.deinterleave(dz)
+        slack = 1.13 * dg * np.abs(u) + (np.abs(g) + 1.13 * dg) * du + 8 * 2.0**-23 * np.abs(g * u)
+    elif act == "srelu":
+        slack = 2 * np.abs(z) * dz + dz * dz
+    else:
+        slack = 1.13 * dz + 8 * 2.0**-23 * np.abs(z)
+    return ref, slack + 2.0**-8 * (np.abs(ref) + slack)
+
+
+@pytest.mark.parametrize("form", [0, 1, 2])
+@pytest.mark.parametrize("T, k, E, d, n, act", [
+    (1, 2, 8, 128, 64, "swiglu"), (37, 4, 16, 192, 128, "geglu"), (300, 2, 8, 320, 192, "swiglu"), (600, 3, 4, 256, 64, "srelu"),
+])
+def test_the_chain_from_the_runs_own_codes(M, form, T, k, E, d, n, act):
+    s = Served(M, weights(M, T, k, E, d, n, act, form))
+    s.run()
+    torch.cuda.synchronize()
+    b, four = s.buf, s.four
+    c = lambda t: t.cpu().numpy()  # noqa: E731
+    counts, offsets = c(b.counts), c(b.offsets)
+    live = np.concatenate([np.arange(o, o + m) for o, m in zip(offsets, counts)])
+    of_token = c(b.src_of)[live] // k
+
+    def rows(v, q, sc, at):
+        """The values that the product read, from the codes; those are the oracle's of the bf16 rows v."""
+        if form == 0:
+            return v
+        q, sc = c(q)[at], c(sc)[at]
+        if form == 1:
+            want = O.quant_mxfp8(v, colwise=False)
+        else:
+            want = B.quant_mxfp4(v)
+            want = B.pack4(want[0]), want[1]
+        assert np.array_equal(q, want[0]) and np.array_equal(sc, want[1])
+        return O.mx_dequant(q, sc) if form == 1 else B.dequant_mxfp4(q, sc)
+
+    x = rows(bf16_values(s.x), four.x_q, four.x_s, slice(None))[of_token]
+    a = rows(bf16_values(b.a)[live], four.a_q, four.a_s, live)
+    w1, w2 = (B.dequant_mxfp4(c(q), c(sc)) for q, sc in ((four.w1_q, four.w1_s), (four.w2_q, four.w2_s)))
+    expert = np.repeat(np.arange(E), counts)
+    for v, w, f, got in ((x, w1, act, b.a), (a, w2, "none", b.y)):
+        got = bf16_values(got)[live]
+        for e in np.flatnonzero(counts):
+            at = expert == e
+            ref, off = product(v[at], w[e], f, form)
+            assert (np.abs(got[at] - ref) <= off).all(), (f, e)
+    # sums of k terms in fp32, rounded to bf16
+    y = np.zeros((b.M_cap, d))
+    y[live] = bf16_values(b.y)[live]
+    w = c(b.topk_w).astype(np.float64)
+    ref, most = (O.combine(v, c(b.row_of), k, w, rounding=False) for v in (y, np.abs(y)))
+    assert (np.abs(bf16_values(b.out) - ref) <= 2.0**-8 * np.abs(ref) + 2 * k * 2.0**-24 * most).all()
 
 
 @pytest.mark.parametrize("form", [0, 1, 2])
