@@ -923,6 +923,12 @@ class Router:
             self.dwg.copy_(dwg[:, :E])
 
 
+def _used_rows(T: int, k: int, E: int) -> int:
+    """Rows of the experts' buffer that a routing of T tokens can reach: those of the experts hit, each up to its
+    region's end. Few tokens hit few of many experts, and the capacity is for all."""
+    return (T * k + (MOE_ALIGN - 1) * min(E, T * k)) // MOE_ALIGN * MOE_ALIGN
+
+
 class Experts4:
     """The routed experts' weights as MXFP4, for serving: w1 [E, d, 2n] (gated; n wide otherwise) and w2
     [E, n, d] in 17 instead of 64 bytes for 32 values. x_form: how the products take their rows, as bf16, or
@@ -950,6 +956,7 @@ class Experts4:
             per = 1 if self.x_form == MOE_X_MXFP8 else 2
             self.x_q, self.x_s = new(T, d // per), new(T, d // MOE_MX_BLOCK)
             self.a_q, self.a_s = new(M, n // per), new(M, n // MOE_MX_BLOCK)
+            self.used = _used_rows(T, self.k, E)
         self.ws = new(max(16, moe_grouped_linear_mxfp4_workspace_bytes(T, self.k, E, d, n1),
                           moe_grouped_linear_mxfp4_workspace_bytes(T, self.k, E, n, d)))
 
@@ -965,10 +972,11 @@ class Experts4:
         moe_quant_mxfp4(w1, MOE_QUANT_COLWISE, q_col=self.w1_q, s_col=self.w1_s)
         moe_quant_mxfp4(w2, MOE_QUANT_COLWISE, q_col=self.w2_q, s_col=self.w2_s)
 
-    def _rows(self, x, q, s):
+    def _rows(self, x, q, s, used=None):
         if self.x_form == MOE_X_BF16:
             return x, None
-        (moe_quant_mxfp8 if self.x_form == MOE_X_MXFP8 else moe_quant_mxfp4)(x, MOE_QUANT_ROWWISE, q, s)
+        quant = moe_quant_mxfp8 if self.x_form == MOE_X_MXFP8 else moe_quant_mxfp4
+        quant(x[:used], MOE_QUANT_ROWWISE, q[:used], s[:used])
         return q, s
 
     def forward(self, x, offsets, counts, src_of, a, y):
@@ -976,7 +984,8 @@ class Experts4:
         q, s = self._rows(x, self.x_q, self.x_s)
         moe_grouped_linear_mxfp4(q, self.w1_q, self.w1_s, offsets, counts, a, self.T, self.k, act=self.act, x_s=s,
                                  src_of=src_of, workspace=self.ws)
-        q, s = self._rows(a, self.a_q, self.a_s)
+        # of rows between those that the routing made, the codes are of whatever the buffer holds, and not read
+        q, s = self._rows(a, self.a_q, self.a_s, None if self.a_q is None else self.used)
         moe_grouped_linear_mxfp4(q, self.w2_q, self.w2_s, offsets, counts, y, self.T, self.k, x_s=s, workspace=self.ws)
 
 

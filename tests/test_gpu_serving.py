@@ -151,3 +151,17 @@ def test_another_token_count_is_refused(M):
     s.logits = s.logits[:4].contiguous()
     with pytest.raises(ValueError, match="expected"):
         s.run()
+
+
+@pytest.mark.parametrize("form", [1, 2])
+def test_codes_past_the_rows_that_a_routing_reaches_are_left(M, form):
+    """One token and 64 experts: its 4 rows lie in the first 4 regions, not in the capacity for any routing."""
+    s = Served(M, weights(M, 1, 4, 64, 64, 64, "swiglu", form))
+    want = s.run().clone()
+    used = int(s.buf.offsets[-1])
+    assert used == 4 * M.MOE_ALIGN < s.buf.M_cap / 16
+    for t in (s.four.a_q, s.four.a_s):
+        t.fill_(0x55)
+    assert torch.equal(s.run(), want)
+    for t in (s.four.a_q, s.four.a_s):
+        assert (t[used:] == 0x55).all()

@@ -1,6 +1,7 @@
 """Experts served on 4-bit weights: what the binding lays out and refuses (CPU)."""
 import os
 
+import numpy as np
 import pytest
 import torch
 
@@ -28,3 +29,18 @@ def test_sized_shares_the_weights_alone(form, per, act):
         assert e.x_q.shape == (T, 64 // per) and e.x_s.shape == (T, 2) and e.a_q.shape == (cap, 96 // per) and e.a_s.shape == (cap, 3)
     if per:
         assert a.a_q.data_ptr() != b.a_q.data_ptr() and a.x_q.data_ptr() != b.x_q.data_ptr()
+
+
+def test_rows_that_a_routing_reaches():
+    """No routing goes past them; some reach them."""
+    rng = np.random.default_rng(0)
+    for T, k, E in [(1, 1, 1), (1, 8, 256), (16, 8, 256), (5, 3, 4), (300, 2, 8), (129, 4, 4), (1021, 8, 32), (1 << 20, 8, 32)]:
+        pairs, used = T * k, M._used_rows(T, k, E)
+        assert used % M.MOE_ALIGN == 0 and used <= M.moe_capacity_rows(T, k, E)
+        ends = []
+        for trial in range(200 if T < 1 << 16 else 5):
+            weight = np.full(E, 1 / E) if trial % 2 else rng.dirichlet(np.full(E, 0.1))
+            counts = np.minimum(rng.multinomial(pairs, weight), T)
+            ends.append(int((-(-counts // M.MOE_ALIGN) * M.MOE_ALIGN).sum()))
+        assert max(ends) <= used
+    assert M._used_rows(1, 8, 256) == 8 * M.MOE_ALIGN and M._used_rows(129, 4, 4) == 4 * 2 * M.MOE_ALIGN   # all of it
