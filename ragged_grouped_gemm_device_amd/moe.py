@@ -1031,9 +1031,15 @@ def forward(buf: Buffers, x, logits, w1, w2, renorm=False, fwd_stages=MOE_STAGES
     is kept as an 8-bit checkpoint. router = (Router, wg): the logits are x wg (logits is None),
     and the router losses follow the routing. shared = (SharedExpert, w1, w2): the shared expert's
     output is added to out. routing = a Routing: its scores, bias, groups and weights (renorm is then its
-    own). experts4 = an Experts4 (serving): its 4-bit weights and activation in place of w1, w2 and act; nothing is
-    kept for a backward pass. norms = (BlockNorms, w_pre, w_post, gate or None): x is the residual
+    own). experts4 = an Experts4 (serving): its 4-bit weights and activation in place of w1, w2 and act; it reads
+    the rows of x through src_of, with gather or without, and nothing is kept for a backward pass, whatever store_h
+    says; mx, and single stages, are refused. norms = (BlockNorms, w_pre, w_post, gate or None): x is the residual
     stream, the layer runs on its norm, buf.out holds the layer's output and the BlockNorms' out the block's."""
+    if experts4 is not None:
+        if mx or fwd_stages & MOE_STAGES_FWD != MOE_STAGES_FWD:
+            raise ValueError("experts4: both products at once, in its own x_form: no mx and no other fwd_stages")
+        if experts4.k != buf.k:   # the products divide src_of by it
+            raise ValueError(f"experts4: made for k = {experts4.k}, the buffers for k = {buf.k}")
     x_in = x
     if norms is not None:
         x = norms[0].before(x_in, norms[1])

@@ -44,3 +44,16 @@ def test_rows_that_a_routing_reaches():
             ends.append(int((-(-counts // M.MOE_ALIGN) * M.MOE_ALIGN).sum()))
         assert max(ends) <= used
     assert M._used_rows(1, 8, 256) == 8 * M.MOE_ALIGN and M._used_rows(129, 4, 4) == 4 * 2 * M.MOE_ALIGN   # all of it
+
+
+@pytest.mark.parametrize("kw, match", [
+    (dict(mx=True), "mx"), (dict(fwd_stages=M.MOE_STAGE_FC1), "fwd_stages"), (dict(fwd_stages=0), "fwd_stages"), (dict(k=3), "k = 3"),
+])
+def test_forward_refuses_what_experts4_has_no_form_of(kw, match):
+    kw = dict(kw)
+    buf = M.Buffers(8, 2, 8, 64, 64, device="cpu")
+    four = M.Experts4(8, kw.pop("k", 2), 8, 64, 64, device="cpu")
+    for norms in (None, (M.BlockNorms(8, 64, device="cpu"), None, None, None)):
+        with pytest.raises(ValueError, match=match):
+            M.forward(buf, torch.zeros(8, 64), torch.zeros(8, 8), None, None, experts4=four, norms=norms, **kw)
+    assert not buf.served
