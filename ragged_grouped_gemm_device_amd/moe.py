@@ -1021,6 +1021,11 @@ class BlockNorms:
         moe_norm_bwd(dy, x, w, self.rstd_pre, self.dx, self.dw_pre, self.ws, dres=dout)
 
 
+def _check_losses(router, routing):
+    if router is not None and routing is not None and routing.how.score == MOE_SCORE_SIGMOID and router[0].balance_coef:
+        raise ValueError("the Router's balance loss is that of softmax probabilities: with sigmoid scores, balance_coef=0")
+
+
 def forward(buf: Buffers, x, logits, w1, w2, renorm=False, fwd_stages=MOE_STAGES_FWD, store_h=True,
             act=MOE_ACT_SWIGLU, gather=False, mx=False, router=None, shared=None, routing=None, experts4=None,
             norms=None):
@@ -1031,8 +1036,9 @@ def forward(buf: Buffers, x, logits, w1, w2, renorm=False, fwd_stages=MOE_STAGES
     is kept as an 8-bit checkpoint. router = (Router, wg): the logits are x wg (logits is None),
     and the router losses follow the routing. shared = (SharedExpert, w1, w2): the shared expert's
     output is added to out. routing = a Routing: its scores, bias, groups and weights (renorm is then its
-    own). experts4 = an Experts4 (serving): its 4-bit weights and activation in place of w1, w2 and act; it reads
-    the rows of x through src_of, with gather or without, and nothing is kept for a backward pass, whatever store_h
+    own); a Router beside sigmoid scores needs balance_coef = 0, as its balance loss is a softmax's.
+    experts4 = an Experts4 (serving): its 4-bit weights and activation in place of w1, w2 and act; it reads the
+    rows of x through src_of, with gather or without, and nothing is kept for a backward pass, whatever store_h
     says; mx, and single stages, are refused. norms = (BlockNorms, w_pre, w_post, gate or None): x is the residual
     stream, the layer runs on its norm, buf.out holds the layer's output and the BlockNorms' out the block's."""
     if experts4 is not None:
@@ -1040,6 +1046,7 @@ def forward(buf: Buffers, x, logits, w1, w2, renorm=False, fwd_stages=MOE_STAGES
             raise ValueError("experts4: both products at once, in its own x_form: no mx and no other fwd_stages")
         if experts4.k != buf.k:   # the products divide src_of by it
             raise ValueError(f"experts4: made for k = {experts4.k}, the buffers for k = {buf.k}")
+    _check_losses(router, routing)
     x_in = x
     if norms is not None:
         x = norms[0].before(x_in, norms[1])
@@ -1102,6 +1109,7 @@ def backward(buf: Buffers, dout, w1, w2, stages=MOE_STAGES_BWD, act=MOE_ACT_SWIG
     that of the residual stream."""
     if buf.served:
         raise ValueError("the last forward ran on 4-bit weights and kept nothing for a backward pass")
+    _check_losses(router, routing)
     x_in = x if x is not None else x_tokens
     if norms is not None:
         if x_in is None:

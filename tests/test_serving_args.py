@@ -57,3 +57,19 @@ def test_forward_refuses_what_experts4_has_no_form_of(kw, match):
         with pytest.raises(ValueError, match=match):
             M.forward(buf, torch.zeros(8, 64), torch.zeros(8, 8), None, None, experts4=four, norms=norms, **kw)
     assert not buf.served
+
+
+def test_sigmoid_routing_beside_the_softmax_balance_loss_is_refused():
+    """The balance loss is that of softmax probabilities: beside sigmoid scores it would train the router towards
+    another distribution than the one it routes by. The z loss takes any."""
+    buf = M.Buffers(8, 2, 8, 64, 64, device="cpu")
+    z = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t)  # noqa: E731
+    for score, coef, refused in [(M.MOE_SCORE_SIGMOID, 1e-2, True), (M.MOE_SCORE_SIGMOID, 0.0, False), (M.MOE_SCORE_SOFTMAX, 1e-2, False)]:
+        router = (M.Router(8, 64, 8, 2, balance_coef=coef, z_coef=1e-3, device="cpu"), z(64, 8))
+        kw = dict(router=router, routing=M.Routing(score=score))
+        match = "balance_coef" if refused else "GPU"   # off the GPU, where it is not refused before
+        with pytest.raises(ValueError, match=match):
+            M.forward(buf, z(8, 64), None, None, None, **kw)
+        if refused:
+            with pytest.raises(ValueError, match=match):
+                M.backward(buf, z(8, 64), None, None, x_tokens=z(8, 64), **kw)
