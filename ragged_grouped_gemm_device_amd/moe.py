@@ -1013,6 +1013,8 @@ class BlockNorms:
                           scale=self.scale, **rows)
 
     def back_after(self, dout, w, gate, y):
+        if gate is not None and self.dgate is None:
+            raise ValueError("gate: its gradient has no place, gate_cols was 0")
         moe_post_norm_bwd(dout, y, w, self.rstd_post, self.dy, self.dw_post, self.ws, gate=gate, dgate=self.dgate,
                           gate_act=self.gate_act, scale=self.scale)
         return self.dy

@@ -73,3 +73,11 @@ def test_sigmoid_routing_beside_the_softmax_balance_loss_is_refused():
         if refused:
             with pytest.raises(ValueError, match=match):
                 M.backward(buf, z(8, 64), None, None, x_tokens=z(8, 64), **kw)
+
+
+def test_a_gate_that_the_norms_were_not_made_for_has_no_silent_backward():
+    z = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t)  # noqa: E731
+    for cols, gate in ((0, z(8, 1)), (0, z(8, 64)), (1, z(8, 64)), (64, z(8, 1)), (1, None)):
+        norms = M.BlockNorms(8, 64, cols, device="cpu")
+        with pytest.raises(ValueError, match="gate"):
+            norms.back_after(z(8, 64), z(64), gate, z(8, 64))
