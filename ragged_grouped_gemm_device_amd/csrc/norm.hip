@@ -409,10 +409,26 @@ size_t norm_workspace_bytes(int T, int d) {
 
 static int done() { return hipGetLastError() == hipSuccess ? 0 : -4; }
 
+// The rows in launches of at most kNormGroups workgroups, f(first row, rows): one of 2^32 threads and more would be cut
+// off without an error.
+constexpr int64_t kNormGroups = 1 << 22;
+template <class F>
+static void by_rows(int T, int rows_per_group, F&& f) {
+    const int64_t step = kNormGroups * rows_per_group;
+    for (int64_t t = 0; t < T; t += step) f(t, (int)std::min(step, T - t));
+}
+template <class E>
+static E* at_row(E* p, int64_t offset) { return p ? p + offset : p; }
+
 int launch_norm_fwd(const NormFwd& p, hipStream_t s) {
     norm_dispatch(p.d, [&](auto A, auto B) {
         constexpr int TPR = decltype(A)::value, NC = decltype(B)::value, RPB = kNormThreads / TPR;
-        norm_fwd_kernel<TPR, NC><<<(unsigned)((p.T + RPB - 1) / RPB), kNormThreads, 0, s>>>(p);
+        by_rows(p.T, RPB, [&](int64_t t, int rows) {
+            NormFwd q = p;
+            const int64_t o = t * p.d;
+            q.T = rows, q.x = p.x + o, q.res = at_row(p.res, o), q.total = at_row(p.total, o), q.y = p.y + o, q.rstd = at_row(p.rstd, t);
+            norm_fwd_kernel<TPR, NC><<<(unsigned)((rows + RPB - 1) / RPB), kNormThreads, 0, s>>>(q);
+        });
     });
     return done();
 }
@@ -420,7 +436,14 @@ int launch_norm_fwd(const NormFwd& p, hipStream_t s) {
 int launch_post_norm_fwd(const PostNormFwd& p, hipStream_t s) {
     norm_dispatch(p.d, [&](auto A, auto B) {
         constexpr int TPR = decltype(A)::value, NC = decltype(B)::value, RPB = kNormThreads / TPR;
-        post_norm_fwd_kernel<TPR, NC><<<(unsigned)((p.T + RPB - 1) / RPB), kNormThreads, 0, s>>>(p);
+        by_rows(p.T, RPB, [&](int64_t t, int rows) {
+            PostNormFwd q = p;
+            const int64_t o = t * p.d;
+            if (!p.row_of) q.y = p.y + o;  // else the experts' rows, wherever they are
+            q.row_of = at_row(p.row_of, t * p.k), q.topk_w = at_row(p.topk_w, t * p.k), q.gate = at_row(p.gate, t * p.gate_cols);
+            q.T = rows, q.x = p.x + o, q.total = at_row(p.total, o), q.out = p.out + o, q.rstd = at_row(p.rstd, t);
+            post_norm_fwd_kernel<TPR, NC><<<(unsigned)((rows + RPB - 1) / RPB), kNormThreads, 0, s>>>(q);
+        });
     });
     return done();
 }
