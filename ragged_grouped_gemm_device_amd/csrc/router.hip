@@ -791,12 +791,17 @@ int launch_route_scores(const RouteCall& c, hipStream_t s) {
 
 int launch_route_scores_bwd(const float* logits, const float* bias, const int32_t* topk_idx, const float* ds, int T,
                             int E, int k, int sigmoid, int renorm, float scale, float* dlogits, hipStream_t s) {
-    const RouteBwdArgs p{logits, bias, topk_idx, ds, T, E, k, sigmoid, renorm, scale, dlogits};
     by_experts(E, k, [&](auto A, auto B) {
-        constexpr int L = decltype(A)::value, PER = decltype(B)::value;
-        const unsigned grid = (unsigned)(((int64_t)T + 256 / L - 1) / (256 / L));
-        if (!sigmoid && !renorm) route_scores_bwd_kernel<L, PER, true><<<grid, 256, 0, s>>>(p);
-        else route_scores_bwd_kernel<L, PER, false><<<grid, 256, 0, s>>>(p);
+        constexpr int L = decltype(A)::value, PER = decltype(B)::value, TB = 256 / L;  // tokens a workgroup
+        // 2^22 workgroups a launch: one of 2^32 threads and more would be cut off without an error
+        const int64_t step = ((int64_t)1 << 22) * TB;
+        for (int64_t t = 0; t < T; t += step) {
+            const int n = (int)std::min(step, T - t);
+            const RouteBwdArgs p{logits + t * E, bias, topk_idx + t * k, ds + t * k, n, E, k, sigmoid, renorm, scale, dlogits + t * E};
+            const unsigned grid = (unsigned)((n + TB - 1) / TB);
+            if (!sigmoid && !renorm) route_scores_bwd_kernel<L, PER, true><<<grid, 256, 0, s>>>(p);
+            else route_scores_bwd_kernel<L, PER, false><<<grid, 256, 0, s>>>(p);
+        }
     });
     return hipGetLastError() == hipSuccess ? 0 : -4;
 }

@@ -1,4 +1,4 @@
-"""Norms of more tokens than one launch has room for: a workgroup's share of them each, they
+"""Norms and the router's gradient of more tokens than one launch has room for: a workgroup's share of them each, they
 would be 2^32 threads and more, which is cut off without an error (GPU). The rows repeat a block of 4096, so that
 every result is that of the block."""
 import pytest
@@ -65,4 +65,17 @@ def test_norm_with_residual_and_post_norm(M, rows):
 
     for big, block in zip(run(T, lambda a: tiled(a, T)), run(BLOCK, lambda a: a)):
         assert torch.isfinite(block).all()
+        same(big, block)
+
+
+@pytest.mark.parametrize("T, E, k", [((1 << 28) + 5, 4, 2), ((1 << 26) + 5, 20, 17)])
+def test_router_gradient(M, T, E, k):
+    g = torch.Generator("cuda").manual_seed(E)
+    lg, ds = torch.randn(BLOCK, E, device="cuda", generator=g), torch.randn(BLOCK, k, device="cuda", generator=g)
+    idx = torch.rand(BLOCK, E, device="cuda", generator=g).topk(k, 1).indices.int()
+    for score, renorm in ((M.MOE_SCORE_SIGMOID, True), (M.MOE_SCORE_SOFTMAX, False)):
+        how = M.Routing(score, renorm=renorm)
+        block, big = torch.empty_like(lg), torch.full((T, E), float("nan"), device="cuda")
+        M.moe_route_scores_bwd(lg, idx, ds, block, how)
+        M.moe_route_scores_bwd(tiled(lg, T), tiled(idx, T), tiled(ds, T), big, how)
         same(big, block)
