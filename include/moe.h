@@ -620,7 +620,7 @@ int moe_route_scores_bwd(const float* logits, const float* bias, const moe_routi
  *     [batch, R, C / 32]. Needs C % 32 == 0.
  *   MOE_QUANT_COLWISE: blocks along the rows, stored transposed; q_col
  *     [batch, C, R / 2], s_col [batch, C, R / 32]: weights [E, K, N] as
- *     moe_grouped_linear_mxfp4 reads them. Needs R % 32 == 0, C % 8 == 0.
+ *     moe_grouped_linear_mxfp4 reads them. Needs R % 32 == 0, C % 8 == 0, C < 2^30.
  *   src and the codes 16-byte aligned.
  */
 int moe_quant_mxfp4(const uint16_t* src, int batch, int64_t R, int C, int mode, uint8_t* q_row, uint8_t* s_row,

@@ -98,7 +98,8 @@ int moe_quant_mxfp4(const uint16_t* src, int batch, int64_t R, int C, int mode, 
     if ((mode & MOE_QUANT_COLWISE) && (!q_col || !s_col)) return MOE_ERR_INVALID_ARG;
     if (!aligned({src, q_row, q_col})) return MOE_ERR_INVALID_ARG;
     if (C % 8 || ((mode & MOE_QUANT_ROWWISE) && C % MOE_MX_BLOCK)) return MOE_ERR_UNSUPPORTED;
-    if ((mode & MOE_QUANT_COLWISE) && (R % MOE_MX_BLOCK || (R + 255) / 256 > 65535)) return MOE_ERR_UNSUPPORTED;
+    // a launch holds 65535 workgroups of 256 rows, and below 2^32 threads, four a column
+    if ((mode & MOE_QUANT_COLWISE) && (R % MOE_MX_BLOCK || (R + 255) / 256 > 65535 || C >= 1 << 30)) return MOE_ERR_UNSUPPORTED;
     if (R > ((int64_t)1 << 40) / C / batch || batch > 65535) return MOE_ERR_UNSUPPORTED;
     return status(moe::launch_quant_mxfp4(src, batch, R, C, mode, q_row, s_row, q_col, s_col, S(stream)));
 }
