@@ -68,8 +68,9 @@ __device__ __forceinline__ i32x8_t operand8(uint4 a, uint4 b) {
 // 64 rows of 128 bytes, one ahead of the one it multiplies, and waits for no other. X, a few rows, comes
 // straight from the caches: lanes without a row ask for nothing. The scales of W's rows, 8 bytes of a line a
 // block, are laid into LDS once for 8192 of K.
-// One token, 8 of 32 experts: 7168 x 4096 SwiGLU 25 us (5.0 TB/s, a large copy's rate), 2048 x 7168 15.7 (4.0); 16 tokens,
-// all experts, 7168 x 4096: 88 to 90 (5.5).
+// One token, 8 of 32 experts: 7168 x 4096 SwiGLU 24 to 26 us (4.8 to 5.1 TB/s, a large copy's rate), 2048 x 7168 15.7 to
+// 17.1 (3.7 to 4.0); 16 tokens, all experts, 7168 x 4096: 88 to 100 (5.0 to 5.6). With 32 bf16 rows one register goes to
+// scratch.
 constexpr int kScaleChunk = 256;  // scale bytes of a row in LDS; 16-byte pieces XOR-swizzled by the row
 
 template <int F, int RT, int NW>
@@ -310,8 +311,8 @@ constexpr int wait_vmcnt(int n) { return 0x0F70 | (n & 15) | (n >> 4 << 14); }
 // Tiles of BMX rows x 256 columns, 2 x 4 wavefronts, each every other block of 32 rows and 64 columns; two slabs in LDS, the
 // next on its way by copies that pass no registers while one is multiplied. The slabs of all of a workgroup's tiles are
 // one sequence, so that the next tile's first arrives during the last's epilogue. 16384 tokens x 8 of 32 experts,
-// 7168 x 4096, SwiGLU: 4-bit rows 1990 to 2060 us (3800 TFLOP/s), 8-bit 3130 to 3230 (2430), bf16 5980 to 6240 (1260, as a
-// large library product). bf16 is bound by the matrix cores; in the 4-bit form they are busy 46% at the 1.8 GHz that the
+// 7168 x 4096, SwiGLU, by box and run: 4-bit rows 1990 to 2160 us (3560 to 3870 TFLOP/s), 8-bit 3130 to 3230 (2380 to
+// 2460), bf16 5980 to 6300 (1220 to 1290, as a large library product). bf16 is bound by the matrix cores; in the 4-bit form they are busy 46% at the 1.8 GHz that the
 // power limit leaves: multiplying alone took 1588 us, copying alone 1650, neither quite hidden behind the other.
 // Tiles of fewer rows wait for W from HBM: there (kEarly) a slab's copies go out before the one they replace is multiplied to
 // its end, as soon as all wavefronts have its last fragments: a barrier more a slab, and 7 to 11% less time (32 rows

@@ -8,7 +8,8 @@
 // all of them).
 //
 // Both directions are bound by HBM: 2 bytes in and 17/32 out a value, or the reverse. 8 x 7168 x 4096 values: by
-// columns 122 us (4.9 TB/s), restored 101 (5.9); 1021 x 2880: 3.2 us by rows, 3.4 restored, a launch's time.
+// columns 122 us (4.9 TB/s), restored 101 (5.9); by rows 16384 x 7168 53 (5.6) and 131072 x 2048 114 (5.9), restored 44
+// and 96 (6.8, 7.1: the codes come from the last-level cache); 1021 x 2880: 3.1 us by rows, 3.4 restored, a launch's time.
 #include <algorithm>
 
 #include "block_common.hpp"

@@ -7,9 +7,11 @@
 //           ds = rho (g - h mean(g h)),  dw = sum over rows of dy h
 //
 // All are bound by HBM traffic: a row stays in registers between its statistics and its
-// output, so every tensor is read once and written once. 32768 x 8192 with the residual: forward 370 us (5.8
-// TB/s), backward 428 (5.0); 16384 x 7168 of 8 experts with a full gate: forward 561 (5.0), backward 229 (5.1). A large
-// copy reaches 5.0.
+// output, so every tensor is read once and written once. 32768 x 8192 with the residual: forward 366 us (5.9
+// TB/s), backward 420 (5.1); 16384 x 7168 of 8 experts with a full gate: forward 558 (5.0), backward 228 (5.1). A large
+// copy reaches 5.0 to 5.1. Past 8192 columns a thread of a gradient holds eight pieces of a row and their sums, so that two
+// wavefronts (one behind the block) fit a SIMD and its loads are exposed: 16384 x 16384 forward 400 (5.4) and 373 (5.7),
+// backward 617 (3.5) and 792 (3.4).
 #include <algorithm>
 
 #include "block_common.hpp"

@@ -245,8 +245,9 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t, doubl
 }
 
 // SIGMOID: the scores; BIAS: there is one, so that scores and not logits are compared. 131072 x 256, k = 8, sigmoid
-// with bias and groups: 90 us (134 MB of logits, 1.5 TB/s); 16 x 256: 9.3. Bound by its instructions and their
-// latency (about 700 for the four tokens of a wavefront, four wavefronts a SIMD), so the steps are written to be few: values that
+// with bias and groups: 91 us (134 MB of logits, 1.5 TB/s); 16 x 256: 9.3. Bound by its instructions and their
+// latency (about 880 vector instructions for the four tokens of a wavefront, those in doubt included; four wavefronts
+// a SIMD by registers and LDS), so the steps are written to be few: values that
 // take no part are -inf, not NaN; maxima are integers where lanes exchange them; the candidates are found from
 // a bit mask a lane; their order is one 64-bit comparison.
 template <int L, int PER, bool SIGMOID, bool BIAS>
@@ -646,7 +647,8 @@ struct RouteBwdArgs {
 //   softmax, plain   dL/dl_e = scale p_e (g_e - sum_j p_j ds_j), g_e = ds_j for a chosen one, else 0
 // and 0 for every other expert. L lanes a token, one slot each; the slots' values go through an LDS row. DENSE:
 // the softmax that is not renormalised, the one form that reads all logits. Bound by the latency of a slot's
-// loads (expert, then its logit) and the write of dlogits: 131072 x 256, sigmoid, renormalised 35.5 us (3.8 TB/s).
+// loads (expert, then its logit) and the write of dlogits: 131072 x 256, sigmoid, renormalised 31 to
+// 36 us (3.8 to 4.3 TB/s); DENSE 46, reading as much again.
 template <int L, int PER, bool DENSE>
 __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs p) {
     __shared__ __align__(16) float s_row[256 / L][L * PER];
